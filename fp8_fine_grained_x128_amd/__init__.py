@@ -16,6 +16,10 @@ from .binding import (  # noqa: F401
     fp8q_transpose_weight, fp8q_gather_quantize_act, gather_quantize_act, fp8q_gemm_splitk, fp8q_clock_probe,
     fp8q_gemm_splitk_noalloc, SPLITK_SCRATCH_BYTES,
     fp8q_gemm_splitk_workspace,
+    FP8Q_NORM_LAYER, FP8Q_NORM_RMS, LayernormOut, MOE_MAX_TOKENS, MOE_MAX_TOP_K, NORM_MAX_COLS, SwigluCheckpoint,
+    SwigluGrads, fp8q_layernorm, fp8q_layernorm_backward, fp8q_layernorm_backward_workspace, fp8q_moe_decode,
+    fp8q_moe_decode_workspace, fp8q_swiglu_backward, fp8q_swiglu_backward_quantize, fp8q_swiglu_quantize, layernorm,
+    layernorm_backward, moe_decode, swiglu_backward, swiglu_backward_quantize, swiglu_quantize,
 )
 
-__version__ = "0.2.0"
+__version__ = "0.3.0"

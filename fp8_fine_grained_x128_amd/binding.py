@@ -16,7 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -40,12 +40,16 @@ FP8Q_GEMM_MMA_FP8 = 1
 FP8Q_GEMM_POW2_SCALES = 2
 FP8Q_SCALE_FP32 = 0
 FP8Q_SCALE_POW2 = 1
+FP8Q_NORM_LAYER = 0
+FP8Q_NORM_RMS = 1
 
 EXPORTS = ("fp8q_quantize_act", "fp8q_quantize_weight", "fp8q_requant_transpose", "fp8q_gemm",
            "fp8q_grouped_gemm", "fp8q_gemm_ex", "fp8q_grouped_gemm_ex", "fp8q_quantize_act_ex",
            "fp8q_quantize_weight_ex", "fp8q_requant_transpose_ex", "fp8q_transpose_weight",
            "fp8q_gather_quantize_act", "fp8q_gemm_splitk", "fp8q_gemm_splitk_noalloc", "fp8q_clock_probe",
-           "fp8q_gemm_splitk_workspace", "fp8q_strerror", "fp8q_version")
+           "fp8q_layernorm", "fp8q_layernorm_backward", "fp8q_swiglu_quantize", "fp8q_swiglu_backward",
+           "fp8q_swiglu_backward_quantize", "fp8q_moe_decode", "fp8q_layernorm_backward_workspace",
+           "fp8q_moe_decode_workspace", "fp8q_gemm_splitk_workspace", "fp8q_strerror", "fp8q_version")
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is not built; run __graft_entry__.build() (hipcc, gfx950)")
@@ -73,11 +77,25 @@ _lib.fp8q_gemm_splitk_noalloc.argtypes = _lib.fp8q_gemm.argtypes[:-1] + [_u32, _
 _lib.fp8q_clock_probe.argtypes = [_p, _i64, _p]
 _lib.fp8q_gemm_splitk_workspace.argtypes = [_i64, _i64, _i64]
 _lib.fp8q_gemm_splitk_workspace.restype = _i64
+_f32 = ctypes.c_float
+_lib.fp8q_layernorm.argtypes = [_p, _i32, _i64, _i64, _i64, _p, _p, _i32, _f32, _i32, _p, _i32, _i64, _p, _i64, _p,
+                                _i64, _i32, _p, _p, _p]
+_lib.fp8q_layernorm_backward.argtypes = [_p, _i64, _p, _i64, _i32, _i64, _i64, _p, _i32, _p, _p, _i32, _p, _i64, _p,
+                                         _i64, _p, _p, _i32, _p, _i64, _p]
+_lib.fp8q_layernorm_backward_workspace.argtypes = [_i64, _i64]
+_lib.fp8q_swiglu_quantize.argtypes = [_p, _p, _i32, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _p, _i64, _p, _p, _i64,
+                                      _i32, _p]
+_lib.fp8q_swiglu_backward.argtypes = [_p, _p, _i64, _p, _p, _i64, _p, _i32, _i64, _i64, _i64, _p, _p, _i64, _p]
+_lib.fp8q_swiglu_backward_quantize.argtypes = [_p, _p, _i64, _p, _p, _i64, _p, _i32, _i64, _i64, _i64, _p, _p, _i64,
+                                               _p, _p, _i64, _p, _p, _i64, _p, _p, _i64, _p, _i64, _p, _i64, _i32, _p]
+_lib.fp8q_moe_decode_workspace.argtypes = [_i64, _i64, _i64, _i32, _i32]
+_lib.fp8q_moe_decode.argtypes = [_p, _i64, _i64, _i64, _p, _i64, _i32, _i32, _i32, _i64, _p, _i64, _i64, _p, _i64,
+                                 _i64, _p, _i64, _i64, _p, _i64, _i64, _p, _i32, _i64, _p, _i64, _p]
 _lib.fp8q_strerror.argtypes = [_i32]
 _lib.fp8q_strerror.restype = ctypes.c_char_p
 _lib.fp8q_version.argtypes = []
 for _n in EXPORTS[:-3]:
-    getattr(_lib, _n).restype = _i32
+    getattr(_lib, _n).restype = _i64 if _n.endswith("_workspace") else _i32
 
 
 def library() -> ctypes.CDLL:
@@ -171,6 +189,58 @@ def fp8q_clock_probe(out, ticks, stream=None) -> int:
 
 def fp8q_gemm_splitk_workspace(M, N, K) -> int:
     return _lib.fp8q_gemm_splitk_workspace(M, N, K)
+
+
+def fp8q_layernorm(x, x_dtype, rows, cols, ldx, gamma, beta, w_dtype, eps, kind, y, y_dtype, ldy, q, ldq, s, lds,
+                   scale_mode, mean, rstd, stream=None) -> int:
+    return _lib.fp8q_layernorm(x, x_dtype, rows, cols, ldx, gamma, beta, w_dtype, eps, kind, y, y_dtype, ldy, q, ldq,
+                               s, lds, scale_mode, mean, rstd, stream)
+
+
+def fp8q_layernorm_backward_workspace(rows, cols) -> int:
+    return _lib.fp8q_layernorm_backward_workspace(rows, cols)
+
+
+def fp8q_layernorm_backward(dy, lddy, x, ldx, dtype, rows, cols, gamma, w_dtype, mean, rstd, kind, skip, ldskip, dx,
+                            lddx, dgamma, dbeta, accumulate, workspace, workspace_bytes, stream=None) -> int:
+    return _lib.fp8q_layernorm_backward(dy, lddy, x, ldx, dtype, rows, cols, gamma, w_dtype, mean, rstd, kind, skip,
+                                        ldskip, dx, lddx, dgamma, dbeta, accumulate, workspace, workspace_bytes,
+                                        stream)
+
+
+def fp8q_swiglu_quantize(g, u, dtype, ldgu, rows, cols, qh, ldqh, sh, ldsh, qg, qu, ldq, sg, su, lds, scale_mode,
+                         stream=None) -> int:
+    return _lib.fp8q_swiglu_quantize(g, u, dtype, ldgu, rows, cols, qh, ldqh, sh, ldsh, qg, qu, ldq, sg, su, lds,
+                                     scale_mode, stream)
+
+
+def fp8q_swiglu_backward(qg, qu, ldq, sg, su, lds, dh, dtype, lddh, rows, cols, dg, du, ldd, stream=None) -> int:
+    return _lib.fp8q_swiglu_backward(qg, qu, ldq, sg, su, lds, dh, dtype, lddh, rows, cols, dg, du, ldd, stream)
+
+
+def fp8q_swiglu_backward_quantize(qg, qu, ldq, sg, su, lds, dh, dtype, lddh, rows, cols, qdg, qdu, ldqd, sdg, sdu,
+                                  ldsd, qdgt, qdut, ldqt, sdgt, sdut, ldst, qht, ldqht, sht, ldsht, scale_mode,
+                                  stream=None) -> int:
+    return _lib.fp8q_swiglu_backward_quantize(qg, qu, ldq, sg, su, lds, dh, dtype, lddh, rows, cols, qdg, qdu, ldqd,
+                                              sdg, sdu, ldsd, qdgt, qdut, ldqt, sdgt, sdut, ldst, qht, ldqht, sht,
+                                              ldsht, scale_mode, stream)
+
+
+def fp8q_moe_decode_workspace(tokens, hidden, inner, experts, top_k) -> int:
+    return _lib.fp8q_moe_decode_workspace(tokens, hidden, inner, experts, top_k)
+
+
+def fp8q_moe_decode(x, ldx, tokens, hidden, logits, ldl, experts, top_k, renormalize, inner, w_gu, ldw_gu,
+                    w_gu_stride, s_gu, lds_gu, s_gu_stride, w_down, ldw_down, w_down_stride, s_down, lds_down,
+                    s_down_stride, y, y_dtype, ldy, workspace, workspace_bytes, stream=None) -> int:
+    return _lib.fp8q_moe_decode(x, ldx, tokens, hidden, logits, ldl, experts, top_k, renormalize, inner, w_gu, ldw_gu,
+                                w_gu_stride, s_gu, lds_gu, s_gu_stride, w_down, ldw_down, w_down_stride, s_down,
+                                lds_down, s_down_stride, y, y_dtype, ldy, workspace, workspace_bytes, stream)
+
+
+NORM_MAX_COLS = 16384
+MOE_MAX_TOKENS = 64
+MOE_MAX_TOP_K = 32
 
 
 def fp8q_strerror(status: int) -> str:
@@ -421,3 +491,281 @@ def grouped_gemm(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.T
     else:
         _check(fp8q_grouped_gemm(*args, _stream()), "fp8q_grouped_gemm")
     return c
+
+
+# ------------------------------------------------------------------ feed-forward block
+
+def _rows(rows: int, cols: int, dtype: torch.dtype, device) -> torch.Tensor:
+    """[rows][cols] whose row stride is a multiple of 16 bytes."""
+    per16 = 16 // dtype.itemsize
+    return torch.empty((rows, _cdiv(max(cols, 1), per16) * per16), dtype=dtype, device=device)[:, :cols]
+
+
+def _scales(groups: int, n: int, device) -> torch.Tensor:
+    return torch.empty((groups, n), dtype=torch.float32, device=device)
+
+
+def _workspace(need: int, device) -> Tuple[Optional[torch.Tensor], int]:
+    """A buffer that holds `need` bytes at a 256-byte aligned address, and that address."""
+    if need == 0:
+        return None, 0
+    ws = torch.empty(need + 256, dtype=torch.uint8, device=device)
+    return ws, (ws.data_ptr() + 255) // 256 * 256
+
+
+def _like(what: str, name: str, t: torch.Tensor, ref: torch.Tensor) -> None:
+    if t.shape != ref.shape or t.dtype != ref.dtype:
+        raise ValueError(f"{what}: {name} is {tuple(t.shape)} {t.dtype}, expected {tuple(ref.shape)} {ref.dtype}")
+
+
+def _check_vector(what: str, name: str, t: torch.Tensor, n: int, dtype: Optional[torch.dtype] = None) -> None:
+    if t.dim() != 1 or t.numel() != n or (n > 1 and t.stride(0) != 1) or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{what}: {name} must be a contiguous vector of {n}"
+                         f"{'' if dtype is None else f' {dtype}'}, got {tuple(t.shape)} {t.dtype}")
+
+
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+class LayernormOut(NamedTuple):
+    """What layernorm() gives: 1x128 codes and scales, the values, and the rows' statistics; None where not asked
+    for (mean: layer norm only)."""
+    q: Optional[torch.Tensor]
+    s: Optional[torch.Tensor]
+    y: Optional[torch.Tensor]
+    mean: Optional[torch.Tensor]
+    rstd: torch.Tensor
+
+
+def layernorm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Optional[torch.Tensor] = None,
+              eps: float = 1e-5, kind: int = FP8Q_NORM_LAYER, quantize: bool = True,
+              out_dtype: Optional[torch.dtype] = None, scale_mode: int = FP8Q_SCALE_FP32) -> LayernormOut:
+    """Layer norm (FP8Q_NORM_RMS: RMS norm) of the rows of x, into the next GEMM's FP8 operand (`quantize`) and/or
+    values of `out_dtype`; see fp8q_layernorm."""
+    rows, cols = x.shape
+    if not quantize and out_dtype is None:
+        raise ValueError("layernorm: nothing to compute (quantize=False and no out_dtype)")
+    given = [w for w in (gamma, beta) if w is not None]
+    for name, w in (("gamma", gamma), ("beta", beta)):
+        if w is not None:
+            _check_vector("layernorm", name, w, cols, given[0].dtype)
+    _on_device("layernorm", x, *given)
+    dev = x.device
+    q = _codes(rows, cols, dev) if quantize else None
+    s = _scales(_cdiv(cols, 128), rows, dev) if quantize else None
+    y = _rows(rows, cols, out_dtype, dev) if out_dtype is not None else None
+    mean = torch.empty(rows, dtype=torch.float32, device=dev) if kind == FP8Q_NORM_LAYER else None
+    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    _check(fp8q_layernorm(x.data_ptr(), _dtype_code(x), rows, cols, _ld(x), _ptr(gamma), _ptr(beta),
+                          _dtype_code(given[0]) if given else FP8Q_F32, eps, kind, _ptr(y),
+                          FP8Q_F32 if y is None else _dtype_code(y), 0 if y is None else _ld(y), _ptr(q),
+                          0 if q is None else _ld(q), _ptr(s), 0 if s is None else max(s.stride(0), 1), scale_mode,
+                          _ptr(mean), rstd.data_ptr(), _stream()), "fp8q_layernorm")
+    return LayernormOut(q, s, y, mean, rstd)
+
+
+def layernorm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: Optional[torch.Tensor],
+                       mean: Optional[torch.Tensor], rstd: torch.Tensor, skip: Optional[torch.Tensor] = None,
+                       kind: int = FP8Q_NORM_LAYER, dgamma: Optional[torch.Tensor] = None,
+                       dbeta: Optional[torch.Tensor] = None, accumulate: bool = False
+                       ) -> Tuple[torch.Tensor, torch.Tensor, Optional[torch.Tensor]]:
+    """(dx, dgamma, dbeta) of layernorm(); dbeta only for a layer norm or where given.  `skip` is added to dx;
+    with `accumulate` the sums are added to the given fp32 dgamma / dbeta.  See fp8q_layernorm_backward."""
+    rows, cols = x.shape
+    _like("layernorm_backward", "dy", dy, x)
+    if skip is not None:
+        _like("layernorm_backward", "skip", skip, x)
+    if accumulate and dgamma is None:
+        raise ValueError("layernorm_backward: accumulate needs the gradients to add to")
+    if gamma is not None:
+        _check_vector("layernorm_backward", "gamma", gamma, cols)
+    if kind == FP8Q_NORM_LAYER:
+        if mean is None or (accumulate and dbeta is None):
+            raise ValueError("layernorm_backward: a layer norm needs mean (and dbeta to accumulate into)")
+        _check_vector("layernorm_backward", "mean", mean, rows, torch.float32)
+    _check_vector("layernorm_backward", "rstd", rstd, rows, torch.float32)
+    dev = x.device
+    if dgamma is None:
+        dgamma = torch.empty(cols, dtype=torch.float32, device=dev)
+    if dbeta is None and kind == FP8Q_NORM_LAYER:
+        dbeta = torch.empty(cols, dtype=torch.float32, device=dev)
+    for name, w in (("dgamma", dgamma), ("dbeta", dbeta)):
+        if w is not None:
+            _check_vector("layernorm_backward", name, w, cols, torch.float32)
+    _on_device("layernorm_backward", dy, x, rstd,
+               *(t for t in (gamma, mean, skip, dgamma, dbeta) if t is not None))
+    dx = _rows(rows, cols, x.dtype, dev)
+    need = fp8q_layernorm_backward_workspace(rows, cols)
+    ws, base = _workspace(need, dev)
+    _check(fp8q_layernorm_backward(dy.data_ptr(), _ld(dy), x.data_ptr(), _ld(x), _dtype_code(x), rows, cols,
+                                   _ptr(gamma), FP8Q_F32 if gamma is None else _dtype_code(gamma),
+                                   _ptr(mean) if kind == FP8Q_NORM_LAYER else None, rstd.data_ptr(), kind,
+                                   _ptr(skip), 0 if skip is None else _ld(skip), dx.data_ptr(), _ld(dx),
+                                   dgamma.data_ptr(), _ptr(dbeta), 1 if accumulate else 0, base, need, _stream()),
+           "fp8q_layernorm_backward")
+    return dx, dgamma, dbeta
+
+
+class SwigluCheckpoint(NamedTuple):
+    """The SwiGLU's inputs in 8 bits: 1x128 codes [rows][cols] of gate and up, scales [ceil(cols/128)][rows]."""
+    qg: torch.Tensor
+    qu: torch.Tensor
+    sg: torch.Tensor
+    su: torch.Tensor
+
+
+def _pair(rows: int, cols: int, multiple: int, dtype: torch.dtype, device) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Two [rows][cols] halves with one row stride: side by side in one buffer if cols % multiple == 0, else in
+    buffers of their own."""
+    if cols % multiple == 0:
+        both = torch.empty((rows, 2 * cols), dtype=dtype, device=device)
+        return both[:, :cols], both[:, cols:]
+    return _rows(rows, cols, dtype, device), _rows(rows, cols, dtype, device)
+
+
+def _stack(groups: int, n: int, dtype: torch.dtype, device) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Two [groups][n] halves, one below the other, row stride a multiple of 16 bytes for codes."""
+    ld = n if dtype == torch.float32 else _pad16(max(n, 1))
+    both = torch.empty((2 * groups, ld), dtype=dtype, device=device)
+    return both[:groups, :n], both[groups:, :n]
+
+
+def swiglu_quantize(g: torch.Tensor, u: torch.Tensor, checkpoint: bool = True, scale_mode: int = FP8Q_SCALE_FP32
+                    ) -> Tuple[torch.Tensor, torch.Tensor, Optional[SwigluCheckpoint]]:
+    """SwiGLU of gate g and up u [rows][cols] into the down projection's operand: (codes, scales, checkpoint of g
+    and u or None).  g and u are the halves of a fused product, or two tensors with the same row stride."""
+    _like("swiglu_quantize", "u", u, g)
+    rows, cols = g.shape
+    if _ld(g) != _ld(u):
+        raise ValueError(f"swiglu_quantize: row strides {_ld(g)} and {_ld(u)} differ")
+    _on_device("swiglu_quantize", g, u)
+    dev, groups = g.device, _cdiv(cols, 128)
+    qh, sh = _codes(rows, cols, dev), _scales(groups, rows, dev)
+    kept = None
+    if checkpoint:
+        kept = SwigluCheckpoint(*_pair(rows, cols, 16, torch.uint8, dev), *_stack(groups, rows, torch.float32, dev))
+    _check(fp8q_swiglu_quantize(g.data_ptr(), u.data_ptr(), _dtype_code(g), _ld(g), rows, cols, qh.data_ptr(), _ld(qh),
+                                sh.data_ptr(), max(rows, 1), *((None, None, 0, None, None, 0) if kept is None else
+                                                               (kept.qg.data_ptr(), kept.qu.data_ptr(), _ld(kept.qg),
+                                                                kept.sg.data_ptr(), kept.su.data_ptr(), max(rows, 1))),
+                                scale_mode, _stream()), "fp8q_swiglu_quantize")
+    return qh, sh, kept
+
+
+def _check_checkpoint(what: str, kept: SwigluCheckpoint, dh: torch.Tensor) -> None:
+    rows, cols = dh.shape
+    for t in (kept.qg, kept.qu):
+        _check_codes(f"{what} checkpoint", t)
+        if tuple(t.shape) != (rows, cols):
+            raise ValueError(f"{what}: checkpoint {tuple(t.shape)}, gradient {tuple(dh.shape)}")
+    for t in (kept.sg, kept.su):
+        _check_scales(f"{what} checkpoint scales (layout [ceil(cols/128)][rows])", t, _cdiv(cols, 128), rows)
+    if _ld(kept.qg) != _ld(kept.qu) or (kept.sg.shape[0] > 1 and kept.sg.stride(0) != kept.su.stride(0)):
+        raise ValueError(f"{what}: the strides of the checkpoint's halves differ")
+    _on_device(what, *kept, dh)
+
+
+def _checkpoint_args(kept: SwigluCheckpoint, dh: torch.Tensor) -> tuple:
+    rows, cols = dh.shape
+    return (kept.qg.data_ptr(), kept.qu.data_ptr(), _ld(kept.qg), kept.sg.data_ptr(), kept.su.data_ptr(),
+            max(kept.sg.stride(0), rows), dh.data_ptr(), _dtype_code(dh), _ld(dh), rows, cols)
+
+
+def swiglu_backward(kept: SwigluCheckpoint, dh: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(dg, du) of the SwiGLU at the checkpoint's values, in dh's dtype; halves of one buffer [rows][2*cols] where
+    cols allows it."""
+    _check_checkpoint("swiglu_backward", kept, dh)
+    rows, cols = dh.shape
+    dg, du = _pair(rows, cols, 16 // dh.element_size(), dh.dtype, dh.device)
+    _check(fp8q_swiglu_backward(*_checkpoint_args(kept, dh), dg.data_ptr(), du.data_ptr(), _ld(dg), _stream()),
+           "fp8q_swiglu_backward")
+    return dg, du
+
+
+class SwigluGrads(NamedTuple):
+    """FP8 operands of the backward GEMMs: gradients of gate and up in 1x128 tiles (q, s: Dgrad) and transposed in
+    128x1 tiles (qt, st: Wgrad), and the recomputed h transposed in 128x1 tiles (the down projection's Wgrad)."""
+    qdg: torch.Tensor
+    qdu: torch.Tensor
+    sdg: torch.Tensor
+    sdu: torch.Tensor
+    qdgt: torch.Tensor
+    qdut: torch.Tensor
+    sdgt: torch.Tensor
+    sdut: torch.Tensor
+    qht: torch.Tensor
+    sht: torch.Tensor
+
+    def gate_up(self) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+        """The operands of a fused gate|up projection: codes [rows][2*cols] with scales [2*cols/128][rows], and codes
+        [2*cols][rows] with scales [ceil(rows/128)][2*cols]; views, for cols a multiple of 128."""
+        rows, cols = self.qdg.shape
+        if cols % 128 != 0:
+            raise ValueError(f"gate_up: {cols} columns are not a multiple of 128")
+        groups = self.sdgt.shape[0]
+        return (self.qdg.as_strided((rows, 2 * cols), (2 * cols, 1)),
+                self.sdg.as_strided((2 * cols // 128, rows), (rows, 1)),
+                self.qdgt.as_strided((2 * cols, rows), (self.qdgt.stride(0), 1)),
+                self.sdgt.as_strided((groups, 2 * cols), (2 * cols, 1)))
+
+
+def swiglu_backward_quantize(kept: SwigluCheckpoint, dh: torch.Tensor, scale_mode: int = FP8Q_SCALE_FP32
+                             ) -> SwigluGrads:
+    """Every FP8 operand of the block's backward GEMMs from the checkpoint and dh; see
+    fp8q_swiglu_backward_quantize."""
+    _check_checkpoint("swiglu_backward_quantize", kept, dh)
+    rows, cols = dh.shape
+    dev, groups, tgroups = dh.device, _cdiv(cols, 128), _cdiv(rows, 128)
+    o = SwigluGrads(*_pair(rows, cols, 16, torch.uint8, dev), *_stack(groups, rows, torch.float32, dev),
+                    *_stack(cols, rows, torch.uint8, dev), *_pair(tgroups, cols, 1, torch.float32, dev),
+                    _codes(cols, rows, dev), _scales(tgroups, cols, dev))
+    ldq = cols * 2 if cols % 16 == 0 else _ld(o.qdg)
+    ldt = _pad16(max(rows, 1))
+    _check(fp8q_swiglu_backward_quantize(*_checkpoint_args(kept, dh), o.qdg.data_ptr(), o.qdu.data_ptr(), ldq,
+                                         o.sdg.data_ptr(), o.sdu.data_ptr(), max(rows, 1), o.qdgt.data_ptr(),
+                                         o.qdut.data_ptr(), ldt, o.sdgt.data_ptr(), o.sdut.data_ptr(), 2 * cols,
+                                         o.qht.data_ptr(), ldt, o.sht.data_ptr(), max(cols, 1), scale_mode, _stream()),
+           "fp8q_swiglu_backward_quantize")
+    return o
+
+
+def _check_experts(what: str, w: torch.Tensor, s: torch.Tensor, shape: Tuple[int, int, int]) -> None:
+    _check_codes(what, w)
+    E, N, K = shape
+    if tuple(w.shape) != shape or (K > 1 and w.stride(2) != 1):
+        raise ValueError(f"{what}: codes {tuple(w.shape)}, expected [{E}][{N}][{K}] with unit inner stride")
+    if s.dtype != torch.float32 or tuple(s.shape) != (E, _cdiv(N, 128), _cdiv(K, 128)) or \
+            (s.shape[2] > 1 and s.stride(2) != 1):
+        raise ValueError(f"{what}: scales {tuple(s.shape)} {s.dtype}, expected float32 "
+                         f"[{E}][{_cdiv(N, 128)}][{_cdiv(K, 128)}] with unit inner stride")
+
+
+def moe_decode(x: torch.Tensor, logits: torch.Tensor, w_gu: torch.Tensor, s_gu: torch.Tensor, w_down: torch.Tensor,
+               s_down: torch.Tensor, top_k: int, renormalize: bool = True,
+               out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """A mixture-of-experts layer for up to MOE_MAX_TOKENS tokens: x [tokens][hidden] bf16, router logits
+    [tokens][experts] fp32, weights w_gu [experts][2*inner][hidden] (gate rows first) and w_down
+    [experts][hidden][inner] as FP8 codes with 128x128 block scales.  See fp8q_moe_decode."""
+    if x.dtype != torch.bfloat16 or logits.dtype != torch.float32:
+        raise ValueError(f"moe_decode: x must be bfloat16 and logits float32, got {x.dtype} and {logits.dtype}")
+    if logits.dim() != 2 or logits.shape[0] != x.shape[0] or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError(f"moe_decode: logits {tuple(logits.shape)} for {x.shape[0]} tokens")
+    tokens, hidden = x.shape
+    experts = logits.shape[1]
+    if w_down.dim() != 3:
+        raise ValueError(f"moe_decode: w_down {tuple(w_down.shape)} is not [experts][hidden][inner]")
+    inner = w_down.shape[2]
+    _check_experts("moe_decode w_gu", w_gu, s_gu, (experts, 2 * inner, hidden))
+    _check_experts("moe_decode w_down", w_down, s_down, (experts, hidden, inner))
+    _on_device("moe_decode", x, logits, w_gu, s_gu, w_down, s_down)
+    y = torch.empty((tokens, hidden), dtype=out_dtype, device=x.device)
+    need = fp8q_moe_decode_workspace(tokens, hidden, inner, experts, top_k)
+    ws, base = _workspace(need, x.device)
+    _check(fp8q_moe_decode(x.data_ptr(), _ld(x), tokens, hidden, logits.data_ptr(),
+                           max(logits.stride(0), experts) if tokens <= 1 else logits.stride(0), experts, top_k,
+                           1 if renormalize else 0, inner, w_gu.data_ptr(), w_gu.stride(1),
+                           w_gu.stride(0), s_gu.data_ptr(), s_gu.stride(1), s_gu.stride(0), w_down.data_ptr(),
+                           w_down.stride(1), w_down.stride(0), s_down.data_ptr(), s_down.stride(1), s_down.stride(0),
+                           y.data_ptr(), _dtype_code(y), _ld(y), base, need, _stream()), "fp8q_moe_decode")
+    return y

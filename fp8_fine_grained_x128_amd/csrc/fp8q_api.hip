@@ -116,6 +116,16 @@ int grouped_impl(const uint8_t* a, int64_t lda, const float* sa, int64_t ldsa, c
     return status_of(fp8q::launch_grouped_gemm(g, static_cast<hipStream_t>(stream)));
 }
 
+// The checkpoint and incoming gradient of a SwiGLU backward call.
+fp8q::SwigluBackwardArgs swiglu_inputs(const uint8_t* qg, const uint8_t* qu, int64_t ldq, const float* sg,
+                                       const float* su, int64_t lds, const void* dh, int dtype, int64_t lddh,
+                                       int64_t rows, int64_t cols) {
+    fp8q::SwigluBackwardArgs a{};
+    a.qg = qg; a.qu = qu; a.ldq = ldq; a.sg = sg; a.su = su; a.lds = lds;
+    a.dh = dh; a.dtype = dtype; a.lddh = lddh; a.rows = rows; a.cols = cols;
+    return a;
+}
+
 }  // namespace
 
 extern "C" {
@@ -132,7 +142,7 @@ const char* fp8q_strerror(int status) {
     }
 }
 
-int fp8q_version(void) { return 200; }
+int fp8q_version(void) { return 300; }
 
 int fp8q_quantize_act(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, int tile,
                       uint8_t* q, int64_t ldq, float* s, int64_t lds, void* stream) {
@@ -262,6 +272,116 @@ int fp8q_grouped_gemm_ex(const uint8_t* a, int64_t lda, const float* sa, int64_t
                          void* stream) {
     return grouped_impl(a, lda, sa, ldsa, b, ldb, b_group_stride, sb, ldsb, sb_group_stride, group_offsets, G,
                         M_total, N, K, c, c_dtype, ldc, flags, stream);
+}
+
+int fp8q_layernorm(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, const void* gamma,
+                   const void* beta, int w_dtype, float eps, int kind, void* y, int y_dtype, int64_t ldy, uint8_t* q,
+                   int64_t ldq, float* s, int64_t lds, int scale_mode, float* mean, float* rstd, void* stream) {
+    const int rc = fp8q::check::layernorm(x, x_dtype, rows, cols, ldx, gamma, beta, w_dtype, eps, kind, y, y_dtype,
+                                          ldy, q, ldq, s, lds, scale_mode, mean, rstd);
+    if (rc != kLaunch) return rc;
+    fp8q::LayernormArgs a{};
+    a.x = x; a.x_dtype = x_dtype; a.rows = rows; a.cols = cols; a.ldx = ldx;
+    a.gamma = gamma; a.beta = beta; a.w_dtype = w_dtype; a.eps = eps;
+    a.layer = kind == FP8Q_NORM_LAYER;
+    a.y = y; a.y_dtype = y_dtype; a.ldy = ldy;
+    a.q = q; a.ldq = ldq; a.s = s; a.lds = lds; a.pow2 = scale_mode == FP8Q_SCALE_POW2;
+    a.mean = mean; a.rstd = rstd;
+    return status_of(fp8q::launch_layernorm(a, static_cast<hipStream_t>(stream)));
+}
+
+int64_t fp8q_layernorm_backward_workspace(int64_t rows, int64_t cols) {
+    if (rows <= 0 || cols <= 0 || cols > FP8Q_NORM_MAX_COLS) return 0;
+    return fp8q::layernorm_backward_bytes(rows, cols);
+}
+
+int fp8q_layernorm_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, int dtype, int64_t rows,
+                            int64_t cols, const void* gamma, int w_dtype, const float* mean, const float* rstd,
+                            int kind, const void* skip, int64_t ldskip, void* dx, int64_t lddx, float* dgamma,
+                            float* dbeta, int accumulate, void* workspace, int64_t workspace_bytes, void* stream) {
+    const int64_t need = fp8q_layernorm_backward_workspace(rows, cols);
+    const int rc = fp8q::check::layernorm_backward(dy, lddy, x, ldx, dtype, rows, cols, gamma, w_dtype, mean, rstd,
+                                                   kind, skip, ldskip, dx, lddx, dgamma, dbeta, accumulate, need,
+                                                   workspace, workspace_bytes);
+    if (rc != kLaunch) return rc;
+    fp8q::LayernormBackwardArgs a{};
+    a.dy = dy; a.lddy = lddy; a.x = x; a.ldx = ldx; a.dtype = dtype; a.rows = rows; a.cols = cols;
+    a.gamma = gamma; a.w_dtype = w_dtype; a.mean = mean; a.rstd = rstd;
+    a.layer = kind == FP8Q_NORM_LAYER;
+    a.skip = skip; a.ldskip = ldskip; a.dx = dx; a.lddx = lddx;
+    a.dgamma = dgamma; a.dbeta = dbeta; a.accumulate = accumulate ? 1 : 0;
+    return status_of(fp8q::launch_layernorm_backward(a, workspace, static_cast<hipStream_t>(stream)));
+}
+
+int fp8q_swiglu_quantize(const void* g, const void* u, int dtype, int64_t ldgu, int64_t rows, int64_t cols,
+                         uint8_t* qh, int64_t ldqh, float* sh, int64_t ldsh, uint8_t* qg, uint8_t* qu, int64_t ldq,
+                         float* sg, float* su, int64_t lds, int scale_mode, void* stream) {
+    const int rc = fp8q::check::swiglu_quantize(g, u, dtype, ldgu, rows, cols, qh, ldqh, sh, ldsh, qg, qu, ldq, sg,
+                                                su, lds, scale_mode);
+    if (rc != kLaunch) return rc;
+    fp8q::SwigluArgs a{};
+    a.g = g; a.u = u; a.dtype = dtype; a.ldgu = ldgu; a.rows = rows; a.cols = cols;
+    a.qh = qh; a.ldqh = ldqh; a.sh = sh; a.ldsh = ldsh;
+    a.qg = qg; a.qu = qu; a.ldq = ldq; a.sg = sg; a.su = su; a.lds = lds;
+    a.pow2 = scale_mode == FP8Q_SCALE_POW2;
+    return status_of(fp8q::launch_swiglu_quantize(a, static_cast<hipStream_t>(stream)));
+}
+
+int fp8q_swiglu_backward(const uint8_t* qg, const uint8_t* qu, int64_t ldq, const float* sg, const float* su,
+                         int64_t lds, const void* dh, int dtype, int64_t lddh, int64_t rows, int64_t cols, void* dg,
+                         void* du, int64_t ldd, void* stream) {
+    const int rc = fp8q::check::swiglu_backward(qg, qu, ldq, sg, su, lds, dh, dtype, lddh, rows, cols, dg, du, ldd);
+    if (rc != kLaunch) return rc;
+    fp8q::SwigluBackwardArgs a = swiglu_inputs(qg, qu, ldq, sg, su, lds, dh, dtype, lddh, rows, cols);
+    a.dg = dg; a.du = du; a.ldd = ldd;
+    return status_of(fp8q::launch_swiglu_backward(a, static_cast<hipStream_t>(stream)));
+}
+
+int fp8q_swiglu_backward_quantize(const uint8_t* qg, const uint8_t* qu, int64_t ldq, const float* sg,
+                                  const float* su, int64_t lds, const void* dh, int dtype, int64_t lddh, int64_t rows,
+                                  int64_t cols, uint8_t* qdg, uint8_t* qdu, int64_t ldqd, float* sdg, float* sdu,
+                                  int64_t ldsd, uint8_t* qdgt, uint8_t* qdut, int64_t ldqt, float* sdgt, float* sdut,
+                                  int64_t ldst, uint8_t* qht, int64_t ldqht, float* sht, int64_t ldsht,
+                                  int scale_mode, void* stream) {
+    const int rc = fp8q::check::swiglu_backward_quantize(qg, qu, ldq, sg, su, lds, dh, dtype, lddh, rows, cols, qdg,
+                                                         qdu, ldqd, sdg, sdu, ldsd, qdgt, qdut, ldqt, sdgt, sdut,
+                                                         ldst, qht, ldqht, sht, ldsht, scale_mode);
+    if (rc != kLaunch) return rc;
+    fp8q::SwigluBackwardArgs a = swiglu_inputs(qg, qu, ldq, sg, su, lds, dh, dtype, lddh, rows, cols);
+    a.qdg = qdg; a.qdu = qdu; a.ldqd = ldqd; a.sdg = sdg; a.sdu = sdu; a.ldsd = ldsd;
+    a.qdgt = qdgt; a.qdut = qdut; a.ldqt = ldqt; a.sdgt = sdgt; a.sdut = sdut; a.ldst = ldst;
+    a.qht = qht; a.ldqht = ldqht; a.sht = sht; a.ldsht = ldsht;
+    a.pow2 = scale_mode == FP8Q_SCALE_POW2;
+    return status_of(fp8q::launch_swiglu_backward_quantize(a, static_cast<hipStream_t>(stream)));
+}
+
+int64_t fp8q_moe_decode_workspace(int64_t tokens, int64_t hidden, int64_t inner, int experts, int top_k) {
+    if (tokens == 0 || fp8q::check::moe_sizes(tokens, hidden, inner, experts, top_k) != kLaunch) return 0;
+    return fp8q::moe_decode_bytes(tokens, hidden, inner, experts, top_k);
+}
+
+int fp8q_moe_decode(const void* x, int64_t ldx, int64_t tokens, int64_t hidden, const float* logits, int64_t ldl,
+                    int experts, int top_k, int renormalize, int64_t inner, const uint8_t* w_gu, int64_t ldw_gu,
+                    int64_t w_gu_stride, const float* s_gu, int64_t lds_gu, int64_t s_gu_stride,
+                    const uint8_t* w_down, int64_t ldw_down, int64_t w_down_stride, const float* s_down,
+                    int64_t lds_down, int64_t s_down_stride, void* y, int y_dtype, int64_t ldy, void* workspace,
+                    int64_t workspace_bytes, void* stream) {
+    const int64_t need = fp8q_moe_decode_workspace(tokens, hidden, inner, experts, top_k);
+    const int rc = fp8q::check::moe_decode(x, ldx, tokens, hidden, logits, ldl, experts, top_k, inner, w_gu, ldw_gu,
+                                           w_gu_stride, s_gu, lds_gu, s_gu_stride, w_down, ldw_down, w_down_stride,
+                                           s_down, lds_down, s_down_stride, y, y_dtype, ldy, need, workspace,
+                                           workspace_bytes);
+    if (rc != kLaunch) return rc;
+    fp8q::MoeArgs a{};
+    a.x = static_cast<const uint16_t*>(x); a.ldx = ldx;
+    a.tokens = (int)tokens; a.hidden = hidden; a.inner = inner;
+    a.logits = logits; a.ldl = ldl; a.experts = experts; a.top_k = top_k; a.renormalize = renormalize ? 1 : 0;
+    a.w_gu = w_gu; a.ldw_gu = ldw_gu; a.w_gu_stride = w_gu_stride;
+    a.s_gu = s_gu; a.lds_gu = lds_gu; a.s_gu_stride = s_gu_stride;
+    a.w_down = w_down; a.ldw_down = ldw_down; a.w_down_stride = w_down_stride;
+    a.s_down = s_down; a.lds_down = lds_down; a.s_down_stride = s_down_stride;
+    a.y = y; a.y_dtype = y_dtype; a.ldy = ldy; a.workspace = workspace;
+    return status_of(fp8q::launch_moe_decode(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -78,4 +78,132 @@ struct SplitPlan {
 SplitPlan plan_splitk(int64_t M, int64_t N, int64_t K);
 hipError_t launch_grouped_gemm(const GemmArgs& g, hipStream_t st);
 
+// ---- feed-forward operators around the GEMMs
+struct LayernormArgs {
+    const void* x;
+    int x_dtype;
+    int64_t rows, cols, ldx;
+    const void* gamma;  // nullptr: ones
+    const void* beta;   // nullptr: zeros
+    int w_dtype;
+    float eps;
+    int layer;  // 1 layer norm, 0 RMS norm
+    void* y;    // nullptr: not written
+    int y_dtype;
+    int64_t ldy;
+    uint8_t* q;  // nullptr: no codes
+    int64_t ldq;
+    float* s;
+    int64_t lds;
+    int pow2;
+    float* mean;  // nullptr: not written (both)
+    float* rstd;
+    float shrink;  // set by the launcher
+};
+hipError_t launch_layernorm(LayernormArgs a, hipStream_t st);
+
+struct LayernormBackwardArgs {
+    const void* dy;
+    int64_t lddy;
+    const void* x;
+    int64_t ldx;
+    int dtype;  // of dy, x, skip and dx
+    int64_t rows, cols;
+    const void* gamma;
+    int w_dtype;
+    const float* mean;
+    const float* rstd;
+    int layer;
+    const void* skip;  // nullptr: nothing added to dx
+    int64_t ldskip;
+    void* dx;
+    int64_t lddx;
+    float* dgamma;  // nullptr: not computed (both)
+    float* dbeta;
+    int accumulate;
+    float* parts;  // set by the launcher from the workspace
+    int64_t ldparts;
+};
+int64_t layernorm_backward_bytes(int64_t rows, int64_t cols);
+hipError_t launch_layernorm_backward(LayernormBackwardArgs a, void* workspace, hipStream_t st);
+
+struct SwigluArgs {
+    const void* g;
+    const void* u;
+    int dtype;
+    int64_t ldgu;
+    int64_t rows, cols;
+    uint8_t* qh;
+    int64_t ldqh;
+    float* sh;
+    int64_t ldsh;
+    uint8_t* qg;  // nullptr: no checkpoint
+    uint8_t* qu;
+    int64_t ldq;
+    float* sg;
+    float* su;
+    int64_t lds;
+    int pow2;
+};
+hipError_t launch_swiglu_quantize(const SwigluArgs& a, hipStream_t st);
+
+struct SwigluBackwardArgs {
+    const uint8_t* qg;  // checkpoint
+    const uint8_t* qu;
+    int64_t ldq;
+    const float* sg;
+    const float* su;
+    int64_t lds;
+    const void* dh;
+    int dtype;  // of dh, dg and du
+    int64_t lddh;
+    int64_t rows, cols;
+    void* dg;  // plain gradients
+    void* du;
+    int64_t ldd;
+    uint8_t* qdg;  // gradients in 1x128 tiles
+    uint8_t* qdu;
+    int64_t ldqd;
+    float* sdg;
+    float* sdu;
+    int64_t ldsd;
+    uint8_t* qdgt;  // gradients in 128x1 tiles, transposed
+    uint8_t* qdut;
+    int64_t ldqt;
+    float* sdgt;
+    float* sdut;
+    int64_t ldst;
+    uint8_t* qht;  // recomputed h in 128x1 tiles, transposed
+    int64_t ldqht;
+    float* sht;
+    int64_t ldsht;
+    int pow2;
+};
+hipError_t launch_swiglu_backward(const SwigluBackwardArgs& a, hipStream_t st);
+hipError_t launch_swiglu_backward_quantize(const SwigluBackwardArgs& a, hipStream_t st);
+
+struct MoeArgs {
+    const uint16_t* x;  // bf16
+    int64_t ldx;
+    int tokens;
+    int64_t hidden, inner;
+    const float* logits;
+    int64_t ldl;
+    int experts, top_k, renormalize;
+    const uint8_t* w_gu;  // [experts][2*inner][hidden], gate rows first
+    int64_t ldw_gu, w_gu_stride;
+    const float* s_gu;
+    int64_t lds_gu, s_gu_stride;
+    const uint8_t* w_down;  // [experts][hidden][inner]
+    int64_t ldw_down, w_down_stride;
+    const float* s_down;
+    int64_t lds_down, s_down_stride;
+    void* y;
+    int y_dtype;
+    int64_t ldy;
+    void* workspace;
+};
+int64_t moe_decode_bytes(int64_t tokens, int64_t hidden, int64_t inner, int experts, int top_k);
+hipError_t launch_moe_decode(const MoeArgs& a, hipStream_t st);
+
 }  // namespace fp8q

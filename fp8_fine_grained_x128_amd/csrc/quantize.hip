@@ -22,164 +22,10 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "device_common.hpp"
 #include "launch.hpp"
+#include "tile_io.hpp"
 
 namespace fp8q {
-
-// ----------------------------------------------------------------------------
-// Helpers
-// ----------------------------------------------------------------------------
-typedef unsigned short us2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
-// 16-byte load, marked non-temporal when NT: a quantizer that reads each
-// input byte once need not let its input displace cached data (such as the
-// codes a GEMM is about to read); measured 3-6 % faster at the step's sizes.
-// A gather reads repeated source rows and keeps the normal (cached) load.
-template <bool NT>
-__device__ __forceinline__ uint4 load16(const void* p) {
-    if constexpr (NT) {
-        const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
-        return make_uint4(v[0], v[1], v[2], v[3]);
-    } else {
-        return *reinterpret_cast<const uint4*>(p);
-    }
-}
-
-// Orders LDS traffic between the lanes of one wave: a wave's LDS operations
-// execute in program order, the fences keep the compiler from reordering them.
-__device__ __forceinline__ void wave_lds_sync() {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
-__device__ __forceinline__ bool wave_all(bool p) { return __all((int)p) != 0; }
-
-// fl32(x/s) by the reciprocal path (valid when s >= kFastScaleMin).
-__device__ __forceinline__ float quotient_fast(float x, float s, float r) {
-    const float y = x * r;
-    const float e = __builtin_fmaf(y, s, -x);
-    return __builtin_fmaf(-e, r, y);
-}
-
-__device__ __forceinline__ uint32_t encode4_fast(float v0, float v1, float v2, float v3, float s, float r) {
-    const uint32_t w = cvt2_in_range<false>(quotient_fast(v0, s, r), quotient_fast(v1, s, r), 0u);
-    return cvt2_in_range<true>(quotient_fast(v2, s, r), quotient_fast(v3, s, r), w);
-}
-
-// General-path encoder of either scale rule.
-template <bool POW2>
-__device__ __forceinline__ uint32_t encode4_any(float v0, float v1, float v2, float v3, const TileScale& t) {
-    if constexpr (POW2)
-        return encode4_mul(v0, v1, v2, v3, t.r);
-    else
-        return encode4(v0, v1, v2, v3, t);
-}
-
-// Fast-path encoder of either scale rule (s, r of a tile whose quotient may
-// take the reciprocal path).
-template <bool POW2>
-__device__ __forceinline__ uint32_t encode4_sr(float v0, float v1, float v2, float v3, float s, float r) {
-    if constexpr (POW2)
-        return encode4_mul(v0, v1, v2, v3, r);
-    else
-        return encode4_fast(v0, v1, v2, v3, s, r);
-}
-
-__device__ __forceinline__ TileScale scale_from(float s, float r) {
-    TileScale t;
-    t.s = s;
-    t.r = r;
-    t.fast = s >= kFastScaleMin;
-    return t;
-}
-
-// Eight consecutive input elements of one row, kept in their storage form.
-template <typename T>
-struct Raw8;
-
-template <>
-struct Raw8<uint16_t> {  // bf16 bit patterns, two per dword
-    uint4 d;
-    __device__ void zero() { d = make_uint4(0, 0, 0, 0); }
-    template <bool NT = true>
-    __device__ void load_full(const uint16_t* p) { d = load16<NT>(p); }
-    __device__ void load_partial(const uint16_t* p, int64_t n) {  // n < 8 valid elements
-        uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) w[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
-        d = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    __device__ uint32_t amax_bits() const {  // fp32 bits of max |x|
-        const us2 m0 = __builtin_bit_cast(us2, d.x & 0x7fff7fffu);
-        const us2 m1 = __builtin_bit_cast(us2, d.y & 0x7fff7fffu);
-        const us2 m2 = __builtin_bit_cast(us2, d.z & 0x7fff7fffu);
-        const us2 m3 = __builtin_bit_cast(us2, d.w & 0x7fff7fffu);
-        const us2 m = __builtin_elementwise_max(__builtin_elementwise_max(m0, m1),
-                                                __builtin_elementwise_max(m2, m3));
-        const uint32_t mm = m[0] > m[1] ? m[0] : m[1];
-        return mm << 16;
-    }
-    __device__ void values(float v[8]) const {
-        v[0] = bf16_lo(d.x); v[1] = bf16_hi(d.x);
-        v[2] = bf16_lo(d.y); v[3] = bf16_hi(d.y);
-        v[4] = bf16_lo(d.z); v[5] = bf16_hi(d.z);
-        v[6] = bf16_lo(d.w); v[7] = bf16_hi(d.w);
-    }
-};
-
-template <>
-struct Raw8<float> {
-    float4 a, b;
-    __device__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-    template <bool NT = true>
-    __device__ void load_full(const float* p) {
-        const uint4 u = load16<NT>(p), v = load16<NT>(p + 4);
-        a = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
-        b = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
-    }
-    __device__ void load_partial(const float* p, int64_t n) {
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : 0.0f;
-        a = make_float4(v[0], v[1], v[2], v[3]);
-        b = make_float4(v[4], v[5], v[6], v[7]);
-    }
-    __device__ uint32_t amax_bits() const {
-        uint32_t m = max(max(abs_bits(a.x), abs_bits(a.y)), max(abs_bits(a.z), abs_bits(a.w)));
-        return max(m, max(max(abs_bits(b.x), abs_bits(b.y)), max(abs_bits(b.z), abs_bits(b.w))));
-    }
-    __device__ void values(float v[8]) const {
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    }
-};
-
-// Loads x[c .. c+8) of a row; elements at or beyond `valid` read as 0.
-// `full` (wave-uniform) says that all 8 are valid.
-template <typename T, bool NT = true>
-__device__ __forceinline__ void load_row8(Raw8<T>& r, const T* row, int64_t c, int64_t valid, bool full) {
-    if (full || c + 8 <= valid)
-        r.template load_full<NT>(row + c);
-    else if (c < valid)
-        r.load_partial(row + c, valid - c);
-    else
-        r.zero();
-}
-
-// Stores 8 codes (two dwords) at q[c .. c+8), clipped to `valid`.
-__device__ __forceinline__ void store8(uint8_t* q, int64_t c, int64_t valid, uint32_t w0, uint32_t w1) {
-    if (c + 8 <= valid) {
-        *reinterpret_cast<uint2*>(q + c) = make_uint2(w0, w1);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c + i < valid) q[c + i] = (uint8_t)(((i < 4 ? w0 : w1) >> (8 * (i & 3))) & 0xffu);
-    }
-}
 
 // ----------------------------------------------------------------------------
 // 1x128 activation tiles.
@@ -371,15 +217,6 @@ __global__ __launch_bounds__(512) void quantize_128x128_kernel(
 // maxima of all 32 row groups in LDS: 12 % more bandwidth for requantization
 // and bf16 at 8192x7168, from 4 to 8 resident work-groups per CU.)
 // ----------------------------------------------------------------------------
-// Hides a register's value from the optimizer: values derived from it are
-// recomputed after this point instead of being kept live across it.
-template <typename V>
-__device__ __forceinline__ void opaque(V& x) {
-#if defined(__HIP_DEVICE_COMPILE__)
-    asm volatile("" : "+v"(x));
-#endif
-}
-
 enum SrcKind { SRC_F32 = 0, SRC_BF16 = 1, SRC_FP8 = 2 };
 
 __device__ __forceinline__ int swz_unit(int ch, int unit) { return unit ^ ((ch >> 3) & 7); }

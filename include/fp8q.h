@@ -347,6 +347,144 @@ int fp8q_gemm_splitk_noalloc(const uint8_t *a, int64_t lda, const float *sa, int
  */
 int fp8q_clock_probe(uint64_t *out, int64_t ticks, void *stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Operators around the GEMMs of a feed-forward block: the norm in front of
+ * it, the SwiGLU between its GEMMs, and the whole mixture-of-experts layer
+ * for the few tokens of a decode step.  The conventions above hold; sums,
+ * statistics and everything between the stored types are fp32.
+ * ---------------------------------------------------------------------------
+ */
+
+typedef enum { FP8Q_NORM_LAYER = 0, FP8Q_NORM_RMS = 1 } fp8q_norm_kind;
+
+/* Largest number of columns of the norms (a work-group holds a row in registers). */
+#define FP8Q_NORM_MAX_COLS 16384
+
+/*
+ * Layer norm or RMS norm of each row of x[rows][cols] (x_dtype, stride ldx):
+ *   mu = mean x (RMS: 0),  r = 1 / sqrt(mean (x - mu)^2 + eps),
+ *   y  = (x - mu) * r * gamma + beta.
+ * gamma, beta: [cols] of w_dtype, 16-byte aligned; NULL = ones, zeros.
+ * Outputs, at least one of the first two:
+ *   y[rows][cols] (y_dtype, stride ldy; NULL = not written);
+ *   codes q[rows][cols] and scales s[ceil(cols/128)][rows], the 1x128
+ *     quantization of the fp32 y with `scale_mode` (NULL both = none): the
+ *     operand of the next GEMM and what the backward pass keeps of it (page
+ *     1, why-be.why-be.co.kr wr_id=65900, passage on activations cached in
+ *     FP8);
+ *   mean[rows] (layer norm) and rstd[rows], fp32, for the backward pass
+ *     (NULL = not written).
+ * Each row is read once.  cols > FP8Q_NORM_MAX_COLS gives FP8Q_EUNSUPPORTED.
+ */
+int fp8q_layernorm(const void *x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx,
+                   const void *gamma, const void *beta, int w_dtype, float eps, int kind,
+                   void *y, int y_dtype, int64_t ldy, uint8_t *q, int64_t ldq, float *s, int64_t lds,
+                   int scale_mode, float *mean, float *rstd, void *stream);
+
+/*
+ * Backward pass of fp8q_layernorm.  dy, x, skip and dx are [rows][cols] of
+ * one dtype; mean (layer norm only) and rstd as the forward pass wrote them.
+ * With xh = (x - mean) * rstd and w = dy * gamma, over each row:
+ *   dx = rstd * (w - xh * mean(w * xh) - mean(w)) + skip   (RMS: no mean(w))
+ * skip (NULL = none) is the gradient that reaches x by another way (the
+ * residual around the block).  dx may be dy or skip itself.  Over all rows:
+ *   dgamma[cols] (=|+=) sum dy * xh,  dbeta[cols] (=|+=) sum dy    (fp32;
+ * NULL = not computed; += with accumulate != 0).
+ * The weights' gradients are summed in a fixed order through `workspace`
+ * (DEVICE memory of at least fp8q_layernorm_backward_workspace(rows, cols)
+ * bytes, 256-byte aligned, not needed if both are NULL; see
+ * fp8q_gemm_splitk for its rules): repeated calls give the same bits.
+ * rows == 0 sets dgamma and dbeta to zero (or leaves them, with accumulate).
+ */
+int64_t fp8q_layernorm_backward_workspace(int64_t rows, int64_t cols);
+
+int fp8q_layernorm_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx, int dtype,
+                            int64_t rows, int64_t cols, const void *gamma, int w_dtype,
+                            const float *mean, const float *rstd, int kind, const void *skip,
+                            int64_t ldskip, void *dx, int64_t lddx, float *dgamma, float *dbeta,
+                            int accumulate, void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * SwiGLU into FP8 codes, its inputs kept as 8-bit checkpoints: the pages
+ * cache the SwiGLU's inputs and recompute its output in the backward pass
+ * (page 1, why-be.why-be.co.kr wr_id=65900, passage on the SwiGLU operator).
+ *   h = g * u / (1 + exp(-g))
+ * g, u: [rows][cols] of `dtype`, both with row stride ldgu (the two halves of
+ * a fused gate|up product, or two arrays).
+ * qh[rows][cols], sh[ceil(cols/128)][rows]: h in 1x128 tiles (`scale_mode`),
+ * the A operand of the down projection.  qg, qu (stride ldq) and sg, su
+ * (stride lds): g and u in 1x128 tiles, the same codes and scales that
+ * fp8q_quantize_act gives; all four NULL = no checkpoint (inference).
+ */
+int fp8q_swiglu_quantize(const void *g, const void *u, int dtype, int64_t ldgu, int64_t rows,
+                         int64_t cols, uint8_t *qh, int64_t ldqh, float *sh, int64_t ldsh,
+                         uint8_t *qg, uint8_t *qu, int64_t ldq, float *sg, float *su, int64_t lds,
+                         int scale_mode, void *stream);
+
+/*
+ * Backward pass of the SwiGLU from its checkpoint: with g, u the values
+ * fl32(dec(q) * s), sg = 1 / (1 + exp(-g)) and the incoming gradient
+ * dh[rows][cols] (`dtype`, stride lddh),
+ *   du = dh * g * sg,   dg = dh * u * sg * (1 + g * (1 - sg)).
+ * fp8q_swiglu_backward writes dg and du, [rows][cols] of `dtype`, row stride
+ * ldd.  fp8q_swiglu_backward_quantize writes every FP8 operand that the
+ * backward GEMMs of the block take, from one read of the checkpoint:
+ *   qdg, qdu (stride ldqd), sdg, sdu (stride ldsd >= rows): 1x128 tiles, the
+ *     A operand of the gate and up projections' Dgrad;
+ *   qdgt, qdut [cols][rows] (stride ldqt), sdgt, sdut [ceil(rows/128)][cols]
+ *     (stride ldst): 128x1 tiles, transposed, the A operand of their Wgrad;
+ *   qht [cols][rows] (stride ldqht), sht (stride ldsht): the recomputed h in
+ *     128x1 tiles, transposed, the B operand (FP8Q_BSCALE_ROW) of the down
+ *     projection's Wgrad.
+ */
+int fp8q_swiglu_backward(const uint8_t *qg, const uint8_t *qu, int64_t ldq, const float *sg,
+                         const float *su, int64_t lds, const void *dh, int dtype, int64_t lddh,
+                         int64_t rows, int64_t cols, void *dg, void *du, int64_t ldd, void *stream);
+
+int fp8q_swiglu_backward_quantize(const uint8_t *qg, const uint8_t *qu, int64_t ldq, const float *sg,
+                                  const float *su, int64_t lds, const void *dh, int dtype, int64_t lddh,
+                                  int64_t rows, int64_t cols, uint8_t *qdg, uint8_t *qdu, int64_t ldqd,
+                                  float *sdg, float *sdu, int64_t ldsd, uint8_t *qdgt, uint8_t *qdut,
+                                  int64_t ldqt, float *sdgt, float *sdut, int64_t ldst, uint8_t *qht,
+                                  int64_t ldqht, float *sht, int64_t ldsht, int scale_mode, void *stream);
+
+/*
+ * A whole mixture-of-experts layer for few tokens (fp8q_grouped_gemm is made
+ * for many): routing, the chosen experts' gate, up and down projections with
+ * the SwiGLU between them, and the weighted sum.
+ *   x[tokens][hidden] bf16 (stride ldx); logits[tokens][experts] fp32 (ldl);
+ *   w_gu [experts][2*inner][hidden], gate rows first (row stride ldw_gu,
+ *   expert stride w_gu_stride), scales s_gu [experts][2*inner/128][hidden/128]
+ *   (lds_gu, s_gu_stride); w_down [experts][hidden][inner] and s_down
+ *   likewise: codes with 128x128 block scales as fp8q_quantize_weight writes.
+ * Token t takes the top_k largest of its logits, ties to the lower index,
+ * -inf never: S_t (fewer than top_k where there are fewer candidates).
+ *   p_te = exp(l_te - max) / sum over S_t (renormalize != 0) or over all;
+ *   y_t  = sum_{e in S_t} p_te * Wd_e (silu(Wg_e x_t) * (Wu_e x_t)).
+ * An empty S_t gives a zero row (an empty slot of a batch); a token with a
+ * NaN or +inf logit gives a row of NaN, as its softmax would.
+ * y[tokens][hidden] (y_dtype, stride ldy).  Weights and x are multiplied
+ * exactly and summed in fp32; the SwiGLU's result is held to 16 significant
+ * bits between the products.  Repeated calls give the same bits.
+ * hidden and inner are multiples of 128; tokens <= FP8Q_MOE_MAX_TOKENS,
+ * top_k <= FP8Q_MOE_MAX_TOP_K, experts <= 1024 (else FP8Q_EUNSUPPORTED).
+ * workspace: at least fp8q_moe_decode_workspace(...) bytes (0 for sizes that
+ * the call refuses), 256-byte aligned, under the rules of fp8q_gemm_splitk.
+ */
+#define FP8Q_MOE_MAX_TOKENS 64
+#define FP8Q_MOE_MAX_TOP_K 32
+
+int64_t fp8q_moe_decode_workspace(int64_t tokens, int64_t hidden, int64_t inner, int experts, int top_k);
+
+int fp8q_moe_decode(const void *x, int64_t ldx, int64_t tokens, int64_t hidden, const float *logits,
+                    int64_t ldl, int experts, int top_k, int renormalize, int64_t inner,
+                    const uint8_t *w_gu, int64_t ldw_gu, int64_t w_gu_stride, const float *s_gu,
+                    int64_t lds_gu, int64_t s_gu_stride, const uint8_t *w_down, int64_t ldw_down,
+                    int64_t w_down_stride, const float *s_down, int64_t lds_down, int64_t s_down_stride,
+                    void *y, int y_dtype, int64_t ldy, void *workspace, int64_t workspace_bytes,
+                    void *stream);
+
 /* Static, human-readable name of a status code (never NULL). */
 const char *fp8q_strerror(int status);
 
