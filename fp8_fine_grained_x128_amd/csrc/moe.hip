@@ -36,23 +36,19 @@ typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 
 constexpr int kMaxTokens = 64;
 constexpr int kMaxExperts = 1024;
-constexpr int kMaxTopK = 32;
 
-// Where the pieces of the workspace lie (bytes from its start).
+// Where the pieces of the workspace lie (bytes from its start).  Token t's
+// pairs are t*top_k, t*top_k + 1, ..., one for each of its experts in
+// ascending order.
 struct MoeLayout {
     int slots;      // active experts at most
-    int64_t pairs;  // (token, expert) pairs at most
-    int64_t experts, base, mask, prob, pair, hi, lo, parts, total;
-};
-
-// Routing's result in the workspace.  Pairs are numbered expert by expert
-// (ascending), a pair's place among its expert's is its token's rank in the
-// expert's mask.
-struct MoePlan {
-    int active;         // number of active experts
-    int pad;
-    uint64_t nan_mask;  // tokens whose logits hold NaN or +inf: their rows are NaN
-    int count[kMaxTokens];
+    int words;      // 64-bit words of a token's expert set
+    int64_t sets;   // uint64[tokens][words]
+    int64_t count;  // int[tokens]: experts of the token; -1: its logits hold NaN or +inf
+    int64_t prob;   // float[pairs]
+    int64_t hi, lo; // bf16[pairs][inner]: h
+    int64_t parts;  // float[pairs][hidden]
+    int64_t total;
 };
 
 __device__ __forceinline__ v8bf bf16_of_codes(uint32_t w0, uint32_t w1) {
@@ -74,180 +70,149 @@ __device__ __forceinline__ v4f mfma(v8bf a, v8bf b, v4f c) {
 #endif
 }
 
-__device__ __forceinline__ int rank_below(uint64_t mask, int t) { return __popcll(mask & ((1ull << t) - 1)); }
+// Bitwise or over the lanes of a wave, the same in all of them.
+__device__ __forceinline__ uint32_t wave_or(uint32_t v) {
+    v |= row_ror<8>(v);
+    v |= row_ror<4>(v);
+    v |= row_ror<2>(v);
+    v |= row_ror<1>(v);
+    return __builtin_amdgcn_readlane(v, 0) | __builtin_amdgcn_readlane(v, 16) | __builtin_amdgcn_readlane(v, 32) |
+           __builtin_amdgcn_readlane(v, 48);
+}
 
 }  // namespace
 
 // ----------------------------------------------------------------------------
-// Routing: one work-group, a wave per token at a time.  Logits become
-// order-preserving keys (-0 counts as 0); the k-th largest key is found bit
-// by bit with wave ballots, then ties at that key go to the lowest indices.
+// Routing: a wave per token.  Logits become order-preserving keys (-0 counts
+// as 0); the k-th largest key is found bit by bit with wave ballots, ending
+// early where exactly top_k keys lie at or above the prefix found so far;
+// ties at the k-th key go to the lowest indices.
+//   Only sets of experts are written, so tokens need nothing of each other
+// and every token has a compute unit of its own (one work-group for all
+// tokens was bound by its scalar unit: 10 us for 64 tokens).
 // ----------------------------------------------------------------------------
-constexpr int kRouteWaves = 16;
-
 template <int PL>  // experts per lane
-__global__ __launch_bounds__(64 * kRouteWaves) void moe_route_kernel(MoeArgs a, MoeLayout L) {
-    __shared__ uint64_t s_mask[64 * PL];
-    __shared__ uint64_t s_nan;
-    __shared__ int s_base[64 * PL];
-    __shared__ int s_id[kMaxTokens][kMaxTopK];
-    __shared__ float s_p[kMaxTokens][kMaxTopK];
-    __shared__ int s_n[kMaxTokens];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int e = threadIdx.x; e < 64 * PL; e += blockDim.x) s_mask[e] = 0;
-    if (threadIdx.x == 0) s_nan = 0;
-    __syncthreads();
+__global__ __launch_bounds__(64) void moe_route_kernel(MoeArgs a, MoeLayout L) {
+    const int lane = threadIdx.x, t = blockIdx.x;
     constexpr uint32_t kNone = 0x007fffffu;  // key of -inf; keys up to it are no candidates
     const uint64_t below = (1ull << lane) - 1;
-    for (int t = wave; t < a.tokens; t += blockDim.x / 64) {
-        const float* row = a.logits + (int64_t)t * a.ldl;
-        float l[PL];
-        uint32_t key[PL];
-        float top = -__builtin_inff();
-        bool bad = false;
-#pragma unroll
-        for (int j = 0; j < PL; ++j) {
-            const int e = lane + 64 * j;
-            l[j] = e < a.experts ? row[e] + 0.0f : -__builtin_inff();
-        }
-#pragma unroll
-        for (int j = 0; j < PL; ++j) {
-            const uint32_t b = __float_as_uint(l[j]);
-            key[j] = b & 0x80000000u ? ~b : b | 0x80000000u;
-            bad = bad || !(l[j] < __builtin_inff());
-            top = fmaxf(top, l[j]);
-        }
-        if (__any((int)bad)) {
-            if (lane == 0) {
-                atomicOr((unsigned long long*)&s_nan, 1ull << t);
-                s_n[t] = 0;
-            }
-            continue;
-        }
-#pragma unroll
-        for (int off = 32; off; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
-        uint32_t kth = 0;
-#pragma unroll
-        for (int bit = 31; bit >= 0; --bit) {
-            const uint32_t cand = kth | (1u << bit);
-            int n = 0;
-#pragma unroll
-            for (int j = 0; j < PL; ++j) n += __popcll(__ballot(key[j] >= cand));
-            if (n >= a.top_k) kth = cand;
-        }
-        kth = max(kth, kNone);  // fewer candidates than top_k: all of them
-        int above = 0;
-#pragma unroll
-        for (int j = 0; j < PL; ++j) above += __popcll(__ballot(key[j] > kth));
-        int ties = kth > kNone ? a.top_k - above : 0, n = 0;
-        float p[PL], total = 0.0f;
-        int at[PL];  // place among the token's choices, or -1
-#pragma unroll
-        for (int j = 0; j < PL; ++j) {
-            const uint64_t tie = __ballot(key[j] == kth);
-            const bool in = key[j] > kth || (key[j] == kth && __popcll(tie & below) < ties);
-            const uint64_t in_mask = __ballot(in);
-            ties -= min(ties, (int)__popcll(tie));
-            p[j] = key[j] > kNone ? expf(l[j] - top) : 0.0f;
-            at[j] = in ? n + (int)__popcll(in_mask & below) : -1;
-            n += __popcll(in_mask);
-            total += in || !a.renormalize ? p[j] : 0.0f;
-        }
-        total = wave_sum(total);
-#pragma unroll
-        for (int j = 0; j < PL; ++j) {
-            if (at[j] < 0) continue;
-            s_id[t][at[j]] = lane + 64 * j;
-            s_p[t][at[j]] = p[j] / total;
-            atomicOr((unsigned long long*)&s_mask[lane + 64 * j], 1ull << t);
-        }
-        if (lane == 0) s_n[t] = n;
-    }
-    __syncthreads();
+    const float* row = a.logits + (int64_t)t * a.ldl;
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-    if (wave == 0) {  // active experts in ascending order, with their first pair
-        int active = 0, pairs = 0;
+    uint64_t* set = reinterpret_cast<uint64_t*>(ws + L.sets) + (int64_t)t * L.words;
+    int* count = reinterpret_cast<int*>(ws + L.count) + t;
+
+    float l[PL], top = -__builtin_inff();
+    uint32_t key[PL];
+    bool bad = false;
 #pragma unroll
-        for (int j = 0; j < PL; ++j) {
-            const int e = lane + 64 * j;
-            const uint64_t m = s_mask[e];
-            const uint64_t live = __ballot(m != 0);
-            const int cnt = __popcll(m);
-            int before = cnt;  // inclusive prefix sum over the lanes
+    for (int j = 0; j < PL; ++j) {
+        const int e = lane + 64 * j;
+        l[j] = e < a.experts ? row[e] + 0.0f : -__builtin_inff();
+    }
 #pragma unroll
-            for (int off = 1; off < 64; off <<= 1) {
-                const int o = __shfl_up(before, off);
-                if (lane >= off) before += o;
-            }
-            if (m) {
-                const int idx = active + (int)__popcll(live & below);
-                const int first = pairs + before - cnt;
-                s_base[e] = first;
-                reinterpret_cast<int*>(ws + L.experts)[idx] = e;
-                reinterpret_cast<int*>(ws + L.base)[idx] = first;
-                reinterpret_cast<uint64_t*>(ws + L.mask)[idx] = m;
-            }
-            active += __popcll(live);
-            pairs += __shfl(before, 63);
-        }
-        MoePlan* plan = reinterpret_cast<MoePlan*>(ws);
-        if (lane == 0) {
-            plan->active = active;
-            plan->nan_mask = s_nan;
-        }
-        if (lane < a.tokens) plan->count[lane] = s_n[lane];
+    for (int j = 0; j < PL; ++j) {
+        const uint32_t b = __float_as_uint(l[j]);
+        key[j] = b & 0x80000000u ? ~b : b | 0x80000000u;
+        bad = bad || !(l[j] < __builtin_inff());
+        top = fmaxf(top, l[j]);
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < a.tokens * kMaxTopK; i += blockDim.x) {
-        const int t = i / kMaxTopK, at = i % kMaxTopK;
-        if (at >= s_n[t]) continue;
-        const int e = s_id[t][at];
-        const int pair = s_base[e] + rank_below(s_mask[e], t);
-        reinterpret_cast<float*>(ws + L.prob)[pair] = s_p[t][at];
-        reinterpret_cast<int*>(ws + L.pair)[i] = pair;
+    if (__any((int)bad)) {
+        if (lane < L.words) set[lane] = 0;
+        if (lane == 0) *count = -1;
+        return;
     }
+#pragma unroll
+    for (int off = 32; off; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
+    uint32_t kth = 0;
+    for (int bit = 31; bit >= 0; --bit) {
+        const uint32_t cand = kth | (1u << bit);
+        int n = 0;
+#pragma unroll
+        for (int j = 0; j < PL; ++j) n += __popcll(__ballot(key[j] >= cand));
+        if (n >= a.top_k) kth = cand;
+        if (n == a.top_k) break;
+    }
+    kth = max(kth, kNone + 1);  // fewer candidates than top_k: all of them
+    int above = 0;
+#pragma unroll
+    for (int j = 0; j < PL; ++j) above += __popcll(__ballot(key[j] > kth));
+    int ties = a.top_k - above, n = 0;
+    float p[PL], total = 0.0f;
+    int at[PL];  // place among the token's choices, or -1
+#pragma unroll
+    for (int j = 0; j < PL; ++j) {
+        // the search may end at a prefix below the k-th key: then exactly
+        // top_k keys are at or above it, and all "ties" are in
+        const uint64_t tie = __ballot(key[j] == kth);
+        const bool in = key[j] > kth || (key[j] == kth && __popcll(tie & below) < ties);
+        const uint64_t in_mask = __ballot(in);
+        ties -= min(ties, (int)__popcll(tie));
+        p[j] = key[j] >= kNone + 1 ? expf(l[j] - top) : 0.0f;
+        at[j] = in ? n + (int)__popcll(in_mask & below) : -1;
+        n += __popcll(in_mask);
+        total += in || !a.renormalize ? p[j] : 0.0f;
+        if (lane == 0 && j < L.words) set[j] = in_mask;
+    }
+    total = wave_sum(total);
+    float* prob = reinterpret_cast<float*>(ws + L.prob) + t * a.top_k;
+#pragma unroll
+    for (int j = 0; j < PL; ++j)
+        if (at[j] >= 0) prob[at[j]] = p[j] / total;
+    if (lane == 0) *count = n;
 }
 
 // ----------------------------------------------------------------------------
-// Both projections: a work-group of four waves takes 64 weight rows (four row
-// tiles) of one active expert and 16 of its tokens at a time.  The waves take
-// every fourth 128-wide chunk of the contraction and join their sums in LDS;
-// a wave loads its next chunk while it multiplies the current one.  Weights
-// go straight from memory to the matrix operand (16 rows of 64 contiguous
-// bytes a load: the same rate as whole lines), each one read once; 64 rows
-// share one read of the tokens, so those cost at most (tokens x 2 or 4)/64 of
-// the weights' bytes, from the caches.
-// A lane whose column has no token repeats the first one's reads; its results
-// are dropped.
+// Both projections.  A work-group takes 16*NT weight rows (NT row tiles: rows
+// of the hidden size, or NT/2 tiles of gate rows and the up rows that belong
+// to them) of one active expert.  Its four waves take every fourth 128-wide
+// chunk of the contraction, for 16 of the expert's tokens at a time, and join
+// their sums in LDS.
+//   Weights go straight from memory to the matrix operand (16 rows of 64
+// contiguous bytes a load), each one read once.  The row tiles share one read
+// of the tokens, which comes from the caches; lanes of a column without a
+// token read nothing and their results are dropped.
 // ----------------------------------------------------------------------------
-constexpr int kTiles = 4;  // row tiles of 16 in a work-group
 
-// NB: activation arrays whose sum is multiplied (x, or hi and lo).
-template <int NB>
+// A 128-wide chunk.  NB: activation arrays whose sum is multiplied (x, or hi
+// and lo).
+template <int NT, int NB>
 struct Chunk {
-    uint4 w[kTiles][2];
+    uint4 w[NT][2];
     uint4 b[NB][4];
+    float s[2];  // block scales of the first and of the last half of the row tiles
 };
 
-template <int NB>
-__device__ __forceinline__ void load_chunk(Chunk<NB>& c, const uint8_t* const (&w)[kTiles],
-                                           const uint16_t* const (&b)[NB], int kb) {
+// Where a work-group's chunks come from.
+template <int NT, int NB>
+struct Operands {
+    const uint8_t* w[NT];
+    const uint16_t* b[NB];
+    const float* s[2];
+    uint32_t row_offset;  // of the lane in a row tile
+    bool live;            // the lane's column has a token
+};
+
+template <int NT, int NB>
+__device__ __forceinline__ void load_chunk(Chunk<NT, NB>& c, const Operands<NT, NB>& o, int kb) {
     const int64_t k = 128 * (int64_t)kb;
+    c.s[0] = o.s[0][kb];
+    c.s[1] = o.s[1][kb];
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) c.w[t][j] = *reinterpret_cast<const uint4*>(w[t] + k + 64 * j);
+        for (int j = 0; j < 2; ++j) c.w[t][j] = *reinterpret_cast<const uint4*>(o.w[t] + k + 64 * j + o.row_offset);
+    if (!o.live) return;
 #pragma unroll
     for (int n = 0; n < NB; ++n)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            c.b[n][j] = *reinterpret_cast<const uint4*>(b[n] + k + 64 * (j >> 1) + 8 * (j & 1));
+            c.b[n][j] = *reinterpret_cast<const uint4*>(o.b[n] + k + (NB == 2 ? 32 * j : 64 * (j >> 1) + 8 * (j & 1)));
 }
 
-template <int NB>
-__device__ __forceinline__ void multiply_chunk(v4f (&acc)[kTiles], const Chunk<NB>& c, float s01, float s23) {
+template <int NT, int NB>
+__device__ __forceinline__ void multiply_chunk(v4f (&acc)[NT], const Chunk<NT, NB>& c) {
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
+    for (int t = 0; t < NT; ++t) {
         v4f p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -258,132 +223,170 @@ __device__ __forceinline__ void multiply_chunk(v4f (&acc)[kTiles], const Chunk<N
                 p = mfma(w1, __builtin_bit_cast(v8bf, c.b[n][2 * j + 1]), p);
             }
         }
-        const float s = t < kTiles / 2 ? s01 : s23;
+        const float s = c.s[2 * t / NT];
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[t][i] = __builtin_fmaf(p[i], s, acc[t][i]);
     }
 }
 
-// Sums over the chunks wave, wave+4, ... ; s01 and s23 are the block scales'
-// rows of the first and last two row tiles.
-template <int NB>
-__device__ __forceinline__ void multiply(v4f (&acc)[kTiles], const uint8_t* const (&w)[kTiles],
-                                         const uint16_t* const (&b)[NB], const float* s01, const float* s23,
-                                         int chunks, int wave) {
+// Sums over the chunks wave, wave+4, ..., joined over the waves in LDS:
+// [wave][row tile][token column * 16 + row].
+template <int NT, int NB>
+__device__ __forceinline__ void multiply(float (*sums)[NT][256], const Operands<NT, NB>& o, int chunks, int wave) {
+    v4f acc[NT];
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
-    Chunk<NB> c0, c1;
-    int kb = wave;
-    if (kb >= chunks) return;
-    load_chunk<NB>(c0, w, b, kb);
-    for (;;) {
-        if (kb + 4 < chunks) load_chunk<NB>(c1, w, b, kb + 4);
-        multiply_chunk<NB>(acc, c0, s01[kb], s23[kb]);
-        kb += 4;
-        if (kb >= chunks) return;
-        if (kb + 4 < chunks) load_chunk<NB>(c0, w, b, kb + 4);
-        multiply_chunk<NB>(acc, c1, s01[kb], s23[kb]);
-        kb += 4;
-        if (kb >= chunks) return;
+    for (int t = 0; t < NT; ++t) acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
+    Chunk<NT, NB> c;
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c.b[n][j] = make_uint4(0, 0, 0, 0);
+    for (int kb = wave; kb < chunks; kb += 4) {
+        load_chunk<NT, NB>(c, o, kb);
+        multiply_chunk<NT, NB>(acc, c);
     }
-}
-
-// The lane's token among the expert's (the (t0 + r)-th bit of the mask); the
-// first one's for a lane without.
-__device__ __forceinline__ int token_of(uint64_t mask, int t0, int r) {
-    int mine = __builtin_ctzll(mask);
-    for (int i = 0; mask != 0; ++i, mask &= mask - 1)
-        if (i == t0 + r) mine = __builtin_ctzll(mask);
-    return mine;
-}
-
-// Writes the waves' sums to LDS: element (token column, row) of tile t.
-__device__ __forceinline__ void put_sums(float (*s_acc)[kTiles][256], const v4f (&acc)[kTiles], int wave, int r, int kq) {
+    const int lane = threadIdx.x & 63;
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) *reinterpret_cast<v4f*>(&s_acc[wave][t][r * 16 + 4 * kq]) = acc[t];
+    for (int t = 0; t < NT; ++t) *reinterpret_cast<v4f*>(&sums[wave][t][16 * (lane & 15) + 4 * (lane >> 4)]) = acc[t];
+    __syncthreads();
 }
 
-__device__ __forceinline__ float sum_waves(const float (*s_acc)[kTiles][256], int t, int at) {
-    return (s_acc[0][t][at] + s_acc[1][t][at]) + (s_acc[2][t][at] + s_acc[3][t][at]);
+template <int NT>
+__device__ __forceinline__ float sum_waves(const float (*s)[NT][256], int t, int at) {
+    return (s[0][t][at] + s[1][t][at]) + (s[2][t][at] + s[3][t][at]);
 }
 
-// Gate and up projections with the SwiGLU: 32 gate rows and the 32 up rows
-// that belong to them.
-__global__ __launch_bounds__(256) void moe_up_kernel(MoeArgs a, MoeLayout L) {
-    __shared__ __align__(16) float s_acc[4][kTiles][256];
-    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-    const int idx = blockIdx.y;
-    if (idx >= reinterpret_cast<const MoePlan*>(ws)->active) return;
-    const int e = reinterpret_cast<const int*>(ws + L.experts)[idx];
-    const int base = reinterpret_cast<const int*>(ws + L.base)[idx];
-    const uint64_t mask = reinterpret_cast<const uint64_t*>(ws + L.mask)[idx];
-    const int count = __popcll(mask);
-    const float* prob = reinterpret_cast<const float*>(ws + L.prob) + base;
+// Where column k of h is stored in its row: inside each 128-wide chunk, column
+// 64*j + 16*kq + 8*i + n (the bytes of a 16-byte load of the weights) lies at
+// 64*j + 32*i + 8*kq + n, so that a load instruction of the down projection
+// reads 64 contiguous bytes of every token.
+__device__ __forceinline__ int64_t h_place(int64_t k) {
+    return (k & ~int64_t(0x3f)) | ((k & 8) << 2) | ((k & 0x30) >> 1) | (k & 7);
+}
 
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int r = lane & 15, kq = lane >> 4;
-    const int64_t row0 = (int64_t)blockIdx.x * 32;
-    const uint8_t* wg = a.w_gu + e * a.w_gu_stride + (row0 + r) * a.ldw_gu + 16 * kq;
-    const uint8_t* wu = wg + a.inner * a.ldw_gu;
-    const uint8_t* w[kTiles] = {wg, wg + 16 * a.ldw_gu, wu, wu + 16 * a.ldw_gu};
-    const float* sg = a.s_gu + e * a.s_gu_stride + (row0 >> 7) * a.lds_gu;
-    const float* su = sg + (a.inner >> 7) * a.lds_gu;
+// The work-group's expert, its tokens and their pairs, from the tokens' sets:
+// lane t of every wave looks at token t.
+struct Chosen {
+    int expert;  // -1: there are not that many active experts
+    int count;   // tokens
+};
 
-    for (int t0 = 0; t0 < count; t0 += 16) {
-        const uint16_t* x[1] = {a.x + token_of(mask, t0, r) * a.ldx + 16 * kq};
-        v4f acc[kTiles];
-        multiply<1>(acc, w, x, sg, su, (int)(a.hidden >> 7), wave);
-        put_sums(s_acc, acc, wave, r, kq);
-        __syncthreads();
-        const int tok = threadIdx.x >> 4, c = 2 * (threadIdx.x & 15);  // two neighbouring columns of h
-        if (t0 + tok < count) {
-            float h[2];
+__device__ __forceinline__ Chosen choose(const MoeArgs& a, const MoeLayout& L, int idx, int* tokens, int* pairs) {
+    const int t = threadIdx.x & 63;
+    const uint64_t* set = reinterpret_cast<const uint64_t*>(static_cast<const uint8_t*>(a.workspace) + L.sets) + t * L.words;
+    int rank = 0;  // the token's experts below
+    for (int w0 = 0; w0 < L.words; w0 += 4) {
+        uint64_t m[4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int at = tok * 16 + (c & 15) + i;
-                const float g = sum_waves(s_acc, c >> 4, at), u = sum_waves(s_acc, 2 + (c >> 4), at);
-                h[i] = g / (1.0f + expf(-g)) * u * prob[t0 + tok];
+        for (int i = 0; i < 4; ++i) m[i] = t < a.tokens && w0 + i < L.words ? set[w0 + i] : 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint64_t any = wave_or((uint32_t)m[i]) | (uint64_t)wave_or((uint32_t)(m[i] >> 32)) << 32;
+            const int n = __popcll(any);
+            if (idx >= n) {
+                idx -= n;
+                rank += __popcll(m[i]);
+                continue;
             }
-            const uint32_t hi = pack_bf16(h[0], h[1]);
-            const int64_t at = (int64_t)(base + t0 + tok) * a.inner + row0 + c;
-            *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(ws + L.hi) + at) = hi;
-            *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(ws + L.lo) + at) =
-                pack_bf16(h[0] - bf16_lo(hi), h[1] - bf16_hi(hi));
+            for (; idx > 0; --idx) any &= any - 1;
+            const int bit = __builtin_ctzll(any);
+            const bool mine = (m[i] >> bit) & 1;
+            const uint64_t users = __ballot(mine);
+            if (mine && threadIdx.x < 64) {
+                const int at = __popcll(users & ((1ull << t) - 1));
+                tokens[at] = t;
+                pairs[at] = t * a.top_k + rank + (int)__popcll(m[i] & ((1ull << bit) - 1));
+            }
+            return {64 * (w0 + i) + bit, (int)__popcll(users)};
+        }
+    }
+    return {-1, 0};
+}
+
+// Gate and up projections with the SwiGLU.
+template <int NT>
+__global__ __launch_bounds__(256, 4) void moe_up_kernel(MoeArgs a, MoeLayout L) {
+    __shared__ __align__(16) float s_sums[4][NT][256];
+    __shared__ int s_token[kMaxTokens], s_pair[kMaxTokens];
+    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+    const Chosen e = choose(a, L, blockIdx.y, s_token, s_pair);
+    if (e.expert < 0) return;
+    __syncthreads();
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15, kq = lane >> 4;
+    constexpr int kCols = 8 * NT;  // columns of h
+    const int64_t row0 = (int64_t)blockIdx.x * kCols;
+    Operands<NT, 1> o;
+    const uint8_t* w = a.w_gu + e.expert * a.w_gu_stride + row0 * a.ldw_gu;
+#pragma unroll
+    for (int t = 0; t < NT / 2; ++t) {
+        o.w[t] = w + 16 * t * a.ldw_gu;
+        o.w[NT / 2 + t] = w + (a.inner + 16 * t) * a.ldw_gu;
+    }
+    o.row_offset = (uint32_t)(r * a.ldw_gu) + 16 * kq;
+    o.s[0] = a.s_gu + e.expert * a.s_gu_stride + (row0 >> 7) * a.lds_gu;
+    o.s[1] = o.s[0] + (a.inner >> 7) * a.lds_gu;
+    for (int t0 = 0; t0 < e.count; t0 += 16) {
+        o.live = t0 + r < e.count;
+        o.b[0] = a.x + (o.live ? s_token[t0 + r] : 0) * a.ldx + 16 * kq;
+        multiply<NT, 1>(s_sums, o, (int)(a.hidden >> 7), wave);
+        constexpr int kPer = NT / 2;  // columns of a thread
+        const int tok = threadIdx.x >> 4, c = kPer * (threadIdx.x & 15);
+        if (t0 + tok < e.count) {
+            const int64_t pair = s_pair[t0 + tok];
+            const float p = reinterpret_cast<const float*>(ws + L.prob)[pair];
+            const int64_t at = pair * a.inner + h_place(row0 + c);
+            float h[kPer];
+            uint16_t hi[kPer], lo[kPer];
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int in = tok * 16 + (c & 15) + i;
+                const float g = sum_waves<NT>(s_sums, c >> 4, in), u = sum_waves<NT>(s_sums, NT / 2 + (c >> 4), in);
+                h[i] = g / (1.0f + expf(-g)) * u * p;
+                hi[i] = (uint16_t)pack_bf16(h[i], 0.0f);
+                lo[i] = (uint16_t)pack_bf16(h[i] - bf16_bits_to_f32(hi[i]), 0.0f);
+            }
+            uint16_t* to_hi = reinterpret_cast<uint16_t*>(ws + L.hi) + at;
+            uint16_t* to_lo = reinterpret_cast<uint16_t*>(ws + L.lo) + at;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                to_hi[i] = hi[i];
+                to_lo[i] = lo[i];
+            }
         }
         __syncthreads();
     }
 }
 
-// Down projection: 64 rows of the hidden size, one fp32 row of it per pair.
-__global__ __launch_bounds__(256) void moe_down_kernel(MoeArgs a, MoeLayout L) {
-    __shared__ __align__(16) float s_acc[4][kTiles][256];
+// Down projection: one fp32 row of the hidden size per pair.
+template <int NT>
+__global__ __launch_bounds__(256, 4) void moe_down_kernel(MoeArgs a, MoeLayout L) {
+    __shared__ __align__(16) float s_sums[4][NT][256];
+    __shared__ int s_token[kMaxTokens], s_pair[kMaxTokens];
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-    const int idx = blockIdx.y;
-    if (idx >= reinterpret_cast<const MoePlan*>(ws)->active) return;
-    const int e = reinterpret_cast<const int*>(ws + L.experts)[idx];
-    const int base = reinterpret_cast<const int*>(ws + L.base)[idx];
-    const int count = __popcll(reinterpret_cast<const uint64_t*>(ws + L.mask)[idx]);
-
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const Chosen e = choose(a, L, blockIdx.y, s_token, s_pair);
+    if (e.expert < 0) return;
+    __syncthreads();
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, kq = lane >> 4;
-    const int64_t row0 = (int64_t)blockIdx.x * 64;
-    const uint8_t* w0 = a.w_down + e * a.w_down_stride + (row0 + r) * a.ldw_down + 16 * kq;
-    const uint8_t* w[kTiles] = {w0, w0 + 16 * a.ldw_down, w0 + 32 * a.ldw_down, w0 + 48 * a.ldw_down};
-    const float* s = a.s_down + e * a.s_down_stride + (row0 >> 7) * a.lds_down;
-
-    for (int t0 = 0; t0 < count; t0 += 16) {
-        const int64_t from = (int64_t)(base + t0 + (t0 + r < count ? r : 0)) * a.inner + 16 * kq;
-        const uint16_t* h[2] = {reinterpret_cast<const uint16_t*>(ws + L.hi) + from,
-                                reinterpret_cast<const uint16_t*>(ws + L.lo) + from};
-        v4f acc[kTiles];
-        multiply<2>(acc, w, h, s, s, (int)(a.inner >> 7), wave);
-        put_sums(s_acc, acc, wave, r, kq);
-        __syncthreads();
-        const int c = threadIdx.x & 63;  // row of the hidden size
-        for (int tok = threadIdx.x >> 6; tok < 16 && t0 + tok < count; tok += 4) {
-            const float v = sum_waves(s_acc, c >> 4, tok * 16 + (c & 15));
-            reinterpret_cast<float*>(ws + L.parts)[(int64_t)(base + t0 + tok) * a.hidden + row0 + c] = v;
-        }
+    constexpr int kRows = 16 * NT;
+    const int64_t row0 = (int64_t)blockIdx.x * kRows;
+    Operands<NT, 2> o;
+    const uint8_t* w = a.w_down + e.expert * a.w_down_stride + row0 * a.ldw_down;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) o.w[t] = w + 16 * t * a.ldw_down;
+    o.row_offset = (uint32_t)(r * a.ldw_down) + 16 * kq;
+    o.s[0] = o.s[1] = a.s_down + e.expert * a.s_down_stride + (row0 >> 7) * a.lds_down;
+    for (int t0 = 0; t0 < e.count; t0 += 16) {
+        o.live = t0 + r < e.count;
+        const int64_t from = (int64_t)(o.live ? s_pair[t0 + r] : 0) * a.inner + 8 * kq;
+        o.b[0] = reinterpret_cast<const uint16_t*>(ws + L.hi) + from;
+        o.b[1] = reinterpret_cast<const uint16_t*>(ws + L.lo) + from;
+        multiply<NT, 2>(s_sums, o, (int)(a.inner >> 7), wave);
+        const int c = threadIdx.x % kRows;
+        for (int tok = threadIdx.x / kRows; tok < 16 && t0 + tok < e.count; tok += 256 / kRows)
+            reinterpret_cast<float*>(ws + L.parts)[s_pair[t0 + tok] * a.hidden + row0 + c] =
+                sum_waves<NT>(s_sums, c >> 4, tok * 16 + (c & 15));
         __syncthreads();
     }
 }
@@ -391,16 +394,13 @@ __global__ __launch_bounds__(256) void moe_down_kernel(MoeArgs a, MoeLayout L) {
 // A token's pairs added in the order of their experts.
 __global__ __launch_bounds__(256) void moe_join_kernel(MoeArgs a, MoeLayout L) {
     const uint8_t* ws = static_cast<const uint8_t*>(a.workspace);
-    const MoePlan* plan = reinterpret_cast<const MoePlan*>(ws);
     const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int t = blockIdx.y;
     if (c >= a.hidden) return;
-    const int* pair = reinterpret_cast<const int*>(ws + L.pair) + t * kMaxTopK;
-    const float* parts = reinterpret_cast<const float*>(ws + L.parts) + c;
-    const int n = plan->count[t];
-    float v = 0.0f;
-    for (int i = 0; i < n; ++i) v += parts[pair[i] * a.hidden];
-    if ((plan->nan_mask >> t) & 1) v = __builtin_nanf("");
+    const float* parts = reinterpret_cast<const float*>(ws + L.parts) + (int64_t)t * a.top_k * a.hidden + c;
+    const int n = reinterpret_cast<const int*>(ws + L.count)[t];
+    float v = n < 0 ? __builtin_nanf("") : 0.0f;
+    for (int i = 0; i < n; ++i) v += parts[i * a.hidden];
     if (a.y_dtype == kDtypeBF16)
         static_cast<uint16_t*>(a.y)[t * a.ldy + c] = (uint16_t)pack_bf16(v, 0.0f);
     else
@@ -414,30 +414,30 @@ namespace {
 
 MoeLayout moe_layout(int64_t tokens, int64_t hidden, int64_t inner, int experts, int top_k) {
     MoeLayout L;
-    L.pairs = tokens * std::min(top_k, experts);
-    L.slots = (int)std::min<int64_t>(experts, L.pairs);
+    const int64_t pairs = tokens * top_k;
+    L.slots = (int)std::min<int64_t>(experts, pairs);
+    L.words = (experts + 63) / 64;
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         const int64_t here = at;
         at += (bytes + 255) / 256 * 256;
         return here;
     };
-    take(sizeof(MoePlan));
-    L.experts = take(4 * (int64_t)L.slots);
-    L.base = take(4 * (int64_t)L.slots);
-    L.mask = take(8 * (int64_t)L.slots);
-    L.prob = take(4 * L.pairs);
-    L.pair = take(4 * tokens * kMaxTopK);
-    L.hi = take(2 * L.pairs * inner);
-    L.lo = take(2 * L.pairs * inner);
-    L.parts = take(4 * L.pairs * hidden);
+    L.sets = take(8 * tokens * L.words);
+    L.count = take(4 * tokens);
+    L.prob = take(4 * pairs);
+    L.hi = take(2 * pairs * inner);
+    L.lo = take(2 * pairs * inner);
+    L.parts = take(4 * pairs * hidden);
     L.total = at;
     return L;
 }
 
-template <int PL>
-void launch_route(const MoeArgs& a, const MoeLayout& L, hipStream_t st) {
-    hipLaunchKernelGGL(moe_route_kernel<PL>, dim3(1), dim3(64 * std::min(kRouteWaves, a.tokens)), 0, st, a, L);
+template <int NT>
+void launch_products(const MoeArgs& a, const MoeLayout& L, hipStream_t st) {
+    const unsigned slots = (unsigned)L.slots;
+    hipLaunchKernelGGL(moe_up_kernel<NT>, dim3((unsigned)(a.inner / (8 * NT)), slots), dim3(256), 0, st, a, L);
+    hipLaunchKernelGGL(moe_down_kernel<NT>, dim3((unsigned)(a.hidden / (16 * NT)), slots), dim3(256), 0, st, a, L);
 }
 
 }  // namespace
@@ -448,11 +448,11 @@ int64_t moe_decode_bytes(int64_t tokens, int64_t hidden, int64_t inner, int expe
 
 hipError_t launch_moe_decode(const MoeArgs& a, hipStream_t st) {
     const MoeLayout L = moe_layout(a.tokens, a.hidden, a.inner, a.experts, a.top_k);
-    if (a.experts <= 64) launch_route<1>(a, L, st);
-    else if (a.experts <= 256) launch_route<4>(a, L, st);
-    else launch_route<kMaxExperts / 64>(a, L, st);
-    hipLaunchKernelGGL(moe_up_kernel, dim3((unsigned)(a.inner / 32), (unsigned)L.slots), dim3(256), 0, st, a, L);
-    hipLaunchKernelGGL(moe_down_kernel, dim3((unsigned)(a.hidden / 64), (unsigned)L.slots), dim3(256), 0, st, a, L);
+    const dim3 waves((unsigned)a.tokens);
+    if (a.experts <= 64) hipLaunchKernelGGL(moe_route_kernel<1>, waves, dim3(64), 0, st, a, L);
+    else if (a.experts <= 256) hipLaunchKernelGGL(moe_route_kernel<4>, waves, dim3(64), 0, st, a, L);
+    else hipLaunchKernelGGL(moe_route_kernel<kMaxExperts / 64>, waves, dim3(64), 0, st, a, L);
+    launch_products<4>(a, L, st);
     hipLaunchKernelGGL(moe_join_kernel, dim3((unsigned)((a.hidden + 255) / 256), (unsigned)a.tokens), dim3(256), 0, st,
                        a, L);
     return hipGetLastError();
