@@ -24,7 +24,14 @@ namespace fp8q {
 
 namespace {
 
-__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+// 1 / (1 + exp(-x)) from the hardware's 2^p and reciprocal, each good to a
+// unit in the last place; with the rounding of p = -x log2(e) the relative
+// error stays below (5 + 1.3 |x|) 2^-24.  exp(-x) beyond the largest fp32
+// gives 0.  (Against expf and a division, or a corrected p and a Newton step:
+// 7 to 25 instructions fewer per element, in kernels that issue 35 to 55.)
+__device__ __forceinline__ float sigmoid(float x) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -0x1.715476p+0f));
+}
 
 struct SwigluPoint {
     float h, dg, du;
@@ -37,7 +44,7 @@ __device__ __forceinline__ SwigluPoint swiglu_point(float g, float u, float dh) 
     SwigluPoint p;
     p.h = a * u;
     p.du = dh * a;
-    p.dg = dh * u * sg * (1.0f + g * (1.0f - sg));
+    p.dg = dh * u * sg * __builtin_fmaf(g, 1.0f - sg, 1.0f);
     return p;
 }
 
@@ -58,49 +65,120 @@ __device__ __forceinline__ void decode8(uint2 w, float s, float v[8]) {
     for (int k = 0; k < 8; ++k) v[k] *= s;
 }
 
-__device__ __forceinline__ uint32_t amax8(const float v[8]) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) m = max(m, abs_bits(v[k]));
-    return m;
+// Magnitude maxima: the absolute value is an operand modifier and three
+// operands go into one maximum.  The bits of the result order like the number.
+__device__ __forceinline__ float max_abs3(float m, float a, float b) {
+    return __builtin_fmaxf(__builtin_fmaxf(m, __builtin_fabsf(a)), __builtin_fabsf(b));
 }
 
-// One 1x128 tile of 16 lanes with eight values each: scale and codes of row
-// `row`, columns c .. c+7 of this lane.
-template <bool POW2>
-__device__ __forceinline__ void put_tile(const float v[8], int64_t row, int64_t c, int64_t cols, uint8_t* q,
-                                         int64_t ldq, float* s, int64_t lds) {
-    const TileScale t = make_scale_mode<POW2>(row_max_u32(amax8(v)));
-    if (c >= cols) return;
-    if ((threadIdx.x & 15) == 0) s[(c >> 7) * lds + row] = t.s;
-    const uint32_t w0 = encode4_any<POW2>(v[0], v[1], v[2], v[3], t);
-    const uint32_t w1 = encode4_any<POW2>(v[4], v[5], v[6], v[7], t);
-    store8(q + row * ldq, c, cols, w0, w1);
+__device__ __forceinline__ uint32_t amax8(const float v[8]) {
+    float m = __builtin_fmaxf(__builtin_fabsf(v[0]), __builtin_fabsf(v[1]));
+#pragma unroll
+    for (int k = 2; k < 8; k += 2) m = max_abs3(m, v[k], v[k + 1]);
+    return __float_as_uint(m);
+}
+
+// Byte of 16-token unit `unit` of column `ch` in a transposed 128x128 tile of
+// codes.  Units are XOR-ed with the column's group of eight, and the columns
+// of the upper half trade places with their neighbours, so that the 16 column
+// groups that a wave writes at once fall into different LDS banks.
+__device__ __forceinline__ int tile_place(int ch, int unit) {
+    return 128 * (ch ^ (ch >> 6)) + 16 * (unit ^ ((ch >> 3) & 7));
 }
 
 }  // namespace
 
 // ----------------------------------------------------------------------------
-// Forward: a wave per row and 512 columns, eight columns per lane.
+// Forward.  A work-group takes a 512-column segment of W*R rows, a wave R of
+// them, a lane eight columns of each, so a 16-lane DPP row holds one tile of
+// h, g and u for every row.  One lane computes a tile's scale and passes it
+// to the others through LDS.  Segments of one group of rows are dispatched
+// back to back (whole rows stream).
 // ----------------------------------------------------------------------------
-template <typename T, bool POW2, bool KEEP>
-__global__ __launch_bounds__(256) void swiglu_quantize_kernel(SwigluArgs a) {
-    const int lane = threadIdx.x & 63;
-    const int64_t row = ((int64_t)blockIdx.z * 65535 + blockIdx.y) * 4 + (threadIdx.x >> 6);
-    if (row >= a.rows) return;
-    const int64_t c = (int64_t)blockIdx.x * 512 + 8 * lane;
-    Raw8<T> raw;
-    float g[8], u[8], h[8];
-    load_row8(raw, static_cast<const T*>(a.g) + row * a.ldgu, c, a.cols, false);
-    raw.values(g);
-    load_row8(raw, static_cast<const T*>(a.u) + row * a.ldgu, c, a.cols, false);
-    raw.values(u);
+template <typename T, int W, int R, bool POW2, bool KEEP>
+__global__ __launch_bounds__(64 * W) void swiglu_quantize_kernel(SwigluArgs a) {
+    constexpr int M = KEEP ? 3 : 1;  // h, and g and u
+    static_assert(M * R <= 16, "a lane of the DPP row for each tile");
+    __shared__ __align__(16) float2 s_sr[W][4][M * R];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane & 15;
+    const int64_t row0 = (((int64_t)blockIdx.z * 65535 + blockIdx.y) * W + wave) * R;
+    if (row0 >= a.rows) return;
+    const int64_t seg = (int64_t)blockIdx.x * 512, c = seg + 8 * lane;
+    const bool full = seg + 512 <= a.cols && row0 + R <= a.rows;
+    const T* gp = static_cast<const T*>(a.g) + row0 * a.ldgu;
+    const T* up = static_cast<const T*>(a.u) + row0 * a.ldgu;
+    Raw8<T> rg[R], ru[R];
+    if (full) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) h[k] = g[k] * sigmoid(g[k]) * u[k];
-    put_tile<POW2>(h, row, c, a.cols, a.qh, a.ldqh, a.sh, a.ldsh);
-    if constexpr (KEEP) {
-        put_tile<POW2>(g, row, c, a.cols, a.qg, a.ldq, a.sg, a.lds);
-        put_tile<POW2>(u, row, c, a.cols, a.qu, a.ldq, a.su, a.lds);
+        for (int i = 0; i < R; ++i) {
+            rg[i].load_full(gp + i * a.ldgu + c);
+            ru[i].load_full(up + i * a.ldgu + c);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            rg[i].zero();
+            ru[i].zero();
+            if (row0 + i < a.rows) {
+                load_row8(rg[i], gp + i * a.ldgu, c, a.cols, false);
+                load_row8(ru[i], up + i * a.ldgu, c, a.cols, false);
+            }
+        }
+    }
+    float h[R][8];
+    uint32_t mine = 0;  // lane R*m + i of the DPP row: maximum of row i of h, g or u
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        float g[8], u[8];
+        rg[i].values(g);
+        ru[i].values(u);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) h[i][k] = g[k] * sigmoid(g[k]) * u[k];
+        const uint32_t amax[3] = {amax8(h[i]), rg[i].amax_bits(), ru[i].amax_bits()};
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            const uint32_t x = row_max_u32(amax[m]);
+            mine = sub == R * m + i ? x : mine;
+        }
+    }
+    bool my_fast = true;
+    if (sub < M * R) {
+        const TileScale t = make_scale_mode<POW2>(mine);
+        s_sr[wave][lane >> 4][sub] = make_float2(t.s, t.r);
+        my_fast = t.fast;
+        const int64_t chunk = 4 * (int64_t)blockIdx.x + (lane >> 4), row = row0 + sub % R;
+        if (row < a.rows && chunk * 128 < a.cols) {
+            if (!KEEP || sub < R) a.sh[chunk * a.ldsh + row] = t.s;
+            else (sub < 2 * R ? a.sg : a.su)[chunk * a.lds + row] = t.s;
+        }
+    }
+    wave_lds_sync();
+    const bool fast = full && wave_all(my_fast);
+    if (!fast && c >= a.cols) return;
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+        uint8_t* q = m == 0 ? a.qh : m == 1 ? a.qg : a.qu;
+        const int64_t ldq = m == 0 ? a.ldqh : a.ldq;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            float v[8];
+            if (m == 0) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = h[i][k];
+            } else {
+                (m == 1 ? rg[i] : ru[i]).values(v);
+            }
+            const float2 sr = s_sr[wave][lane >> 4][R * m + i];
+            uint8_t* to = q + (row0 + i) * ldq;
+            if (fast) {
+                *reinterpret_cast<uint2*>(to + c) = make_uint2(encode4_sr<POW2>(v[0], v[1], v[2], v[3], sr.x, sr.y),
+                                                               encode4_sr<POW2>(v[4], v[5], v[6], v[7], sr.x, sr.y));
+            } else if (row0 + i < a.rows) {
+                const TileScale t = scale_from(sr.x, sr.y);
+                store8(to, c, a.cols, encode4_any<POW2>(v[0], v[1], v[2], v[3], t),
+                       encode4_any<POW2>(v[4], v[5], v[6], v[7], t));
+            }
+        }
     }
 }
 
@@ -138,34 +216,60 @@ __global__ __launch_bounds__(256) void swiglu_backward_kernel(SwigluBackwardArgs
 // A work-group of 8 waves takes 128 rows x 128 columns: thread t has columns
 // 8*(t%16) .. +7 of rows 4*(t/16) .. +3, so a row's tile maximum is a DPP row
 // maximum and a column's goes across the lanes of a wave and then through
-// LDS.  The codes of the 128x1 tiles are transposed in LDS, whose 16-byte
-// units are XOR-swizzled by ((column >> 3) & 7).
+// LDS.  The codes of the 128x1 tiles are transposed in LDS (tile_place).
 // ----------------------------------------------------------------------------
 template <typename T, bool POW2>
-__global__ __launch_bounds__(512) void swiglu_backward_quantize_kernel(SwigluBackwardArgs a) {
-    __shared__ uint32_t s_part[3][8][128];
-    __shared__ float2 s_sr[3][128];
+__global__ __launch_bounds__(512, 4) void swiglu_backward_quantize_kernel(SwigluBackwardArgs a) {
+    constexpr int kRows = 4;                                   // rows per thread
+    __shared__ __align__(16) float2 s_row[8][4][2 * kRows];    // [wave][row group][dg rows, du rows]: s, 1/s
+    __shared__ __align__(16) float2 s_col[3][8][16];           // [column % 8][column / 8]
+    __shared__ int s_slow;                                     // some column's scale needs the exact division
+    // first the column maxima [3][row group][column], then the transposed codes
     __shared__ __align__(16) uint8_t s_tile[3][128 * 128];
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    uint32_t(*s_part)[32][128] = reinterpret_cast<uint32_t(*)[32][128]>(&s_tile[0][0]);
+    static_assert(sizeof(s_tile) == 3 * 32 * 128 * 4, "the maxima fill the tiles");
+    const int t = threadIdx.x, wave = t >> 6;
     const int cg = t & 15, rg = t >> 4;
     const int64_t r0 = (int64_t)blockIdx.y * 128, c0 = (int64_t)blockIdx.x * 128;
-    const int64_t c = c0 + 8 * cg;
+    const int64_t c = c0 + 8 * cg, row = r0 + kRows * rg;
+    const bool full = r0 + 128 <= a.rows && c0 + 128 <= a.cols;
 
-    float v[3][4][8];  // dg, du, h
+    Raw8<T> raw[kRows];
+    uint2 qg[kRows], qu[kRows];
+    float sg[kRows], su[kRows];
+    if (full) {  // every load goes out before any arithmetic
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t r = r0 + 4 * rg + i;
-        float g[8], u[8], dh[8];
-        if (r < a.rows && c < a.cols) {
-            Raw8<T> raw;
-            load_row8(raw, static_cast<const T*>(a.dh) + r * a.lddh, c, a.cols, false);
-            raw.values(dh);
-            decode8(load_codes8(a.qg + r * a.ldq, c, a.cols), a.sg[(c >> 7) * a.lds + r], g);
-            decode8(load_codes8(a.qu + r * a.ldq, c, a.cols), a.su[(c >> 7) * a.lds + r], u);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) g[k] = u[k] = dh[k] = 0.0f;
+        for (int i = 0; i < kRows; ++i) {
+            qg[i] = *reinterpret_cast<const uint2*>(a.qg + (row + i) * a.ldq + c);
+            qu[i] = *reinterpret_cast<const uint2*>(a.qu + (row + i) * a.ldq + c);
+            raw[i].load_full(static_cast<const T*>(a.dh) + (row + i) * a.lddh + c);
+            sg[i] = a.sg[blockIdx.x * a.lds + row + i];
+            su[i] = a.su[blockIdx.x * a.lds + row + i];
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            if (row + i < a.rows && c < a.cols) {
+                qg[i] = load_codes8(a.qg + (row + i) * a.ldq, c, a.cols);
+                qu[i] = load_codes8(a.qu + (row + i) * a.ldq, c, a.cols);
+                load_row8(raw[i], static_cast<const T*>(a.dh) + (row + i) * a.lddh, c, a.cols, false);
+                sg[i] = a.sg[blockIdx.x * a.lds + row + i];
+                su[i] = a.su[blockIdx.x * a.lds + row + i];
+            } else {
+                qg[i] = qu[i] = make_uint2(0, 0);
+                raw[i].zero();
+                sg[i] = su[i] = 0.0f;
+            }
+        }
+    }
+    float v[3][kRows][8];  // dg, du, h
+    uint32_t mine = 0;     // lane 4*m + i of a row group: maximum of row i of dg (m = 0) or du
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        float g[8], u[8], dh[8];
+        decode8(qg[i], sg[i], g);
+        decode8(qu[i], su[i], u);
+        raw[i].values(dh);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const SwigluPoint p = swiglu_point(g[k], u[k], dh[k]);
@@ -173,25 +277,57 @@ __global__ __launch_bounds__(512) void swiglu_backward_quantize_kernel(SwigluBac
             v[1][i][k] = p.du;
             v[2][i][k] = p.h;
         }
-    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t r = r0 + 4 * rg + i;
-        if (r < a.rows) {  // uniform over the 16 lanes of the tile
-            put_tile<POW2>(v[0][i], r, c, a.cols, a.qdg, a.ldqd, a.sdg, a.ldsd);
-            put_tile<POW2>(v[1][i], r, c, a.cols, a.qdu, a.ldqd, a.sdu, a.ldsd);
+        for (int m = 0; m < 2; ++m) {
+            const uint32_t x = row_max_u32(amax8(v[m][i]));
+            mine = cg == kRows * m + i ? x : mine;
         }
     }
 #pragma unroll
     for (int m = 0; m < 3; ++m) {
+        float x[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            uint32_t x = 0;
+        for (int k = 0; k < 8; ++k)
+            x[k] = max_abs3(__builtin_fmaxf(__builtin_fabsf(v[m][0][k]), __builtin_fabsf(v[m][1][k])), v[m][2][k], v[m][3][k]);
+        float4* part = reinterpret_cast<float4*>(&s_part[m][rg][8 * cg]);
+        part[0] = make_float4(x[0], x[1], x[2], x[3]);
+        part[1] = make_float4(x[4], x[5], x[6], x[7]);
+    }
+    if (t == 0) s_slow = 0;
+    // 1x128 tiles: scales by one lane each, then the codes
+    bool my_fast = true;
+    if (cg < 2 * kRows) {
+        const TileScale ts = make_scale_mode<POW2>(mine);
+        s_row[wave][rg & 3][cg] = make_float2(ts.s, ts.r);
+        my_fast = ts.fast;
+        const int64_t r = row + (cg & (kRows - 1));
+        if (r < a.rows) (cg < kRows ? a.sdg : a.sdu)[blockIdx.x * a.ldsd + r] = ts.s;
+    }
+    wave_lds_sync();
+    if (full && wave_all(my_fast)) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x = max(x, abs_bits(v[m][i][k]));
-            x = max(x, (uint32_t)__shfl_xor((int)x, 16));
-            x = max(x, (uint32_t)__shfl_xor((int)x, 32));
-            if (lane < 16) s_part[m][wave][8 * cg + k] = x;
+        for (int m = 0; m < 2; ++m) {
+            uint8_t* q = (m == 0 ? a.qdg : a.qdu) + row * a.ldqd + c;
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                const float2 sr = s_row[wave][rg & 3][kRows * m + i];
+                const float* x = v[m][i];
+                *reinterpret_cast<uint2*>(q + i * a.ldqd) = make_uint2(
+                    encode4_sr<POW2>(x[0], x[1], x[2], x[3], sr.x, sr.y), encode4_sr<POW2>(x[4], x[5], x[6], x[7], sr.x, sr.y));
+            }
+        }
+    } else if (c < a.cols) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                if (row + i >= a.rows) break;
+                const float2 sr = s_row[wave][rg & 3][kRows * m + i];
+                const TileScale ts = scale_from(sr.x, sr.y);
+                const float* x = v[m][i];
+                store8((m == 0 ? a.qdg : a.qdu) + (row + i) * a.ldqd, c, a.cols,
+                       encode4_any<POW2>(x[0], x[1], x[2], x[3], ts), encode4_any<POW2>(x[4], x[5], x[6], x[7], ts));
+            }
         }
     }
     __syncthreads();
@@ -199,41 +335,43 @@ __global__ __launch_bounds__(512) void swiglu_backward_quantize_kernel(SwigluBac
         const int m = t >> 7, ch = t & 127;
         uint32_t x = 0;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) x = max(x, s_part[m][w][ch]);
+        for (int g = 0; g < 32; ++g) x = max(x, s_part[m][g][ch]);
         const TileScale ts = make_scale_mode<POW2>(x);
-        s_sr[m][ch] = make_float2(ts.s, ts.r);
+        s_col[m][ch & 7][ch >> 3] = make_float2(ts.s, ts.r);
+        if (!ts.fast) s_slow = 1;
         float* st = m == 0 ? a.sdgt : m == 1 ? a.sdut : a.sht;
         const int64_t ldst = m == 2 ? a.ldsht : a.ldst;
-        if (c0 + ch < a.cols) st[(r0 >> 7) * ldst + c0 + ch] = ts.s;
+        if (c0 + ch < a.cols) st[blockIdx.y * ldst + c0 + ch] = ts.s;
     }
     __syncthreads();
+    const bool fast = s_slow == 0;
 #pragma unroll
     for (int m = 0; m < 3; ++m) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const int ch = 8 * cg + k;
-            const float2 sr = s_sr[m][ch];
-            const uint32_t w = encode4_any<POW2>(v[m][0][k], v[m][1][k], v[m][2][k], v[m][3][k], scale_from(sr.x, sr.y));
-            const int unit = (rg >> 2) ^ (cg & 7);
-            *reinterpret_cast<uint32_t*>(s_tile[m] + ch * 128 + 16 * unit + 4 * (rg & 3)) = w;
+            const float2 sr = s_col[m][k][cg];
+            const uint32_t w =
+                fast ? encode4_sr<POW2>(v[m][0][k], v[m][1][k], v[m][2][k], v[m][3][k], sr.x, sr.y)
+                     : encode4_any<POW2>(v[m][0][k], v[m][1][k], v[m][2][k], v[m][3][k], scale_from(sr.x, sr.y));
+            *reinterpret_cast<uint32_t*>(s_tile[m] + tile_place(8 * cg + k, rg >> 2) + 4 * (rg & 3)) = w;
         }
     }
     __syncthreads();
-    // thread t: column 64*j + t/8, 16 tokens of physical unit t%8
+    // thread t: columns t/8 and t/8 + 64, tokens 16*(t%8) .. +15 of the tile
+    const int unit = t & 7;
+    const int64_t tok = r0 + 16 * unit;
 #pragma unroll
     for (int m = 0; m < 3; ++m) {
         uint8_t* qt = m == 0 ? a.qdgt : m == 1 ? a.qdut : a.qht;
         const int64_t ldqt = m == 2 ? a.ldqht : a.ldqt;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int ch = 64 * j + (t >> 3), unit = t & 7;
-            const uint4 val = *reinterpret_cast<const uint4*>(s_tile[m] + ch * 128 + 16 * unit);
-            const int64_t tok = r0 + 16 * (unit ^ ((ch >> 3) & 7));
-            if (c0 + ch >= a.cols) continue;
+            const int ch = 64 * j + (t >> 3);
+            const uint4 val = *reinterpret_cast<const uint4*>(s_tile[m] + tile_place(ch, unit));
             uint8_t* dst = qt + (c0 + ch) * ldqt + tok;
-            if (tok + 16 <= a.rows) {
+            if (full || (c0 + ch < a.cols && tok + 16 <= a.rows)) {
                 *reinterpret_cast<uint4*>(dst) = val;
-            } else {
+            } else if (c0 + ch < a.cols) {
                 const uint32_t wv[4] = {val.x, val.y, val.z, val.w};
 #pragma unroll
                 for (int b = 0; b < 16; ++b)
@@ -248,18 +386,20 @@ __global__ __launch_bounds__(512) void swiglu_backward_quantize_kernel(SwigluBac
 // ----------------------------------------------------------------------------
 namespace {
 
-dim3 row_grid(int64_t rows, int64_t cols) {
-    const int64_t groups = (rows + 3) / 4;
+dim3 row_grid(int64_t rows, int64_t cols, int rows_per_group) {
+    const int64_t groups = (rows + rows_per_group - 1) / rows_per_group;
     return dim3((unsigned)((cols + 511) / 512), (unsigned)std::min<int64_t>(groups, 65535),
                 (unsigned)((groups + 65534) / 65535));
 }
 
 template <typename T, bool POW2>
 void launch_forward(const SwigluArgs& a, hipStream_t st) {
+    constexpr int W = 4, R = 2;  // 8 x 2 and 4 x 4 run alike, one row per wave 10 % slower
+    const dim3 grid = row_grid(a.rows, a.cols, W * R);
     if (a.qg)
-        hipLaunchKernelGGL((swiglu_quantize_kernel<T, POW2, true>), row_grid(a.rows, a.cols), dim3(256), 0, st, a);
+        hipLaunchKernelGGL((swiglu_quantize_kernel<T, W, R, POW2, true>), grid, dim3(64 * W), 0, st, a);
     else
-        hipLaunchKernelGGL((swiglu_quantize_kernel<T, POW2, false>), row_grid(a.rows, a.cols), dim3(256), 0, st, a);
+        hipLaunchKernelGGL((swiglu_quantize_kernel<T, W, R, POW2, false>), grid, dim3(64 * W), 0, st, a);
 }
 
 template <typename T>
@@ -285,7 +425,7 @@ hipError_t launch_swiglu_quantize(const SwigluArgs& a, hipStream_t st) {
 }
 
 hipError_t launch_swiglu_backward(const SwigluBackwardArgs& a, hipStream_t st) {
-    const dim3 grid = row_grid(a.rows, a.cols);
+    const dim3 grid = row_grid(a.rows, a.cols, 4);
     if (a.dtype == kDtypeBF16)
         hipLaunchKernelGGL((swiglu_backward_kernel<uint16_t>), grid, dim3(256), 0, st, a);
     else
