@@ -230,7 +230,13 @@ __global__ __launch_bounds__(512, 4) void swiglu_backward_quantize_kernel(Swiglu
     static_assert(sizeof(s_tile) == 3 * 32 * 128 * 4, "the maxima fill the tiles");
     const int t = threadIdx.x, wave = t >> 6;
     const int cg = t & 15, rg = t >> 4;
-    const int64_t r0 = (int64_t)blockIdx.y * 128, c0 = (int64_t)blockIdx.x * 128;
+    // Eight row tiles of a column tile one after the other: both the rows and
+    // the transposed rows are then written in runs (7 % faster at 8192x7168
+    // than whole rows of tiles or whole columns).
+    const uint32_t band = blockIdx.y / 8, height = min(8u, gridDim.y - 8 * band);
+    const uint32_t in_band = blockIdx.y % 8 * gridDim.x + blockIdx.x;
+    const int64_t tile_c = in_band / height, tile_r = 8 * band + in_band % height;
+    const int64_t r0 = tile_r * 128, c0 = tile_c * 128;
     const int64_t c = c0 + 8 * cg, row = r0 + kRows * rg;
     const bool full = r0 + 128 <= a.rows && c0 + 128 <= a.cols;
 
@@ -240,11 +246,11 @@ __global__ __launch_bounds__(512, 4) void swiglu_backward_quantize_kernel(Swiglu
     if (full) {  // every load goes out before any arithmetic
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            qg[i] = *reinterpret_cast<const uint2*>(a.qg + (row + i) * a.ldq + c);
-            qu[i] = *reinterpret_cast<const uint2*>(a.qu + (row + i) * a.ldq + c);
+            qg[i] = load8_nt(a.qg + (row + i) * a.ldq + c);
+            qu[i] = load8_nt(a.qu + (row + i) * a.ldq + c);
             raw[i].load_full(static_cast<const T*>(a.dh) + (row + i) * a.lddh + c);
-            sg[i] = a.sg[blockIdx.x * a.lds + row + i];
-            su[i] = a.su[blockIdx.x * a.lds + row + i];
+            sg[i] = a.sg[tile_c * a.lds + row + i];
+            su[i] = a.su[tile_c * a.lds + row + i];
         }
     } else {
 #pragma unroll
@@ -253,8 +259,8 @@ __global__ __launch_bounds__(512, 4) void swiglu_backward_quantize_kernel(Swiglu
                 qg[i] = load_codes8(a.qg + (row + i) * a.ldq, c, a.cols);
                 qu[i] = load_codes8(a.qu + (row + i) * a.ldq, c, a.cols);
                 load_row8(raw[i], static_cast<const T*>(a.dh) + (row + i) * a.lddh, c, a.cols, false);
-                sg[i] = a.sg[blockIdx.x * a.lds + row + i];
-                su[i] = a.su[blockIdx.x * a.lds + row + i];
+                sg[i] = a.sg[tile_c * a.lds + row + i];
+                su[i] = a.su[tile_c * a.lds + row + i];
             } else {
                 qg[i] = qu[i] = make_uint2(0, 0);
                 raw[i].zero();
@@ -301,7 +307,7 @@ __global__ __launch_bounds__(512, 4) void swiglu_backward_quantize_kernel(Swiglu
         s_row[wave][rg & 3][cg] = make_float2(ts.s, ts.r);
         my_fast = ts.fast;
         const int64_t r = row + (cg & (kRows - 1));
-        if (r < a.rows) (cg < kRows ? a.sdg : a.sdu)[blockIdx.x * a.ldsd + r] = ts.s;
+        if (r < a.rows) (cg < kRows ? a.sdg : a.sdu)[tile_c * a.ldsd + r] = ts.s;
     }
     wave_lds_sync();
     if (full && wave_all(my_fast)) {
@@ -341,7 +347,7 @@ __global__ __launch_bounds__(512, 4) void swiglu_backward_quantize_kernel(Swiglu
         if (!ts.fast) s_slow = 1;
         float* st = m == 0 ? a.sdgt : m == 1 ? a.sdut : a.sht;
         const int64_t ldst = m == 2 ? a.ldsht : a.ldst;
-        if (c0 + ch < a.cols) st[blockIdx.y * ldst + c0 + ch] = ts.s;
+        if (c0 + ch < a.cols) st[tile_r * ldst + c0 + ch] = ts.s;
     }
     __syncthreads();
     const bool fast = s_slow == 0;
@@ -370,7 +376,7 @@ __global__ __launch_bounds__(512, 4) void swiglu_backward_quantize_kernel(Swiglu
             const uint4 val = *reinterpret_cast<const uint4*>(s_tile[m] + tile_place(ch, unit));
             uint8_t* dst = qt + (c0 + ch) * ldqt + tok;
             if (full || (c0 + ch < a.cols && tok + 16 <= a.rows)) {
-                *reinterpret_cast<uint4*>(dst) = val;
+                store16_nt(dst, val);
             } else if (c0 + ch < a.cols) {
                 const uint32_t wv[4] = {val.x, val.y, val.z, val.w};
 #pragma unroll

@@ -23,6 +23,18 @@ __device__ __forceinline__ uint4 load16(const void* p) {
     }
 }
 
+// 8-byte load and 16-byte store, marked non-temporal.
+__device__ __forceinline__ uint2 load8_nt(const void* p) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
+    return make_uint2(v[0], v[1]);
+}
+
+__device__ __forceinline__ void store16_nt(void* p, uint4 v) {
+    const u32x4 w = {v.x, v.y, v.z, v.w};
+    __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(p));
+}
+
 // Orders LDS traffic between the lanes of one wave: a wave's LDS operations
 // execute in program order, the fences keep the compiler from reordering them.
 __device__ __forceinline__ void wave_lds_sync() {
