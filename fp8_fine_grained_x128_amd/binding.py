@@ -265,7 +265,8 @@ def _check(status: int, what: str) -> None:
 
 
 def _stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+    """Handle of torch's current stream (the raw handle: a Stream object costs 3 us a call)."""
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -320,8 +321,9 @@ def _pad16(n: int) -> int:
 
 def _codes(rows: int, cols: int, device) -> torch.Tensor:
     """uint8 [rows][cols] with a 16-byte-multiple row stride."""
-    buf = torch.empty((rows, _pad16(max(cols, 1))), dtype=torch.uint8, device=device)
-    return buf[:, :cols]
+    ld = _pad16(max(cols, 1))
+    buf = torch.empty((rows, ld), dtype=torch.uint8, device=device)
+    return buf if ld == cols else buf[:, :cols]
 
 
 def _cdiv(a: int, b: int) -> int:
@@ -498,7 +500,9 @@ def grouped_gemm(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.T
 def _rows(rows: int, cols: int, dtype: torch.dtype, device) -> torch.Tensor:
     """[rows][cols] whose row stride is a multiple of 16 bytes."""
     per16 = 16 // dtype.itemsize
-    return torch.empty((rows, _cdiv(max(cols, 1), per16) * per16), dtype=dtype, device=device)[:, :cols]
+    ld = _cdiv(max(cols, 1), per16) * per16
+    buf = torch.empty((rows, ld), dtype=dtype, device=device)
+    return buf if ld == cols else buf[:, :cols]
 
 
 def _scales(groups: int, n: int, device) -> torch.Tensor:
@@ -615,12 +619,16 @@ class SwigluCheckpoint(NamedTuple):
     su: torch.Tensor
 
 
+def _half(both: torch.Tensor, offset: int, rows: int, cols: int) -> torch.Tensor:
+    return both.as_strided((rows, cols), (both.shape[1], 1), offset)
+
+
 def _pair(rows: int, cols: int, multiple: int, dtype: torch.dtype, device) -> Tuple[torch.Tensor, torch.Tensor]:
     """Two [rows][cols] halves with one row stride: side by side in one buffer if cols % multiple == 0, else in
     buffers of their own."""
     if cols % multiple == 0:
         both = torch.empty((rows, 2 * cols), dtype=dtype, device=device)
-        return both[:, :cols], both[:, cols:]
+        return _half(both, 0, rows, cols), _half(both, cols, rows, cols)
     return _rows(rows, cols, dtype, device), _rows(rows, cols, dtype, device)
 
 
@@ -628,7 +636,7 @@ def _stack(groups: int, n: int, dtype: torch.dtype, device) -> Tuple[torch.Tenso
     """Two [groups][n] halves, one below the other, row stride a multiple of 16 bytes for codes."""
     ld = n if dtype == torch.float32 else _pad16(max(n, 1))
     both = torch.empty((2 * groups, ld), dtype=dtype, device=device)
-    return both[:groups, :n], both[groups:, :n]
+    return _half(both, 0, groups, n), _half(both, groups * ld, groups, n)
 
 
 def swiglu_quantize(g: torch.Tensor, u: torch.Tensor, checkpoint: bool = True, scale_mode: int = FP8Q_SCALE_FP32
@@ -705,9 +713,9 @@ class SwigluGrads(NamedTuple):
             raise ValueError(f"gate_up: {cols} columns are not a multiple of 128")
         groups = self.sdgt.shape[0]
         return (self.qdg.as_strided((rows, 2 * cols), (2 * cols, 1)),
-                self.sdg.as_strided((2 * cols // 128, rows), (rows, 1)),
+                self.sdg.as_strided((2 * cols // 128, rows), (rows, 1), self.sdg.storage_offset()),
                 self.qdgt.as_strided((2 * cols, rows), (self.qdgt.stride(0), 1)),
-                self.sdgt.as_strided((groups, 2 * cols), (2 * cols, 1)))
+                self.sdgt.as_strided((groups, 2 * cols), (2 * cols, 1), self.sdgt.storage_offset()))
 
 
 def swiglu_backward_quantize(kept: SwigluCheckpoint, dh: torch.Tensor, scale_mode: int = FP8Q_SCALE_FP32
@@ -717,9 +725,13 @@ def swiglu_backward_quantize(kept: SwigluCheckpoint, dh: torch.Tensor, scale_mod
     _check_checkpoint("swiglu_backward_quantize", kept, dh)
     rows, cols = dh.shape
     dev, groups, tgroups = dh.device, _cdiv(cols, 128), _cdiv(rows, 128)
-    o = SwigluGrads(*_pair(rows, cols, 16, torch.uint8, dev), *_stack(groups, rows, torch.float32, dev),
-                    *_stack(cols, rows, torch.uint8, dev), *_pair(tgroups, cols, 1, torch.float32, dev),
-                    _codes(cols, rows, dev), _scales(tgroups, cols, dev))
+    ns, nt = groups * rows, tgroups * cols  # scales of one 1x128 and one 128x1 array
+    scales = torch.empty(2 * ns + 3 * nt, dtype=torch.float32, device=dev)
+    o = SwigluGrads(*_pair(rows, cols, 16, torch.uint8, dev), scales.as_strided((groups, rows), (rows, 1)),
+                    scales.as_strided((groups, rows), (rows, 1), ns), *_stack(cols, rows, torch.uint8, dev),
+                    scales.as_strided((tgroups, cols), (2 * cols, 1), 2 * ns),
+                    scales.as_strided((tgroups, cols), (2 * cols, 1), 2 * ns + cols), _codes(cols, rows, dev),
+                    scales.as_strided((tgroups, cols), (cols, 1), 2 * ns + 2 * nt))
     ldq = cols * 2 if cols % 16 == 0 else _ld(o.qdg)
     ldt = _pad16(max(rows, 1))
     _check(fp8q_swiglu_backward_quantize(*_checkpoint_args(kept, dh), o.qdg.data_ptr(), o.qdu.data_ptr(), ldq,
