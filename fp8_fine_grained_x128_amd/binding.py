@@ -556,11 +556,13 @@ def layernorm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Optio
             _check_vector("layernorm", name, w, cols, given[0].dtype)
     _on_device("layernorm", x, *given)
     dev = x.device
+    groups = _cdiv(cols, 128) if quantize else 0
     q = _codes(rows, cols, dev) if quantize else None
-    s = _scales(_cdiv(cols, 128), rows, dev) if quantize else None
     y = _rows(rows, cols, out_dtype, dev) if out_dtype is not None else None
-    mean = torch.empty(rows, dtype=torch.float32, device=dev) if kind == FP8Q_NORM_LAYER else None
-    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    small = torch.empty((groups + 2) * rows, dtype=torch.float32, device=dev)  # scales, rstd, mean
+    s = small.as_strided((groups, rows), (rows, 1)) if quantize else None
+    rstd = small.as_strided((rows,), (1,), groups * rows)
+    mean = small.as_strided((rows,), (1,), (groups + 1) * rows) if kind == FP8Q_NORM_LAYER else None
     _check(fp8q_layernorm(x.data_ptr(), _dtype_code(x), rows, cols, _ld(x), _ptr(gamma), _ptr(beta),
                           _dtype_code(given[0]) if given else FP8Q_F32, eps, kind, _ptr(y),
                           FP8Q_F32 if y is None else _dtype_code(y), 0 if y is None else _ld(y), _ptr(q),

@@ -13,9 +13,9 @@
 // (same page, passage on FP8-cached activations): the norm's result leaves
 // this kernel as those codes.  Every sum is fp32.
 //
-// One work-group owns a row and holds it in registers, so the mean, the sum
-// of squared deviations (a second pass, over registers: no cancellation) and
-// the result come from one read of the row.
+// A row is read once and stays in registers, so the mean, the sum of squared
+// deviations (a second pass over registers: no cancellation) and the result
+// come from one read.
 #include <algorithm>
 #include <type_traits>
 
@@ -67,166 +67,462 @@ __device__ __forceinline__ void block_sum(float v[N], float (*red)[16]) {
 }  // namespace
 
 // ----------------------------------------------------------------------------
-// Forward.  W waves hold I groups of eight columns per thread: thread t has
-// columns 8*(t + 64*W*i) .. +7, so 16 neighbouring lanes hold one 128-column
+// Forward.  A row belongs to W waves: thread t of them has columns
+// 8*(t + 64*W*i) .. +7 for i < I, so 16 neighbouring lanes hold one 128-column
 // tile and a tile maximum is a DPP row maximum.
 // ----------------------------------------------------------------------------
-template <typename T, int W, int I, bool LAYER, bool POW2>
-__global__ __launch_bounds__(64 * W) void layernorm_kernel(LayernormArgs a) {
-    __shared__ float s_red[2][1][16];
-    const int64_t cols = a.cols;
-    const float n = (float)cols;
-    int parity = 0;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        float v[I][8];
-        float sum[1] = {0.0f};
+
+// Makes the compiler decode a row's stored values again instead of keeping
+// them as fp32 from pass to pass (twice the registers for bf16).
+template <int I>
+__device__ __forceinline__ void forget(Raw8<uint16_t> (&raw)[I]) {
 #pragma unroll
-        for (int i = 0; i < I; ++i) {
-            Raw8<T> raw;
-            load_row8(raw, static_cast<const T*>(a.x) + row * a.ldx, 8 * (threadIdx.x + 64 * W * i), cols, false);
-            raw.values(v[i]);
+    for (int i = 0; i < I; ++i) {
+        opaque(raw[i].d.x);
+        opaque(raw[i].d.y);
+        opaque(raw[i].d.z);
+        opaque(raw[i].d.w);
+    }
+}
+template <int I>
+__device__ __forceinline__ void forget(Raw8<float> (&)[I]) {}
+
+// Sum of a row's deviations from `mean`, squared, times shrink^2.  Zeros
+// beyond the row's end stay out.
+template <typename T, int W, int I>
+__device__ __forceinline__ float sum_squares(const Raw8<T> (&raw)[I], int t, int64_t cols, float mean, float shrink) {
+    float sq = 0.0f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) sum[0] += v[i][k];
-        }
-        float mean = 0.0f;
-        if constexpr (LAYER) {
-            block_sum<W, 1>(sum, s_red[0]);
-            mean = sum[0] / n;
-        }
-        float sq[1] = {0.0f};
-#pragma unroll
-        for (int i = 0; i < I; ++i) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int64_t c = 8 * (threadIdx.x + 64 * W * i) + k;
-                v[i][k] = c < cols ? v[i][k] - mean : 0.0f;
-                sq[0] += (v[i][k] * a.shrink) * (v[i][k] * a.shrink);
-            }
-        }
-        block_sum<W, 1>(sq, s_red[LAYER ? 1 : parity]);
-        parity ^= 1;
-        const float rstd = 1.0f / sqrtf(sq[0] / (n * a.shrink * a.shrink) + a.eps);
-        if (threadIdx.x == 0) {
-            if (LAYER && a.mean) a.mean[row] = mean;
-            if (a.rstd) a.rstd[row] = rstd;
-        }
-#pragma unroll
-        for (int i = 0; i < I; ++i) {
-            const int64_t c = 8 * (threadIdx.x + 64 * W * i);
-            float gm[8], bt[8];
-            load_weights8(a.gamma, a.w_dtype, c, cols, 1.0f, gm);
-            load_weights8(a.beta, a.w_dtype, c, cols, 0.0f, bt);
-            uint32_t m = 0;
+    for (int i = 0; i < I; ++i) {
+        const int64_t c = 8 * (t + 64 * W * i);
+        float v[8];
+        raw[i].values(v);
+        if (c + 8 <= cols) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                v[i][k] = v[i][k] * rstd * gm[k] + bt[k];
-                if (c + k < cols) m = max(m, abs_bits(v[i][k]));
+                const float d = (v[k] - mean) * shrink;
+                sq = __builtin_fmaf(d, d, sq);
             }
-            if (a.y) {
-                if (a.y_dtype == kDtypeBF16)
-                    store_values8(static_cast<uint16_t*>(a.y) + row * a.ldy, c, cols, v[i]);
-                else
-                    store_values8(static_cast<float*>(a.y) + row * a.ldy, c, cols, v[i]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float d = c + k < cols ? (v[k] - mean) * shrink : 0.0f;
+                sq = __builtin_fmaf(d, d, sq);
             }
-            if (a.q) {
-                const TileScale t = make_scale_mode<POW2>(row_max_u32(m));
-                if (c < cols) {
-                    if ((threadIdx.x & 15) == 0) a.s[(c >> 7) * a.lds + row] = t.s;
-                    const uint32_t w0 = encode4_any<POW2>(v[i][0], v[i][1], v[i][2], v[i][3], t);
-                    const uint32_t w1 = encode4_any<POW2>(v[i][4], v[i][5], v[i][6], v[i][7], t);
-                    store8(a.q + row * a.ldq, c, cols, w0, w1);
-                }
-            }
+        }
+    }
+    return sq;
+}
+
+// Results of G groups of a row: y from the row's statistics, its values and
+// codes to memory.  One lane per tile computes the scale (lane i of a DPP row
+// for group i).  weights(i, gm, bt) gives the weights of group i.
+template <typename T, int W, int G, bool POW2, bool NT, typename Weights>
+__device__ __forceinline__ void finish_groups(const LayernormArgs& a, const Raw8<T>* raw, int i0, int t, int64_t row,
+                                              float mean, float rstd, const Weights& weights) {
+    const int sub = t & 15;
+    float v[G][8];
+    uint32_t mine = 0;
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+        const int64_t c = 8 * (t + 64 * W * (i0 + i));
+        float gm[8], bt[8];
+        weights(i0 + i, gm, bt);
+        raw[i].values(v[i]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[i][k] = __builtin_fmaf((v[i][k] - mean) * rstd, gm[k], bt[k]);
+        if (c + 8 > a.cols) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[i][k] = c + k < a.cols ? v[i][k] : 0.0f;
+        }
+        if (a.y && c < a.cols) {
+            if (a.y_dtype == kDtypeBF16)
+                store_values8<NT>(static_cast<uint16_t*>(a.y) + row * a.ldy, c, a.cols, v[i]);
+            else
+                store_values8<NT>(static_cast<float*>(a.y) + row * a.ldy, c, a.cols, v[i]);
+        }
+        if (a.q) {
+            const uint32_t m = row_max_u32(amax8(v[i]));
+            mine = sub == i ? m : mine;
+        }
+    }
+    if (!a.q) return;
+    const TileScale ts = make_scale_mode<POW2>(mine);
+    if (sub < G) {
+        const int64_t tile = 4 * W * (int64_t)(i0 + sub) + (t >> 4);
+        if (tile * 128 < a.cols) a.s[tile * a.lds + row] = ts.s;
+    }
+    const bool fast = wave_all(sub >= G || ts.fast);
+    float s[G], r[G];
+    row_broadcast(std::make_integer_sequence<int, G>{}, ts.s, s);
+    row_broadcast(std::make_integer_sequence<int, G>{}, ts.r, r);
+    uint8_t* q = a.q + row * a.ldq;
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+        const int64_t c = 8 * (t + 64 * W * (i0 + i));
+        if (fast && c + 8 <= a.cols) {
+            *reinterpret_cast<uint2*>(q + c) =
+                make_uint2(encode4_sr<POW2>(v[i][0], v[i][1], v[i][2], v[i][3], s[i], r[i]),
+                           encode4_sr<POW2>(v[i][4], v[i][5], v[i][6], v[i][7], s[i], r[i]));
+        } else if (c < a.cols) {
+            const TileScale tt = scale_from(s[i], r[i]);
+            store8(q, c, a.cols, encode4_any<POW2>(v[i][0], v[i][1], v[i][2], v[i][3], tt),
+                   encode4_any<POW2>(v[i][4], v[i][5], v[i][6], v[i][7], tt));
         }
     }
 }
 
+// One row per work-group of W waves: few rows, and rows too wide for a wave.
+template <typename T, int W, int I, bool LAYER, bool POW2>
+__global__ __launch_bounds__(64 * W) void layernorm_row_kernel(LayernormArgs a) {
+    __shared__ float s_red[2][1][16];
+    const int64_t cols = a.cols, row = blockIdx.x;
+    const int t = threadIdx.x;
+    const float n = (float)cols;
+    Raw8<T> raw[I];
+#pragma unroll
+    for (int i = 0; i < I; ++i)
+        load_row8(raw[i], static_cast<const T*>(a.x) + row * a.ldx, 8 * (t + 64 * W * i), cols, false);
+    float mean = 0.0f;
+    if constexpr (LAYER) {
+        float sum[1] = {0.0f};
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+            float v[8];
+            raw[i].values(v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum[0] += v[k];
+        }
+        block_sum<W, 1>(sum, s_red[0]);
+        mean = sum[0] / n;
+    }
+    float sq[1] = {sum_squares<T, W, I>(raw, t, cols, mean, a.shrink)};
+    block_sum<W, 1>(sq, s_red[1]);
+    const float rstd = 1.0f / sqrtf(sq[0] / (n * a.shrink * a.shrink) + a.eps);
+    if (t == 0) {
+        if (LAYER && a.mean) a.mean[row] = mean;
+        if (a.rstd) a.rstd[row] = rstd;
+    }
+    finish_groups<T, W, I, POW2, false>(a, raw, 0, t, row, mean, rstd, [&](int i, float gm[8], float bt[8]) {
+        load_weights8(a.gamma, a.w_dtype, 8 * (t + 64 * W * i), cols, 1.0f, gm);
+        load_weights8(a.beta, a.w_dtype, 8 * (t + 64 * W * i), cols, 0.0f, bt);
+    });
+}
+
+// Weights in LDS: the two halves of every group of eight lie in two runs, so
+// that neighbouring lanes read neighbouring 16 bytes.
+template <int N>  // columns
+struct LdsWeights {
+    float4 half[2][N / 8];
+    __device__ __forceinline__ void put(int c, const float v[8]) {
+        half[0][c >> 3] = make_float4(v[0], v[1], v[2], v[3]);
+        half[1][c >> 3] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+    __device__ __forceinline__ void get(int c, float v[8]) const {
+        *reinterpret_cast<float4*>(v) = half[0][c >> 3];
+        *reinterpret_cast<float4*>(v + 4) = half[1][c >> 3];
+    }
+};
+
+// Fills the weights' LDS copy with all threads of the work-group.
+template <int N>
+__device__ __forceinline__ void fill_weights(LdsWeights<N>& to, const void* w, int dtype, int64_t cols, float dflt) {
+    for (int c = 8 * threadIdx.x; c < cols; c += 8 * blockDim.x) {
+        float v[8];
+        load_weights8(w, dtype, c, cols, dflt, v);
+        to.put(c, v);
+    }
+}
+
+// One row per wave, kRowsPerGroup rows per work-group, which share the weights
+// in LDS: many rows of at most 2048 columns.
+constexpr int kRowsPerGroup = 8;
+
+template <typename T, int I, bool LAYER, bool POW2>
+__global__ __launch_bounds__(64 * kRowsPerGroup, 4) void layernorm_rows_kernel(LayernormArgs a) {
+    __shared__ LdsWeights<512 * I> s_gamma, s_beta;
+    const int64_t cols = a.cols;
+    const int t = threadIdx.x & 63;
+    const int64_t row = (int64_t)blockIdx.x * kRowsPerGroup + (threadIdx.x >> 6);
+    const float n = (float)cols;
+    Raw8<T> raw[I];
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+        raw[i].zero();
+        if (row < a.rows && 512 * i < cols)
+            load_row8(raw[i], static_cast<const T*>(a.x) + row * a.ldx, 8 * (t + 64 * i), cols, 512 * (i + 1) <= cols);
+    }
+    fill_weights(s_gamma, a.gamma, a.w_dtype, cols, 1.0f);
+    fill_weights(s_beta, a.beta, a.w_dtype, cols, 0.0f);
+    __syncthreads();
+    if (row >= a.rows) return;
+    float mean = 0.0f;
+    if constexpr (LAYER) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+            float v[8];
+            raw[i].values(v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum += v[k];
+        }
+        mean = wave_sum(sum) / n;
+        forget(raw);
+    }
+    const float sq = wave_sum(sum_squares<T, 1, I>(raw, t, cols, mean, a.shrink));
+    forget(raw);
+    const float rstd = 1.0f / sqrtf(sq / (n * a.shrink * a.shrink) + a.eps);
+    if (t == 0) {
+        if (LAYER && a.mean) a.mean[row] = mean;
+        if (a.rstd) a.rstd[row] = rstd;
+    }
+    finish_groups<T, 1, I, POW2, false>(a, raw, 0, t, row, mean, rstd, [&](int i, float gm[8], float bt[8]) {
+        s_gamma.get(8 * (t + 64 * i), gm);
+        s_beta.get(8 * (t + 64 * i), bt);
+    });
+}
+
+// Teams of four waves with a row each, two teams per work-group, which share
+// the weights in LDS; a team loads its next row before it works on the
+// current one.  A work-group's rows are consecutive, so the scales that it
+// writes fill whole lines.  Many rows of more than 2048 columns (a wave per
+// row needs over 200 registers there, a work-group per row reads the weights
+// again for every row: 85 and 88 us at 8192x7168 bf16 with codes and values,
+// where this one takes 60, 67 without the non-temporal stores of y).
+constexpr int kTeams = 2;
+
+template <typename T, int I, bool LAYER, bool POW2>
+__global__ __launch_bounds__(256 * kTeams, 4) void layernorm_team_kernel(LayernormArgs a, int rows_per_group) {
+    constexpr int W = 4;
+    __shared__ LdsWeights<512 * W * I> s_gamma, s_beta;
+    __shared__ float s_red[2][kTeams][W];
+    const int64_t cols = a.cols;
+    const int team = threadIdx.x / (64 * W), t = threadIdx.x % (64 * W);
+    const int64_t first = (int64_t)blockIdx.x * rows_per_group, end = min(first + rows_per_group, a.rows);
+    const float n = (float)cols;
+    auto load = [&](Raw8<T> (&raw)[I], int64_t row) {
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+            const int64_t c = 8 * (t + 64 * W * i);
+            if (row < end) load_row8(raw[i], static_cast<const T*>(a.x) + row * a.ldx, c, cols, false);
+        }
+    };
+    auto team_sum = [&](float v, int phase) {
+        v = wave_sum(v);
+        if ((t & 63) == 0) s_red[phase][team][t >> 6] = v;
+        lds_barrier();
+        return (s_red[phase][team][0] + s_red[phase][team][1]) + (s_red[phase][team][2] + s_red[phase][team][3]);
+    };
+    Raw8<T> raw[I], next[I];
+#pragma unroll
+    for (int i = 0; i < I; ++i) next[i].zero();
+    load(next, first + team);
+    fill_weights(s_gamma, a.gamma, a.w_dtype, cols, 1.0f);
+    fill_weights(s_beta, a.beta, a.w_dtype, cols, 0.0f);
+    __syncthreads();
+    int phase = 0;
+    for (int64_t r = first; r < end; r += kTeams) {  // the same trips for both teams: the barriers are the work-group's
+        const int64_t row = r + team;
+#pragma unroll
+        for (int i = 0; i < I; ++i) raw[i] = next[i];
+        load(next, row + kTeams);
+        float mean = 0.0f;
+        if constexpr (LAYER) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < I; ++i) {
+                float v[8];
+                raw[i].values(v);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) sum += v[k];
+            }
+            mean = team_sum(sum, 0) / n;
+            forget(raw);
+        }
+        // a layer norm's two sums have a buffer each, an RMS norm's sums take turns
+        const float sq = team_sum(sum_squares<T, W, I>(raw, t, cols, mean, a.shrink), LAYER ? 1 : phase);
+        phase ^= 1;
+        forget(raw);
+        const float rstd = 1.0f / sqrtf(sq / (n * a.shrink * a.shrink) + a.eps);
+        if (row >= end) continue;
+        if (t == 0) {
+            if (LAYER && a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
+        finish_groups<T, W, I, POW2, true>(a, raw, 0, t, row, mean, rstd, [&](int i, float gm[8], float bt[8]) {
+            s_gamma.get(8 * (t + 64 * W * i), gm);
+            s_beta.get(8 * (t + 64 * W * i), bt);
+        });
+    }
+}
+
 // ----------------------------------------------------------------------------
-// Backward.  Work-group p of P handles rows p, p+P, ...: thread columns as in
-// the forward pass, so the sums over rows stay in registers until the end,
-// where they go to part[p][gamma|beta][cols]; layernorm_parts_kernel adds the
-// P partial sums in order, so repeated calls give the same bits.
+// Backward.  A work-group of 16 waves works on 16/W rows at a time, one per
+// team of W waves, with thread columns as in the forward pass; the sums over
+// its rows stay in registers.  At the end the teams' sums are added in LDS and
+// go to part[group][gamma|beta][cols]; layernorm_parts_kernel adds the P
+// partial sums in order, so repeated calls give the same bits.  Where
+// registers allow (I == 1) a team's next row is on its way while a row is
+// worked on; the only wait inside a row is the join of its two sums.
+//   One work-group per compute unit: 8192x7168 bf16 with skip takes 87 us
+// (5.4 TB/s), 94 with two, 116 with work-groups of eight waves, whose twice as
+// many sums per thread leave no registers for the next row.
 // ----------------------------------------------------------------------------
 template <typename T, int W, int I, bool LAYER>
-__global__ __launch_bounds__(64 * W) void layernorm_backward_kernel(LayernormBackwardArgs a) {
+__global__ __launch_bounds__(1024, 4) void layernorm_backward_kernel(LayernormBackwardArgs a) {
+    constexpr int kTeams = 16 / W, kCols = 512 * W * I;
+    constexpr bool kAhead = I == 1;
+    __shared__ LdsWeights<kCols> s_gamma;
     __shared__ float s_red[2][2][16];
+    __shared__ float s_team[kTeams > 1 ? kTeams : 1][kTeams > 1 ? kCols : 1];
     const int64_t cols = a.cols;
+    const int wave = threadIdx.x >> 6, team = wave / W, t = threadIdx.x % (64 * W);
     const float inv_n = 1.0f / (float)cols;
+    auto load = [&](Raw8<T> (&raw)[I], const void* p, int64_t ld, int64_t row) {
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+            raw[i].zero();
+            if (row < a.rows) load_row8(raw[i], static_cast<const T*>(p) + row * ld, 8 * (t + 64 * W * i), cols, false);
+        }
+    };
     float dgamma[I][8], dbeta[I][8];
 #pragma unroll
     for (int i = 0; i < I; ++i)
 #pragma unroll
         for (int k = 0; k < 8; ++k) dgamma[i][k] = dbeta[i][k] = 0.0f;
-    int parity = 0;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        const float mean = LAYER ? a.mean[row] : 0.0f;
-        const float rstd = a.rstd[row];
+    Raw8<T> x[I], dy[I], skip[I], nx[I], ndy[I];
+    const int64_t step = (int64_t)gridDim.x * kTeams;
+    int64_t base = (int64_t)blockIdx.x * kTeams;  // the work-group's rows are base .. base + kTeams - 1
+    auto statistic = [&](const float* p, int64_t row) { return row < a.rows ? p[row] : 0.0f; };
+    float n_mean = LAYER ? statistic(a.mean, base + team) : 0.0f, n_rstd = statistic(a.rstd, base + team);
+    if (kAhead) {
+        load(nx, a.x, a.ldx, base + team);
+        load(ndy, a.dy, a.lddy, base + team);
+    }
+    fill_weights(s_gamma, a.gamma, a.w_dtype, cols, 1.0f);
+    __syncthreads();
+    for (int phase = 0; base < a.rows; base += step, phase ^= 1) {
+        const int64_t row = base + team;
+        const float mean = n_mean, rstd = n_rstd;
+        if (kAhead) {
+#pragma unroll
+            for (int i = 0; i < I; ++i) {
+                x[i] = nx[i];
+                dy[i] = ndy[i];
+            }
+        } else {
+            load(x, a.x, a.ldx, row);
+            load(dy, a.dy, a.lddy, row);
+        }
+        if (a.skip) {
+            load(skip, a.skip, a.ldskip, row);
+        } else {
+#pragma unroll
+            for (int i = 0; i < I; ++i) skip[i].zero();
+        }
+        if (kAhead) {
+            load(nx, a.x, a.ldx, row + step);
+            load(ndy, a.dy, a.lddy, row + step);
+        }
+        if (LAYER) n_mean = statistic(a.mean, row + step);
+        n_rstd = statistic(a.rstd, row + step);
         float xh[I][8], w[I][8];
-        float sum[2] = {0.0f, 0.0f};
+        float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
         for (int i = 0; i < I; ++i) {
-            const int64_t c = 8 * (threadIdx.x + 64 * W * i);
-            Raw8<T> raw;
             float gm[8];
-            load_row8(raw, static_cast<const T*>(a.x) + row * a.ldx, c, cols, false);
-            raw.values(xh[i]);
-            load_row8(raw, static_cast<const T*>(a.dy) + row * a.lddy, c, cols, false);
-            raw.values(w[i]);  // dy, zero beyond the row's end
-            load_weights8(a.gamma, a.w_dtype, c, cols, 1.0f, gm);
+            s_gamma.get(8 * (t + 64 * W * i), gm);
+            x[i].values(xh[i]);
+            dy[i].values(w[i]);  // dy, zero beyond the row's end
+            if (8 * (t + 64 * W * i) >= cols) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) gm[k] = 0.0f;  // LDS holds nothing there
+            }
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 xh[i][k] = (xh[i][k] - mean) * rstd;
-                dgamma[i][k] += w[i][k] * xh[i][k];
+                dgamma[i][k] = __builtin_fmaf(w[i][k], xh[i][k], dgamma[i][k]);
                 dbeta[i][k] += w[i][k];
                 w[i][k] *= gm[k];
-                sum[0] += w[i][k] * xh[i][k];
-                sum[1] += w[i][k];
+                s0 = __builtin_fmaf(w[i][k], xh[i][k], s0);
+                s1 += w[i][k];
             }
         }
-        block_sum<W, 2>(sum, s_red[parity]);
-        parity ^= 1;
-        const float c2 = sum[0] * inv_n, c1 = LAYER ? sum[1] * inv_n : 0.0f;
+        s0 = wave_sum(s0);
+        if (LAYER) s1 = wave_sum(s1);
+        if constexpr (W > 1) {
+            if ((t & 63) == 0) {
+                s_red[phase][0][wave] = s0;
+                if (LAYER) s_red[phase][1][wave] = s1;
+            }
+            lds_barrier();
+            s0 = s1 = 0.0f;
+#pragma unroll
+            for (int k = 0; k < W; ++k) {
+                s0 += s_red[phase][0][W * team + k];
+                if (LAYER) s1 += s_red[phase][1][W * team + k];
+            }
+        }
+        if (row >= a.rows) continue;
+        const float c2 = s0 * inv_n, c1 = LAYER ? s1 * inv_n : 0.0f;
 #pragma unroll
         for (int i = 0; i < I; ++i) {
-            const int64_t c = 8 * (threadIdx.x + 64 * W * i);
-            float add[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (a.skip) {
-                Raw8<T> raw;
-                load_row8(raw, static_cast<const T*>(a.skip) + row * a.ldskip, c, cols, false);
-                raw.values(add);
-            }
+            float add[8];
+            skip[i].values(add);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) w[i][k] = (w[i][k] - xh[i][k] * c2 - c1) * rstd + add[k];
-            store_values8(static_cast<T*>(a.dx) + row * a.lddx, c, cols, w[i]);
+            for (int k = 0; k < 8; ++k)
+                w[i][k] = __builtin_fmaf(__builtin_fmaf(-xh[i][k], c2, w[i][k]) - c1, rstd, add[k]);
+            store_values8(static_cast<T*>(a.dx) + row * a.lddx, 8 * (t + 64 * W * i), cols, w[i]);
         }
     }
     if (a.parts == nullptr) return;
     float* out = a.parts + (int64_t)blockIdx.x * 2 * a.ldparts;
+    if constexpr (kTeams == 1) {
 #pragma unroll
-    for (int i = 0; i < I; ++i) {
-        const int64_t c = 8 * (threadIdx.x + 64 * W * i);
-        store_values8(out, c, cols, dgamma[i]);
-        store_values8(out + a.ldparts, c, cols, dbeta[i]);
+        for (int i = 0; i < I; ++i) {
+            store_values8(out, 8 * (t + 64 * W * i), cols, dgamma[i]);
+            store_values8(out + a.ldparts, 8 * (t + 64 * W * i), cols, dbeta[i]);
+        }
+    } else {
+        static_assert(I == 1, "a column group per thread");
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            __syncthreads();
+            store_values8(s_team[team], 8 * t, kCols, m == 0 ? dgamma[0] : dbeta[0]);
+            __syncthreads();
+            for (int c = threadIdx.x; c < cols; c += 1024) {
+                float v = 0.0f;
+#pragma unroll
+                for (int k = 0; k < kTeams; ++k) v += s_team[k][c];
+                out[m * a.ldparts + c] = v;
+            }
+        }
     }
 }
 
-// Sum of the P partial rows: 64 columns per work-group, 4 waves that take
-// every fourth partial, joined in order.  blockIdx.y: 0 gamma, 1 beta.
-__global__ __launch_bounds__(256) void layernorm_parts_kernel(const float* __restrict__ parts, int64_t ldparts, int P,
-                                                              int64_t cols, float* dgamma, float* dbeta,
-                                                              int accumulate) {
-    __shared__ float s_sum[4][64];
+// Sum of the P partial rows: 64 columns per work-group, 16 waves that take
+// every 16th partial, joined in order.  blockIdx.y: 0 gamma, 1 beta.
+// (256 partials of 7168 columns: 5 us; 512 with four waves took 38.)
+__global__ __launch_bounds__(1024) void layernorm_parts_kernel(const float* __restrict__ parts, int64_t ldparts, int P,
+                                                               int64_t cols, float* dgamma, float* dbeta,
+                                                               int accumulate) {
+    __shared__ float s_sum[16][64];
     float* out = blockIdx.y == 0 ? dgamma : dbeta;
     if (out == nullptr) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t c = (int64_t)blockIdx.x * 64 + lane;
     float v = 0.0f;
-    if (c < cols)
-        for (int p = wave; p < P; p += 4) v += parts[((int64_t)p * 2 + blockIdx.y) * ldparts + c];
+    if (c < cols) {
+        const float* from = parts + blockIdx.y * ldparts + c;
+#pragma unroll 8
+        for (int p = wave; p < P; p += 16) v += from[(int64_t)p * 2 * ldparts];
+    }
     s_sum[wave][lane] = v;
     __syncthreads();
     if (wave == 0 && c < cols) {
-        v = (s_sum[0][lane] + s_sum[1][lane]) + (s_sum[2][lane] + s_sum[3][lane]);
+        v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 16; ++w) v += s_sum[w][lane];
         out[c] = accumulate ? out[c] + v : v;
     }
 }
@@ -236,7 +532,7 @@ __global__ __launch_bounds__(256) void layernorm_parts_kernel(const float* __res
 // ----------------------------------------------------------------------------
 namespace {
 
-constexpr int kMaxParts = 512;  // work-groups (and partial sums) of a backward pass
+constexpr int kMaxParts = 256;  // work-groups (and partial sums) of a backward pass
 
 // The power of two 2^-ceil(log2(n)/2): deviations are scaled by it before they
 // are squared, so the sum of n squares overflows only where their mean does.
@@ -246,58 +542,88 @@ float shrink_of(int64_t n) {
     return c;
 }
 
+#define FP8Q_NORM_LAUNCH(KERNEL, ...)                                                                     \
+    do {                                                                                                  \
+        if (a.layer && a.pow2)                                                                            \
+            hipLaunchKernelGGL((KERNEL<__VA_ARGS__, true, true>), grid, block, 0, st, a);                 \
+        else if (a.layer)                                                                                 \
+            hipLaunchKernelGGL((KERNEL<__VA_ARGS__, true, false>), grid, block, 0, st, a);                \
+        else if (a.pow2)                                                                                  \
+            hipLaunchKernelGGL((KERNEL<__VA_ARGS__, false, true>), grid, block, 0, st, a);                \
+        else                                                                                              \
+            hipLaunchKernelGGL((KERNEL<__VA_ARGS__, false, false>), grid, block, 0, st, a);               \
+    } while (0)
+
 template <typename T, int W, int I>
-void launch_forward(const LayernormArgs& a, hipStream_t st) {
-    const dim3 grid((unsigned)std::min<int64_t>(a.rows, 1 << 20)), block(64 * W);
-    if (a.layer && a.pow2)
-        hipLaunchKernelGGL((layernorm_kernel<T, W, I, true, true>), grid, block, 0, st, a);
-    else if (a.layer)
-        hipLaunchKernelGGL((layernorm_kernel<T, W, I, true, false>), grid, block, 0, st, a);
-    else if (a.pow2)
-        hipLaunchKernelGGL((layernorm_kernel<T, W, I, false, true>), grid, block, 0, st, a);
-    else
-        hipLaunchKernelGGL((layernorm_kernel<T, W, I, false, false>), grid, block, 0, st, a);
+void launch_row(const LayernormArgs& a, hipStream_t st) {
+    const dim3 grid((unsigned)a.rows), block(64 * W);
+    FP8Q_NORM_LAUNCH(layernorm_row_kernel, T, W, I);
 }
 
+template <typename T, int I>
+void launch_rows(const LayernormArgs& a, hipStream_t st) {
+    const dim3 grid((unsigned)((a.rows + kRowsPerGroup - 1) / kRowsPerGroup)), block(64 * kRowsPerGroup);
+    FP8Q_NORM_LAUNCH(layernorm_rows_kernel, T, I);
+}
+
+template <typename T, int I>
+void launch_teams(const LayernormArgs& a, hipStream_t st) {
+    const int64_t groups = 2 * (int64_t)cu_count();  // two work-groups fit a compute unit's LDS and registers
+    const int64_t per = std::max<int64_t>(kTeams, (a.rows + groups - 1) / groups);
+    const dim3 grid((unsigned)((a.rows + per - 1) / per)), block(256 * kTeams);
+    if (a.layer && a.pow2)
+        hipLaunchKernelGGL((layernorm_team_kernel<T, I, true, true>), grid, block, 0, st, a, (int)per);
+    else if (a.layer)
+        hipLaunchKernelGGL((layernorm_team_kernel<T, I, true, false>), grid, block, 0, st, a, (int)per);
+    else if (a.pow2)
+        hipLaunchKernelGGL((layernorm_team_kernel<T, I, false, true>), grid, block, 0, st, a, (int)per);
+    else
+        hipLaunchKernelGGL((layernorm_team_kernel<T, I, false, false>), grid, block, 0, st, a, (int)per);
+}
+
+// Many rows share the weights in LDS, from a team (or wave) per row; few rows
+// get a work-group each.
 template <typename T>
 void launch_forward_for(const LayernormArgs& a, hipStream_t st) {
-    if (a.cols <= 512)
-        launch_forward<T, 1, 1>(a, st);
-    else if (a.cols <= 2048)
-        launch_forward<T, 4, 1>(a, st);
-    else if (a.cols <= 8192)
-        launch_forward<T, 4, 4>(a, st);
-    else
-        launch_forward<T, 16, 2>(a, st);
+    const bool many = a.rows >= 8 * (int64_t)cu_count();
+    if (a.cols <= 512) launch_rows<T, 1>(a, st);
+    else if (a.cols <= 1024 && many) launch_rows<T, 2>(a, st);
+    else if (a.cols <= 2048 && many) launch_rows<T, 4>(a, st);
+    else if (a.cols <= 2048) launch_row<T, 4, 1>(a, st);
+    else if (a.cols <= 4096 && many) launch_teams<T, 2>(a, st);
+    else if (a.cols <= 8192 && many) launch_teams<T, 4>(a, st);
+    else if (a.cols <= 8192) launch_row<T, 16, 1>(a, st);
+    else launch_row<T, 16, 2>(a, st);
 }
 
 template <typename T, int W, int I>
 void launch_backward(const LayernormBackwardArgs& a, int parts, hipStream_t st) {
     if (a.layer)
-        hipLaunchKernelGGL((layernorm_backward_kernel<T, W, I, true>), dim3((unsigned)parts), dim3(64 * W), 0, st, a);
+        hipLaunchKernelGGL((layernorm_backward_kernel<T, W, I, true>), dim3((unsigned)parts), dim3(1024), 0, st, a);
     else
-        hipLaunchKernelGGL((layernorm_backward_kernel<T, W, I, false>), dim3((unsigned)parts), dim3(64 * W), 0, st, a);
+        hipLaunchKernelGGL((layernorm_backward_kernel<T, W, I, false>), dim3((unsigned)parts), dim3(1024), 0, st, a);
 }
 
 template <typename T>
 void launch_backward_for(const LayernormBackwardArgs& a, int parts, hipStream_t st) {
-    if (a.cols <= 512)
-        launch_backward<T, 1, 1>(a, parts, st);
-    else if (a.cols <= 2048)
-        launch_backward<T, 4, 1>(a, parts, st);
-    else if (a.cols <= 8192)
-        launch_backward<T, 4, 4>(a, parts, st);
-    else
-        launch_backward<T, 16, 2>(a, parts, st);
+    if (a.cols <= 512) launch_backward<T, 1, 1>(a, parts, st);
+    else if (a.cols <= 2048) launch_backward<T, 4, 1>(a, parts, st);
+    else if (a.cols <= 8192) launch_backward<T, 16, 1>(a, parts, st);
+    else launch_backward<T, 16, 2>(a, parts, st);
 }
 
-int backward_parts(int64_t rows) { return (int)std::min<int64_t>(rows, kMaxParts); }
+// Work-groups of a backward pass: one per compute unit of an MI355X, fewer
+// where the rows (16, 4 or 1 at a time, by the width) do not go round.
+int backward_parts(int64_t rows, int64_t cols) {
+    const int64_t teams = cols <= 512 ? 16 : cols <= 2048 ? 4 : 1;
+    return (int)std::min<int64_t>((rows + teams - 1) / teams, kMaxParts);
+}
 int64_t parts_ld(int64_t cols) { return (cols + 7) / 8 * 8; }
 
 }  // namespace
 
 int64_t layernorm_backward_bytes(int64_t rows, int64_t cols) {
-    return (int64_t)backward_parts(rows) * 2 * parts_ld(cols) * 4;
+    return (int64_t)backward_parts(rows, cols) * 2 * parts_ld(cols) * 4;
 }
 
 hipError_t launch_layernorm(LayernormArgs a, hipStream_t st) {
@@ -308,7 +634,7 @@ hipError_t launch_layernorm(LayernormArgs a, hipStream_t st) {
 }
 
 hipError_t launch_layernorm_backward(LayernormBackwardArgs a, void* workspace, hipStream_t st) {
-    const int parts = backward_parts(a.rows);  // 0 rows: only the sums of nothing are written
+    const int parts = backward_parts(a.rows, a.cols);  // 0 rows: only the sums of nothing are written
     const bool weights = a.dgamma || a.dbeta;
     a.parts = weights ? static_cast<float*>(workspace) : nullptr;
     a.ldparts = parts_ld(a.cols);
@@ -317,7 +643,7 @@ hipError_t launch_layernorm_backward(LayernormBackwardArgs a, void* workspace, h
         else launch_backward_for<float>(a, parts, st);
     }
     if (weights)
-        hipLaunchKernelGGL(layernorm_parts_kernel, dim3((unsigned)((a.cols + 63) / 64), 2), dim3(256), 0, st, a.parts,
+        hipLaunchKernelGGL(layernorm_parts_kernel, dim3((unsigned)((a.cols + 63) / 64), 2), dim3(1024), 0, st, a.parts,
                            a.ldparts, parts, a.cols, a.dgamma, a.dbeta, a.accumulate);
     return hipGetLastError();
 }

@@ -65,19 +65,6 @@ __device__ __forceinline__ void decode8(uint2 w, float s, float v[8]) {
     for (int k = 0; k < 8; ++k) v[k] *= s;
 }
 
-// Magnitude maxima: the absolute value is an operand modifier and three
-// operands go into one maximum.  The bits of the result order like the number.
-__device__ __forceinline__ float max_abs3(float m, float a, float b) {
-    return __builtin_fmaxf(__builtin_fmaxf(m, __builtin_fabsf(a)), __builtin_fabsf(b));
-}
-
-__device__ __forceinline__ uint32_t amax8(const float v[8]) {
-    float m = __builtin_fmaxf(__builtin_fabsf(v[0]), __builtin_fabsf(v[1]));
-#pragma unroll
-    for (int k = 2; k < 8; k += 2) m = max_abs3(m, v[k], v[k + 1]);
-    return __float_as_uint(m);
-}
-
 // Byte of 16-token unit `unit` of column `ch` in a transposed 128x128 tile of
 // codes.  Units are XOR-ed with the column's group of eight, and the columns
 // of the upper half trade places with their neighbours, so that the 16 column

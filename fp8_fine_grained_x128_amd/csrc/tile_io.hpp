@@ -2,6 +2,8 @@
 // elements, shared by the kernels that read or write 1x128 and 128x1 tiles.
 #pragma once
 
+#include <utility>
+
 #include "device_common.hpp"
 
 namespace fp8q {
@@ -41,6 +43,14 @@ __device__ __forceinline__ void wave_lds_sync() {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Work-group barrier that orders LDS traffic and leaves global loads and
+// stores in flight.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
 
 __device__ __forceinline__ bool wave_all(bool p) { return __all((int)p) != 0; }
@@ -178,11 +188,18 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 }
 
 // Stores 8 values of a row at p[c .. c+8), clipped to `valid`; bf16 rows get
-// the nearest-even rounding.
+// the nearest-even rounding.  NT marks the store non-temporal.
+template <bool NT = false>
+__device__ __forceinline__ void store16(void* p, uint4 v) {
+    if constexpr (NT) store16_nt(p, v);
+    else *reinterpret_cast<uint4*>(p) = v;
+}
+
+template <bool NT = false>
 __device__ __forceinline__ void store_values8(float* p, int64_t c, int64_t valid, const float v[8]) {
     if (c + 8 <= valid) {
-        *reinterpret_cast<float4*>(p + c) = make_float4(v[0], v[1], v[2], v[3]);
-        *reinterpret_cast<float4*>(p + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        store16<NT>(p + c, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
+        store16<NT>(p + c + 4, make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])));
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -190,15 +207,35 @@ __device__ __forceinline__ void store_values8(float* p, int64_t c, int64_t valid
     }
 }
 
+template <bool NT = false>
 __device__ __forceinline__ void store_values8(uint16_t* p, int64_t c, int64_t valid, const float v[8]) {
     const uint32_t w[4] = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
     if (c + 8 <= valid) {
-        *reinterpret_cast<uint4*>(p + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        store16<NT>(p + c, make_uint4(w[0], w[1], w[2], w[3]));
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (c + i < valid) p[c + i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
     }
+}
+
+// Lane n of each 16-lane DPP row to all 16 of them, for n = 0 .. N-1.
+template <int... N>
+__device__ __forceinline__ void row_broadcast(std::integer_sequence<int, N...>, float v, float (&out)[sizeof...(N)]) {
+    ((out[N] = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x150 + N, 0xf, 0xf, false))), ...);
+}
+
+// Magnitude maxima: the absolute value is an operand modifier and three
+// operands go into one maximum.  The bits of the result order like the number.
+__device__ __forceinline__ float max_abs3(float m, float a, float b) {
+    return __builtin_fmaxf(__builtin_fmaxf(m, __builtin_fabsf(a)), __builtin_fabsf(b));
+}
+
+__device__ __forceinline__ uint32_t amax8(const float v[8]) {
+    float m = __builtin_fmaxf(__builtin_fabsf(v[0]), __builtin_fabsf(v[1]));
+#pragma unroll
+    for (int k = 2; k < 8; k += 2) m = max_abs3(m, v[k], v[k + 1]);
+    return __float_as_uint(m);
 }
 
 // Sum over the 64 lanes of a wave; every lane receives the same bits (each
