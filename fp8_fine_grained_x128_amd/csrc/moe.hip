@@ -23,6 +23,7 @@
 // column l%16.  A holds weight rows, B tokens.
 #include <algorithm>
 
+#include "../../include/fp8q.h"
 #include "launch.hpp"
 #include "tile_io.hpp"
 
@@ -36,6 +37,8 @@ typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 
 constexpr int kMaxTokens = 64;
 constexpr int kMaxExperts = 1024;
+constexpr int kFusedTokens = 16;  // tokens that the gate and up projections may route themselves
+constexpr int kFewTokens = 8;     // tokens whose two halves of h share a matrix operand
 
 // Where the pieces of the workspace lie (bytes from its start).  Token t's
 // pairs are t*top_k, t*top_k + 1, ..., one for each of its experts in
@@ -92,14 +95,12 @@ __device__ __forceinline__ uint32_t wave_or(uint32_t v) {
 // tokens was bound by its scalar unit: 10 us for 64 tokens).
 // ----------------------------------------------------------------------------
 template <int PL>  // experts per lane
-__global__ __launch_bounds__(64) void moe_route_kernel(MoeArgs a, MoeLayout L) {
-    const int lane = threadIdx.x, t = blockIdx.x;
+__device__ __forceinline__ void route_token(const MoeArgs& a, const MoeLayout& L, int t, uint64_t* set, int* count,
+                                            float* prob) {
+    const int lane = threadIdx.x & 63;
     constexpr uint32_t kNone = 0x007fffffu;  // key of -inf; keys up to it are no candidates
     const uint64_t below = (1ull << lane) - 1;
     const float* row = a.logits + (int64_t)t * a.ldl;
-    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-    uint64_t* set = reinterpret_cast<uint64_t*>(ws + L.sets) + (int64_t)t * L.words;
-    int* count = reinterpret_cast<int*>(ws + L.count) + t;
 
     float l[PL], top = -__builtin_inff();
     uint32_t key[PL];
@@ -154,11 +155,27 @@ __global__ __launch_bounds__(64) void moe_route_kernel(MoeArgs a, MoeLayout L) {
         if (lane == 0 && j < L.words) set[j] = in_mask;
     }
     total = wave_sum(total);
-    float* prob = reinterpret_cast<float*>(ws + L.prob) + t * a.top_k;
 #pragma unroll
     for (int j = 0; j < PL; ++j)
         if (at[j] >= 0) prob[at[j]] = p[j] / total;
     if (lane == 0) *count = n;
+}
+
+// Where routing leaves its result for the other kernels.
+__device__ __forceinline__ uint64_t* sets_of(const MoeArgs& a, const MoeLayout& L) {
+    return reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(a.workspace) + L.sets);
+}
+__device__ __forceinline__ int* counts_of(const MoeArgs& a, const MoeLayout& L) {
+    return reinterpret_cast<int*>(static_cast<uint8_t*>(a.workspace) + L.count);
+}
+__device__ __forceinline__ float* probs_of(const MoeArgs& a, const MoeLayout& L) {
+    return reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + L.prob);
+}
+
+template <int PL>
+__global__ __launch_bounds__(64) void moe_route_kernel(MoeArgs a, MoeLayout L) {
+    const int t = blockIdx.x;
+    route_token<PL>(a, L, t, sets_of(a, L) + (int64_t)t * L.words, counts_of(a, L) + t, probs_of(a, L) + t * a.top_k);
 }
 
 // ----------------------------------------------------------------------------
@@ -172,6 +189,8 @@ __global__ __launch_bounds__(64) void moe_route_kernel(MoeArgs a, MoeLayout L) {
 // of the tokens, which comes from the caches; lanes of a column without a
 // token read nothing and their results are dropped.
 // ----------------------------------------------------------------------------
+
+constexpr int kTiles = 4;  // row tiles of a work-group
 
 // A 128-wide chunk.  NB: activation arrays whose sum is multiplied (x, or hi
 // and lo).
@@ -271,9 +290,10 @@ struct Chosen {
     int count;   // tokens
 };
 
-__device__ __forceinline__ Chosen choose(const MoeArgs& a, const MoeLayout& L, int idx, int* tokens, int* pairs) {
+__device__ __forceinline__ Chosen choose(const MoeArgs& a, const MoeLayout& L, const uint64_t* sets, int idx, int* tokens,
+                                         int* pairs) {
     const int t = threadIdx.x & 63;
-    const uint64_t* set = reinterpret_cast<const uint64_t*>(static_cast<const uint8_t*>(a.workspace) + L.sets) + t * L.words;
+    const uint64_t* set = sets + t * L.words;
     int rank = 0;  // the token's experts below
     for (int w0 = 0; w0 < L.words; w0 += 4) {
         uint64_t m[4];
@@ -303,13 +323,32 @@ __device__ __forceinline__ Chosen choose(const MoeArgs& a, const MoeLayout& L, i
     return {-1, 0};
 }
 
-// Gate and up projections with the SwiGLU.
-template <int NT>
+// Gate and up projections with the SwiGLU.  PL > 0: every work-group routes
+// the (few) tokens for itself, and the first one leaves the result for the
+// kernels that follow; PL == 0: routing has run.
+template <int NT, int PL>
 __global__ __launch_bounds__(256, 4) void moe_up_kernel(MoeArgs a, MoeLayout L) {
     __shared__ __align__(16) float s_sums[4][NT][256];
     __shared__ int s_token[kMaxTokens], s_pair[kMaxTokens];
+    __shared__ uint64_t s_sets[PL > 0 ? kFusedTokens * PL : 1];
+    __shared__ int s_count[kFusedTokens];
+    __shared__ float s_prob[PL > 0 ? kFusedTokens * FP8Q_MOE_MAX_TOP_K : 1];
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-    const Chosen e = choose(a, L, blockIdx.y, s_token, s_pair);
+    const float* prob = probs_of(a, L);
+    Chosen e;
+    if constexpr (PL > 0) {
+        for (int t = threadIdx.x >> 6; t < a.tokens; t += 4)
+            route_token<PL>(a, L, t, s_sets + t * L.words, s_count + t, s_prob + t * a.top_k);
+        __syncthreads();
+        if (blockIdx.x == 0 && blockIdx.y == 0) {
+            for (int i = threadIdx.x; i < a.tokens * L.words; i += 256) sets_of(a, L)[i] = s_sets[i];
+            if ((int)threadIdx.x < a.tokens) counts_of(a, L)[threadIdx.x] = s_count[threadIdx.x];
+        }
+        e = choose(a, L, s_sets, blockIdx.y, s_token, s_pair);
+        prob = s_prob;
+    } else {
+        e = choose(a, L, sets_of(a, L), blockIdx.y, s_token, s_pair);
+    }
     if (e.expert < 0) return;
     __syncthreads();
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -334,7 +373,7 @@ __global__ __launch_bounds__(256, 4) void moe_up_kernel(MoeArgs a, MoeLayout L) 
         const int tok = threadIdx.x >> 4, c = kPer * (threadIdx.x & 15);
         if (t0 + tok < e.count) {
             const int64_t pair = s_pair[t0 + tok];
-            const float p = reinterpret_cast<const float*>(ws + L.prob)[pair];
+            const float p = prob[pair];
             const int64_t at = pair * a.inner + h_place(row0 + c);
             float h[kPer];
             uint16_t hi[kPer], lo[kPer];
@@ -364,7 +403,7 @@ __global__ __launch_bounds__(256, 4) void moe_down_kernel(MoeArgs a, MoeLayout L
     __shared__ __align__(16) float s_sums[4][NT][256];
     __shared__ int s_token[kMaxTokens], s_pair[kMaxTokens];
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-    const Chosen e = choose(a, L, blockIdx.y, s_token, s_pair);
+    const Chosen e = choose(a, L, sets_of(a, L), blockIdx.y, s_token, s_pair);
     if (e.expert < 0) return;
     __syncthreads();
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -389,6 +428,118 @@ __global__ __launch_bounds__(256, 4) void moe_down_kernel(MoeArgs a, MoeLayout L
                 sum_waves<NT>(s_sums, c >> 4, tok * 16 + (c & 15));
         __syncthreads();
     }
+}
+
+// Down projection and weighted sum of at most eight tokens: a work-group takes
+// 16 rows of the hidden size and all active experts, so y needs no partial
+// results.  Matrix columns 0..7 are the tokens' hi halves of h, columns 8..15
+// their lo halves (half the loads and products of separate operands); a token
+// that did not choose the expert multiplies zeros.  The eight waves share the
+// (expert, chunk) pairs; weights are loaded three of them ahead, h one ahead.
+constexpr int kFewWaves = 8;
+
+__global__ __launch_bounds__(64 * kFewWaves, 4) void moe_down_few_kernel(MoeArgs a, MoeLayout L) {
+    constexpr int kSlots = kFewTokens * FP8Q_MOE_MAX_TOP_K;
+    __shared__ __align__(16) float s_sums[kFewWaves][256];
+    __shared__ int s_expert[kSlots];
+    __shared__ int s_pair[kSlots][kFewTokens];  // the token's pair with the expert, or -1
+    const uint8_t* ws = static_cast<const uint8_t*>(a.workspace);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15, kq = lane >> 4;
+    const int64_t row0 = (int64_t)blockIdx.x * 16;
+    const int chunks = (int)(a.inner >> 7);
+
+    int active = 0, rank = 0;  // experts so far; the lane's token's experts so far
+    for (int w = 0; w < L.words; ++w) {
+        const uint64_t m = lane < a.tokens ? sets_of(a, L)[lane * L.words + w] : 0;
+        uint64_t any = wave_or((uint32_t)m) | (uint64_t)wave_or((uint32_t)(m >> 32)) << 32;
+        for (; any != 0; any &= any - 1, ++active) {
+            const int bit = __builtin_ctzll(any);
+            if (active % kFewWaves != wave) continue;
+            if (lane < kFewTokens)
+                s_pair[active][lane] =
+                    (m >> bit) & 1 ? lane * a.top_k + rank + (int)__popcll(m & ((1ull << bit) - 1)) : -1;
+            if (lane == 0) s_expert[active] = 64 * w + bit;
+        }
+        rank += __popcll(m);
+    }
+    __syncthreads();
+
+    struct Item {  // an (expert, chunk) pair of this wave
+        int idx, kb;
+    };
+    auto advance = [&](Item& i) {
+        i.kb += kFewWaves;
+        while (i.kb >= chunks) {
+            i.kb -= chunks;
+            ++i.idx;
+        }
+    };
+    const uint8_t* w_rows = a.w_down + row0 * a.ldw_down;
+    const uint32_t row_offset = (uint32_t)(r * a.ldw_down) + 16 * kq;
+    const float* s_rows = a.s_down + (row0 >> 7) * a.lds_down;
+    const uint16_t* half = reinterpret_cast<const uint16_t*>(ws + (r < kFewTokens ? L.hi : L.lo));
+    uint4 w[4][2], h[2][4];
+    float scale[4];
+    auto load_w = [&](const Item& i, int slot) {
+        if (i.idx >= active) return;
+        const int e = __builtin_amdgcn_readfirstlane(s_expert[i.idx]);
+        const uint8_t* p = w_rows + e * a.w_down_stride + 128 * (int64_t)i.kb;
+        w[slot][0] = *reinterpret_cast<const uint4*>(p + row_offset);
+        w[slot][1] = *reinterpret_cast<const uint4*>(p + 64 + row_offset);
+        scale[slot] = s_rows[e * a.s_down_stride + i.kb];
+    };
+    auto load_h = [&](const Item& i, int slot) {
+        const int pair = i.idx < active ? s_pair[i.idx][r % kFewTokens] : -1;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[slot][j] = make_uint4(0, 0, 0, 0);
+        if (pair < 0) return;
+        const uint16_t* p = half + (int64_t)pair * a.inner + 128 * (int64_t)i.kb + 8 * kq;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[slot][j] = *reinterpret_cast<const uint4*>(p + 32 * j);
+    };
+    Item now{0, wave - kFewWaves}, next_h, next_w;
+    advance(now);
+    next_h = next_w = now;
+#pragma unroll
+    for (int u = 0; u < 3; ++u) {
+        load_w(next_w, u);
+        advance(next_w);
+    }
+    load_h(next_h, 0);
+    advance(next_h);
+    v4f acc = {0.f, 0.f, 0.f, 0.f};
+    while (now.idx < active) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (now.idx >= active) break;
+            load_w(next_w, (u + 3) & 3);
+            advance(next_w);
+            load_h(next_h, (u + 1) & 1);
+            advance(next_h);
+            v4f p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                p = mfma(bf16_of_codes(w[u][j].x, w[u][j].y), __builtin_bit_cast(v8bf, h[u & 1][2 * j]), p);
+                p = mfma(bf16_of_codes(w[u][j].z, w[u][j].w), __builtin_bit_cast(v8bf, h[u & 1][2 * j + 1]), p);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(p[i], scale[u], acc[i]);
+            advance(now);
+        }
+    }
+    *reinterpret_cast<v4f*>(&s_sums[wave][16 * r + 4 * kq]) = acc;
+    __syncthreads();
+    const int t = threadIdx.x >> 4, c = threadIdx.x & 15;  // token and row
+    if (t >= a.tokens) return;
+    float v = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kFewWaves; ++k) v += s_sums[k][16 * t + c] + s_sums[k][16 * (t + kFewTokens) + c];
+    if (counts_of(a, L)[t] < 0) v = __builtin_nanf("");
+    if (a.y_dtype == kDtypeBF16)
+        static_cast<uint16_t*>(a.y)[t * a.ldy + row0 + c] = (uint16_t)pack_bf16(v, 0.0f);
+    else
+        static_cast<float*>(a.y)[t * a.ldy + row0 + c] = v;
 }
 
 // A token's pairs added in the order of their experts.
@@ -433,11 +584,15 @@ MoeLayout moe_layout(int64_t tokens, int64_t hidden, int64_t inner, int experts,
     return L;
 }
 
-template <int NT>
-void launch_products(const MoeArgs& a, const MoeLayout& L, hipStream_t st) {
-    const unsigned slots = (unsigned)L.slots;
-    hipLaunchKernelGGL(moe_up_kernel<NT>, dim3((unsigned)(a.inner / (8 * NT)), slots), dim3(256), 0, st, a, L);
-    hipLaunchKernelGGL(moe_down_kernel<NT>, dim3((unsigned)(a.hidden / (16 * NT)), slots), dim3(256), 0, st, a, L);
+template <int PL>
+void launch_up(const MoeArgs& a, const MoeLayout& L, bool fused, hipStream_t st) {
+    const dim3 grid((unsigned)(a.inner / (8 * kTiles)), (unsigned)L.slots);
+    if (fused) {
+        hipLaunchKernelGGL((moe_up_kernel<kTiles, PL>), grid, dim3(256), 0, st, a, L);
+    } else {
+        hipLaunchKernelGGL(moe_route_kernel<PL>, dim3((unsigned)a.tokens), dim3(64), 0, st, a, L);
+        hipLaunchKernelGGL((moe_up_kernel<kTiles, 0>), grid, dim3(256), 0, st, a, L);
+    }
 }
 
 }  // namespace
@@ -448,13 +603,23 @@ int64_t moe_decode_bytes(int64_t tokens, int64_t hidden, int64_t inner, int expe
 
 hipError_t launch_moe_decode(const MoeArgs& a, hipStream_t st) {
     const MoeLayout L = moe_layout(a.tokens, a.hidden, a.inner, a.experts, a.top_k);
-    const dim3 waves((unsigned)a.tokens);
-    if (a.experts <= 64) hipLaunchKernelGGL(moe_route_kernel<1>, waves, dim3(64), 0, st, a, L);
-    else if (a.experts <= 256) hipLaunchKernelGGL(moe_route_kernel<4>, waves, dim3(64), 0, st, a, L);
-    else hipLaunchKernelGGL(moe_route_kernel<kMaxExperts / 64>, waves, dim3(64), 0, st, a, L);
-    launch_products<4>(a, L, st);
-    hipLaunchKernelGGL(moe_join_kernel, dim3((unsigned)((a.hidden + 255) / 256), (unsigned)a.tokens), dim3(256), 0, st,
-                       a, L);
+    const int cus = cu_count();
+    // A kernel of its own for routing costs 5 us; done by every work-group of
+    // the gate and up projections it costs each about 1 us for four tokens.
+    const bool fused = a.tokens <= 4 || (a.tokens <= kFusedTokens && a.inner / (8 * kTiles) * L.slots <= 4 * cus);
+    if (a.experts <= 64) launch_up<1>(a, L, fused, st);
+    else if (a.experts <= 256) launch_up<4>(a, L, fused, st);
+    else launch_up<kMaxExperts / 64>(a, L, fused, st);
+    // All experts in one work-group where there are rows enough for the chip,
+    // or little to read for each work-group.
+    if (a.tokens <= kFewTokens && (a.hidden / 16 >= cus || L.slots * 16 * a.inner <= 1 << 20)) {
+        hipLaunchKernelGGL(moe_down_few_kernel, dim3((unsigned)(a.hidden / 16)), dim3(64 * kFewWaves), 0, st, a, L);
+    } else {
+        hipLaunchKernelGGL(moe_down_kernel<kTiles>, dim3((unsigned)(a.hidden / (16 * kTiles)), (unsigned)L.slots),
+                           dim3(256), 0, st, a, L);
+        hipLaunchKernelGGL(moe_join_kernel, dim3((unsigned)((a.hidden + 255) / 256), (unsigned)a.tokens), dim3(256), 0,
+                           st, a, L);
+    }
     return hipGetLastError();
 }
 
