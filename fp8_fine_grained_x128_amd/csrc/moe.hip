@@ -610,9 +610,11 @@ hipError_t launch_moe_decode(const MoeArgs& a, hipStream_t st) {
     if (a.experts <= 64) launch_up<1>(a, L, fused, st);
     else if (a.experts <= 256) launch_up<4>(a, L, fused, st);
     else launch_up<kMaxExperts / 64>(a, L, fused, st);
-    // All experts in one work-group where there are rows enough for the chip,
-    // or little to read for each work-group.
-    if (a.tokens <= kFewTokens && (a.hidden / 16 >= cus || L.slots * 16 * a.inner <= 1 << 20)) {
+    // All experts in one work-group where that is little to read for each: a
+    // kernel less is worth 2 to 5 us, but the work-groups do not fill the
+    // chip evenly (one token of 64 experts 7168/2048, 256 KiB each: 72 against
+    // 73 us; two tokens 130 against 124).
+    if (a.tokens <= kFewTokens && L.slots * 16 * a.inner <= 1 << 18) {
         hipLaunchKernelGGL(moe_down_few_kernel, dim3((unsigned)(a.hidden / 16)), dim3(64 * kFewWaves), 0, st, a, L);
     } else {
         hipLaunchKernelGGL(moe_down_kernel<kTiles>, dim3((unsigned)(a.hidden / (16 * kTiles)), (unsigned)L.slots),

@@ -67,9 +67,9 @@ __device__ __forceinline__ void block_sum(float v[N], float (*red)[16]) {
 }  // namespace
 
 // ----------------------------------------------------------------------------
-// Forward.  A row belongs to W waves: thread t of them has columns
-// 8*(t + 64*W*i) .. +7 for i < I, so 16 neighbouring lanes hold one 128-column
-// tile and a tile maximum is a DPP row maximum.
+// Forward.  A row belongs to N lanes (16, a wave, or whole waves): lane t of
+// them has columns 8*(t + N*i) .. +7 for i < I, so 16 neighbouring lanes hold
+// one 128-column tile and a tile maximum is a DPP row maximum.
 // ----------------------------------------------------------------------------
 
 // Makes the compiler decode a row's stored values again instead of keeping
@@ -89,12 +89,12 @@ __device__ __forceinline__ void forget(Raw8<float> (&)[I]) {}
 
 // Sum of a row's deviations from `mean`, squared, times shrink^2.  Zeros
 // beyond the row's end stay out.
-template <typename T, int W, int I>
+template <typename T, int N, int I>
 __device__ __forceinline__ float sum_squares(const Raw8<T> (&raw)[I], int t, int64_t cols, float mean, float shrink) {
     float sq = 0.0f;
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-        const int64_t c = 8 * (t + 64 * W * i);
+        const int64_t c = 8 * (t + N * i);
         float v[8];
         raw[i].values(v);
         if (c + 8 <= cols) {
@@ -117,7 +117,7 @@ __device__ __forceinline__ float sum_squares(const Raw8<T> (&raw)[I], int t, int
 // Results of G groups of a row: y from the row's statistics, its values and
 // codes to memory.  One lane per tile computes the scale (lane i of a DPP row
 // for group i).  weights(i, gm, bt) gives the weights of group i.
-template <typename T, int W, int G, bool POW2, bool NT, typename Weights>
+template <typename T, int N, int G, bool POW2, bool NT, typename Weights>
 __device__ __forceinline__ void finish_groups(const LayernormArgs& a, const Raw8<T>* raw, int i0, int t, int64_t row,
                                               float mean, float rstd, const Weights& weights) {
     const int sub = t & 15;
@@ -125,7 +125,7 @@ __device__ __forceinline__ void finish_groups(const LayernormArgs& a, const Raw8
     uint32_t mine = 0;
 #pragma unroll
     for (int i = 0; i < G; ++i) {
-        const int64_t c = 8 * (t + 64 * W * (i0 + i));
+        const int64_t c = 8 * (t + N * (i0 + i));
         float gm[8], bt[8];
         weights(i0 + i, gm, bt);
         raw[i].values(v[i]);
@@ -149,7 +149,7 @@ __device__ __forceinline__ void finish_groups(const LayernormArgs& a, const Raw8
     if (!a.q) return;
     const TileScale ts = make_scale_mode<POW2>(mine);
     if (sub < G) {
-        const int64_t tile = 4 * W * (int64_t)(i0 + sub) + (t >> 4);
+        const int64_t tile = (N / 16) * (int64_t)(i0 + sub) + (t >> 4);
         if (tile * 128 < a.cols) a.s[tile * a.lds + row] = ts.s;
     }
     const bool fast = wave_all(sub >= G || ts.fast);
@@ -159,7 +159,7 @@ __device__ __forceinline__ void finish_groups(const LayernormArgs& a, const Raw8
     uint8_t* q = a.q + row * a.ldq;
 #pragma unroll
     for (int i = 0; i < G; ++i) {
-        const int64_t c = 8 * (t + 64 * W * (i0 + i));
+        const int64_t c = 8 * (t + N * (i0 + i));
         if (fast && c + 8 <= a.cols) {
             *reinterpret_cast<uint2*>(q + c) =
                 make_uint2(encode4_sr<POW2>(v[i][0], v[i][1], v[i][2], v[i][3], s[i], r[i]),
@@ -196,14 +196,14 @@ __global__ __launch_bounds__(64 * W) void layernorm_row_kernel(LayernormArgs a) 
         block_sum<W, 1>(sum, s_red[0]);
         mean = sum[0] / n;
     }
-    float sq[1] = {sum_squares<T, W, I>(raw, t, cols, mean, a.shrink)};
+    float sq[1] = {sum_squares<T, 64 * W, I>(raw, t, cols, mean, a.shrink)};
     block_sum<W, 1>(sq, s_red[1]);
     const float rstd = 1.0f / sqrtf(sq[0] / (n * a.shrink * a.shrink) + a.eps);
     if (t == 0) {
         if (LAYER && a.mean) a.mean[row] = mean;
         if (a.rstd) a.rstd[row] = rstd;
     }
-    finish_groups<T, W, I, POW2, false>(a, raw, 0, t, row, mean, rstd, [&](int i, float gm[8], float bt[8]) {
+    finish_groups<T, 64 * W, I, POW2, false>(a, raw, 0, t, row, mean, rstd, [&](int i, float gm[8], float bt[8]) {
         load_weights8(a.gamma, a.w_dtype, 8 * (t + 64 * W * i), cols, 1.0f, gm);
         load_weights8(a.beta, a.w_dtype, 8 * (t + 64 * W * i), cols, 0.0f, bt);
     });
@@ -234,84 +234,40 @@ __device__ __forceinline__ void fill_weights(LdsWeights<N>& to, const void* w, i
     }
 }
 
-// One row per wave, kRowsPerGroup rows per work-group, which share the weights
-// in LDS: many rows of at most 2048 columns.
-constexpr int kRowsPerGroup = 8;
+// Teams of N lanes with a row each, 512/N teams per work-group, which share
+// the weights in LDS; a team loads its next row before it works on the current
+// one.  A work-group's rows are consecutive, so the scales that it writes fill
+// whole lines.  Many rows, or narrow ones.  G work-groups are meant to share a
+// compute unit.  (8192x7168 bf16 with codes and values: 60 us, 67 without the
+// non-temporal stores of y; a wave per row needs over 200 registers there and
+// took 85, a work-group per row reads the weights again for every row, 88.)
+constexpr int kTeamThreads = 512;
 
-template <typename T, int I, bool LAYER, bool POW2>
-__global__ __launch_bounds__(64 * kRowsPerGroup, 4) void layernorm_rows_kernel(LayernormArgs a) {
-    __shared__ LdsWeights<512 * I> s_gamma, s_beta;
+template <typename T, int N, int I, int G, bool LAYER, bool POW2>
+__global__ __launch_bounds__(kTeamThreads, 2 * G) void layernorm_team_kernel(LayernormArgs a, int rows_per_group) {
+    constexpr int kTeams = kTeamThreads / N, W = N / 64;
+    __shared__ LdsWeights<8 * N * I> s_gamma, s_beta;
+    __shared__ float s_red[2][kTeams][W > 1 ? W : 1];
     const int64_t cols = a.cols;
-    const int t = threadIdx.x & 63;
-    const int64_t row = (int64_t)blockIdx.x * kRowsPerGroup + (threadIdx.x >> 6);
-    const float n = (float)cols;
-    Raw8<T> raw[I];
-#pragma unroll
-    for (int i = 0; i < I; ++i) {
-        raw[i].zero();
-        if (row < a.rows && 512 * i < cols)
-            load_row8(raw[i], static_cast<const T*>(a.x) + row * a.ldx, 8 * (t + 64 * i), cols, 512 * (i + 1) <= cols);
-    }
-    fill_weights(s_gamma, a.gamma, a.w_dtype, cols, 1.0f);
-    fill_weights(s_beta, a.beta, a.w_dtype, cols, 0.0f);
-    __syncthreads();
-    if (row >= a.rows) return;
-    float mean = 0.0f;
-    if constexpr (LAYER) {
-        float sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < I; ++i) {
-            float v[8];
-            raw[i].values(v);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) sum += v[k];
-        }
-        mean = wave_sum(sum) / n;
-        forget(raw);
-    }
-    const float sq = wave_sum(sum_squares<T, 1, I>(raw, t, cols, mean, a.shrink));
-    forget(raw);
-    const float rstd = 1.0f / sqrtf(sq / (n * a.shrink * a.shrink) + a.eps);
-    if (t == 0) {
-        if (LAYER && a.mean) a.mean[row] = mean;
-        if (a.rstd) a.rstd[row] = rstd;
-    }
-    finish_groups<T, 1, I, POW2, false>(a, raw, 0, t, row, mean, rstd, [&](int i, float gm[8], float bt[8]) {
-        s_gamma.get(8 * (t + 64 * i), gm);
-        s_beta.get(8 * (t + 64 * i), bt);
-    });
-}
-
-// Teams of four waves with a row each, two teams per work-group, which share
-// the weights in LDS; a team loads its next row before it works on the
-// current one.  A work-group's rows are consecutive, so the scales that it
-// writes fill whole lines.  Many rows of more than 2048 columns (a wave per
-// row needs over 200 registers there, a work-group per row reads the weights
-// again for every row: 85 and 88 us at 8192x7168 bf16 with codes and values,
-// where this one takes 60, 67 without the non-temporal stores of y).
-constexpr int kTeams = 2;
-
-template <typename T, int I, bool LAYER, bool POW2>
-__global__ __launch_bounds__(256 * kTeams, 4) void layernorm_team_kernel(LayernormArgs a, int rows_per_group) {
-    constexpr int W = 4;
-    __shared__ LdsWeights<512 * W * I> s_gamma, s_beta;
-    __shared__ float s_red[2][kTeams][W];
-    const int64_t cols = a.cols;
-    const int team = threadIdx.x / (64 * W), t = threadIdx.x % (64 * W);
+    const int team = threadIdx.x / N, t = threadIdx.x % N;
     const int64_t first = (int64_t)blockIdx.x * rows_per_group, end = min(first + rows_per_group, a.rows);
     const float n = (float)cols;
     auto load = [&](Raw8<T> (&raw)[I], int64_t row) {
 #pragma unroll
-        for (int i = 0; i < I; ++i) {
-            const int64_t c = 8 * (t + 64 * W * i);
-            if (row < end) load_row8(raw[i], static_cast<const T*>(a.x) + row * a.ldx, c, cols, false);
-        }
+        for (int i = 0; i < I; ++i)
+            if (row < end) load_row8(raw[i], static_cast<const T*>(a.x) + row * a.ldx, 8 * (t + N * i), cols, false);
     };
     auto team_sum = [&](float v, int phase) {
+        if constexpr (N == 16) return row_sum(v);
         v = wave_sum(v);
-        if ((t & 63) == 0) s_red[phase][team][t >> 6] = v;
-        lds_barrier();
-        return (s_red[phase][team][0] + s_red[phase][team][1]) + (s_red[phase][team][2] + s_red[phase][team][3]);
+        if constexpr (W > 1) {
+            if ((t & 63) == 0) s_red[phase][team][t >> 6] = v;
+            lds_barrier();
+            v = s_red[phase][team][0];
+#pragma unroll
+            for (int w = 1; w < W; ++w) v += s_red[phase][team][w];
+        }
+        return v;
     };
     Raw8<T> raw[I], next[I];
 #pragma unroll
@@ -321,7 +277,7 @@ __global__ __launch_bounds__(256 * kTeams, 4) void layernorm_team_kernel(Layerno
     fill_weights(s_beta, a.beta, a.w_dtype, cols, 0.0f);
     __syncthreads();
     int phase = 0;
-    for (int64_t r = first; r < end; r += kTeams) {  // the same trips for both teams: the barriers are the work-group's
+    for (int64_t r = first; r < end; r += kTeams) {  // the same trips for all teams: the barriers are the work-group's
         const int64_t row = r + team;
 #pragma unroll
         for (int i = 0; i < I; ++i) raw[i] = next[i];
@@ -340,7 +296,7 @@ __global__ __launch_bounds__(256 * kTeams, 4) void layernorm_team_kernel(Layerno
             forget(raw);
         }
         // a layer norm's two sums have a buffer each, an RMS norm's sums take turns
-        const float sq = team_sum(sum_squares<T, W, I>(raw, t, cols, mean, a.shrink), LAYER ? 1 : phase);
+        const float sq = team_sum(sum_squares<T, N, I>(raw, t, cols, mean, a.shrink), LAYER ? 1 : phase);
         phase ^= 1;
         forget(raw);
         const float rstd = 1.0f / sqrtf(sq / (n * a.shrink * a.shrink) + a.eps);
@@ -349,16 +305,16 @@ __global__ __launch_bounds__(256 * kTeams, 4) void layernorm_team_kernel(Layerno
             if (LAYER && a.mean) a.mean[row] = mean;
             if (a.rstd) a.rstd[row] = rstd;
         }
-        finish_groups<T, W, I, POW2, true>(a, raw, 0, t, row, mean, rstd, [&](int i, float gm[8], float bt[8]) {
-            s_gamma.get(8 * (t + 64 * W * i), gm);
-            s_beta.get(8 * (t + 64 * W * i), bt);
+        finish_groups<T, N, I, POW2, true>(a, raw, 0, t, row, mean, rstd, [&](int i, float gm[8], float bt[8]) {
+            s_gamma.get(8 * (t + N * i), gm);
+            s_beta.get(8 * (t + N * i), bt);
         });
     }
 }
 
 // ----------------------------------------------------------------------------
-// Backward.  A work-group of 16 waves works on 16/W rows at a time, one per
-// team of W waves, with thread columns as in the forward pass; the sums over
+// Backward.  A work-group of 1024 threads works on 1024/N rows at a time, one
+// per team of N lanes, with columns as in the forward pass; the sums over
 // its rows stay in registers.  At the end the teams' sums are added in LDS and
 // go to part[group][gamma|beta][cols]; layernorm_parts_kernel adds the P
 // partial sums in order, so repeated calls give the same bits.  Where
@@ -368,21 +324,21 @@ __global__ __launch_bounds__(256 * kTeams, 4) void layernorm_team_kernel(Layerno
 // (5.4 TB/s), 94 with two, 116 with work-groups of eight waves, whose twice as
 // many sums per thread leave no registers for the next row.
 // ----------------------------------------------------------------------------
-template <typename T, int W, int I, bool LAYER>
+template <typename T, int N, int I, bool LAYER>
 __global__ __launch_bounds__(1024, 4) void layernorm_backward_kernel(LayernormBackwardArgs a) {
-    constexpr int kTeams = 16 / W, kCols = 512 * W * I;
+    constexpr int kTeams = 1024 / N, kCols = 8 * N * I, W = N / 64;
     constexpr bool kAhead = I == 1;
     __shared__ LdsWeights<kCols> s_gamma;
     __shared__ float s_red[2][2][16];
     __shared__ float s_team[kTeams > 1 ? kTeams : 1][kTeams > 1 ? kCols : 1];
     const int64_t cols = a.cols;
-    const int wave = threadIdx.x >> 6, team = wave / W, t = threadIdx.x % (64 * W);
+    const int wave = threadIdx.x >> 6, team = threadIdx.x / N, t = threadIdx.x % N;
     const float inv_n = 1.0f / (float)cols;
     auto load = [&](Raw8<T> (&raw)[I], const void* p, int64_t ld, int64_t row) {
 #pragma unroll
         for (int i = 0; i < I; ++i) {
             raw[i].zero();
-            if (row < a.rows) load_row8(raw[i], static_cast<const T*>(p) + row * ld, 8 * (t + 64 * W * i), cols, false);
+            if (row < a.rows) load_row8(raw[i], static_cast<const T*>(p) + row * ld, 8 * (t + N * i), cols, false);
         }
     };
     float dgamma[I][8], dbeta[I][8];
@@ -431,10 +387,10 @@ __global__ __launch_bounds__(1024, 4) void layernorm_backward_kernel(LayernormBa
 #pragma unroll
         for (int i = 0; i < I; ++i) {
             float gm[8];
-            s_gamma.get(8 * (t + 64 * W * i), gm);
+            s_gamma.get(8 * (t + N * i), gm);
             x[i].values(xh[i]);
             dy[i].values(w[i]);  // dy, zero beyond the row's end
-            if (8 * (t + 64 * W * i) >= cols) {
+            if (8 * (t + N * i) >= cols) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) gm[k] = 0.0f;  // LDS holds nothing there
             }
@@ -448,8 +404,8 @@ __global__ __launch_bounds__(1024, 4) void layernorm_backward_kernel(LayernormBa
                 s1 += w[i][k];
             }
         }
-        s0 = wave_sum(s0);
-        if (LAYER) s1 = wave_sum(s1);
+        s0 = N == 16 ? row_sum(s0) : wave_sum(s0);
+        if (LAYER) s1 = N == 16 ? row_sum(s1) : wave_sum(s1);
         if constexpr (W > 1) {
             if ((t & 63) == 0) {
                 s_red[phase][0][wave] = s0;
@@ -472,7 +428,7 @@ __global__ __launch_bounds__(1024, 4) void layernorm_backward_kernel(LayernormBa
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 w[i][k] = __builtin_fmaf(__builtin_fmaf(-xh[i][k], c2, w[i][k]) - c1, rstd, add[k]);
-            store_values8(static_cast<T*>(a.dx) + row * a.lddx, 8 * (t + 64 * W * i), cols, w[i]);
+            store_values8(static_cast<T*>(a.dx) + row * a.lddx, 8 * (t + N * i), cols, w[i]);
         }
     }
     if (a.parts == nullptr) return;
@@ -480,8 +436,8 @@ __global__ __launch_bounds__(1024, 4) void layernorm_backward_kernel(LayernormBa
     if constexpr (kTeams == 1) {
 #pragma unroll
         for (int i = 0; i < I; ++i) {
-            store_values8(out, 8 * (t + 64 * W * i), cols, dgamma[i]);
-            store_values8(out + a.ldparts, 8 * (t + 64 * W * i), cols, dbeta[i]);
+            store_values8(out, 8 * (t + N * i), cols, dgamma[i]);
+            store_values8(out + a.ldparts, 8 * (t + N * i), cols, dbeta[i]);
         }
     } else {
         static_assert(I == 1, "a column group per thread");
@@ -542,80 +498,77 @@ float shrink_of(int64_t n) {
     return c;
 }
 
-#define FP8Q_NORM_LAUNCH(KERNEL, ...)                                                                     \
-    do {                                                                                                  \
-        if (a.layer && a.pow2)                                                                            \
-            hipLaunchKernelGGL((KERNEL<__VA_ARGS__, true, true>), grid, block, 0, st, a);                 \
-        else if (a.layer)                                                                                 \
-            hipLaunchKernelGGL((KERNEL<__VA_ARGS__, true, false>), grid, block, 0, st, a);                \
-        else if (a.pow2)                                                                                  \
-            hipLaunchKernelGGL((KERNEL<__VA_ARGS__, false, true>), grid, block, 0, st, a);                \
-        else                                                                                              \
-            hipLaunchKernelGGL((KERNEL<__VA_ARGS__, false, false>), grid, block, 0, st, a);               \
-    } while (0)
-
 template <typename T, int W, int I>
 void launch_row(const LayernormArgs& a, hipStream_t st) {
     const dim3 grid((unsigned)a.rows), block(64 * W);
-    FP8Q_NORM_LAUNCH(layernorm_row_kernel, T, W, I);
+    if (a.layer && a.pow2) hipLaunchKernelGGL((layernorm_row_kernel<T, W, I, true, true>), grid, block, 0, st, a);
+    else if (a.layer) hipLaunchKernelGGL((layernorm_row_kernel<T, W, I, true, false>), grid, block, 0, st, a);
+    else if (a.pow2) hipLaunchKernelGGL((layernorm_row_kernel<T, W, I, false, true>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((layernorm_row_kernel<T, W, I, false, false>), grid, block, 0, st, a);
 }
 
-template <typename T, int I>
-void launch_rows(const LayernormArgs& a, hipStream_t st) {
-    const dim3 grid((unsigned)((a.rows + kRowsPerGroup - 1) / kRowsPerGroup)), block(64 * kRowsPerGroup);
-    FP8Q_NORM_LAUNCH(layernorm_rows_kernel, T, I);
-}
-
-template <typename T, int I>
+template <typename T, int N, int I, int G>
 void launch_teams(const LayernormArgs& a, hipStream_t st) {
-    const int64_t groups = 2 * (int64_t)cu_count();  // two work-groups fit a compute unit's LDS and registers
-    const int64_t per = std::max<int64_t>(kTeams, (a.rows + groups - 1) / groups);
-    const dim3 grid((unsigned)((a.rows + per - 1) / per)), block(256 * kTeams);
-    if (a.layer && a.pow2)
-        hipLaunchKernelGGL((layernorm_team_kernel<T, I, true, true>), grid, block, 0, st, a, (int)per);
-    else if (a.layer)
-        hipLaunchKernelGGL((layernorm_team_kernel<T, I, true, false>), grid, block, 0, st, a, (int)per);
-    else if (a.pow2)
-        hipLaunchKernelGGL((layernorm_team_kernel<T, I, false, true>), grid, block, 0, st, a, (int)per);
-    else
-        hipLaunchKernelGGL((layernorm_team_kernel<T, I, false, false>), grid, block, 0, st, a, (int)per);
+    constexpr int64_t kTeams = kTeamThreads / N;
+    const int64_t groups = G * (int64_t)cu_count();
+    const int64_t per = ((a.rows + groups - 1) / groups + kTeams - 1) / kTeams * kTeams;
+    const dim3 grid((unsigned)((a.rows + per - 1) / per)), block(kTeamThreads);
+    const int n = (int)per;
+    if (a.layer && a.pow2) hipLaunchKernelGGL((layernorm_team_kernel<T, N, I, G, true, true>), grid, block, 0, st, a, n);
+    else if (a.layer) hipLaunchKernelGGL((layernorm_team_kernel<T, N, I, G, true, false>), grid, block, 0, st, a, n);
+    else if (a.pow2) hipLaunchKernelGGL((layernorm_team_kernel<T, N, I, G, false, true>), grid, block, 0, st, a, n);
+    else hipLaunchKernelGGL((layernorm_team_kernel<T, N, I, G, false, false>), grid, block, 0, st, a, n);
 }
 
-// Many rows share the weights in LDS, from a team (or wave) per row; few rows
-// get a work-group each.
+// Many rows, and narrow ones, go to teams; few wide rows get a work-group
+// each.  Registers and LDS decide how many work-groups share a compute unit.
 template <typename T>
 void launch_forward_for(const LayernormArgs& a, hipStream_t st) {
     const bool many = a.rows >= 8 * (int64_t)cu_count();
-    if (a.cols <= 512) launch_rows<T, 1>(a, st);
-    else if (a.cols <= 1024 && many) launch_rows<T, 2>(a, st);
-    else if (a.cols <= 2048 && many) launch_rows<T, 4>(a, st);
+    if (a.cols <= 128) launch_teams<T, 16, 1, 4>(a, st);
+    else if (a.cols <= 512) launch_teams<T, 64, 1, 4>(a, st);
+    else if (a.cols <= 1024 && many) launch_teams<T, 64, 2, 3>(a, st);
+    else if (a.cols <= 2048 && many) launch_teams<T, 64, 4, 2>(a, st);
     else if (a.cols <= 2048) launch_row<T, 4, 1>(a, st);
-    else if (a.cols <= 4096 && many) launch_teams<T, 2>(a, st);
-    else if (a.cols <= 8192 && many) launch_teams<T, 4>(a, st);
+    else if (a.cols <= 4096 && many) launch_teams<T, 256, 2, 3>(a, st);
+    else if (a.cols <= 8192 && many) launch_teams<T, 256, 4, 2>(a, st);
     else if (a.cols <= 8192) launch_row<T, 16, 1>(a, st);
     else launch_row<T, 16, 2>(a, st);
 }
 
-template <typename T, int W, int I>
+template <typename T, int N, int I>
 void launch_backward(const LayernormBackwardArgs& a, int parts, hipStream_t st) {
     if (a.layer)
-        hipLaunchKernelGGL((layernorm_backward_kernel<T, W, I, true>), dim3((unsigned)parts), dim3(1024), 0, st, a);
+        hipLaunchKernelGGL((layernorm_backward_kernel<T, N, I, true>), dim3((unsigned)parts), dim3(1024), 0, st, a);
     else
-        hipLaunchKernelGGL((layernorm_backward_kernel<T, W, I, false>), dim3((unsigned)parts), dim3(1024), 0, st, a);
+        hipLaunchKernelGGL((layernorm_backward_kernel<T, N, I, false>), dim3((unsigned)parts), dim3(1024), 0, st, a);
+}
+
+// Lanes of a row in the backward pass.
+int backward_lanes(int64_t cols) {
+    int n = 64;
+    while (n < 1024 && 8 * n < cols) n *= 2;
+    return cols <= 128 ? 16 : n;
 }
 
 template <typename T>
 void launch_backward_for(const LayernormBackwardArgs& a, int parts, hipStream_t st) {
-    if (a.cols <= 512) launch_backward<T, 1, 1>(a, parts, st);
-    else if (a.cols <= 2048) launch_backward<T, 4, 1>(a, parts, st);
-    else if (a.cols <= 8192) launch_backward<T, 16, 1>(a, parts, st);
-    else launch_backward<T, 16, 2>(a, parts, st);
+    switch (backward_lanes(a.cols)) {
+        case 16: launch_backward<T, 16, 1>(a, parts, st); break;
+        case 64: launch_backward<T, 64, 1>(a, parts, st); break;
+        case 128: launch_backward<T, 128, 1>(a, parts, st); break;
+        case 256: launch_backward<T, 256, 1>(a, parts, st); break;
+        case 512: launch_backward<T, 512, 1>(a, parts, st); break;
+        default:
+            if (a.cols <= 8192) launch_backward<T, 1024, 1>(a, parts, st);
+            else launch_backward<T, 1024, 2>(a, parts, st);
+    }
 }
 
 // Work-groups of a backward pass: one per compute unit of an MI355X, fewer
-// where the rows (16, 4 or 1 at a time, by the width) do not go round.
+// where the rows do not go round.
 int backward_parts(int64_t rows, int64_t cols) {
-    const int64_t teams = cols <= 512 ? 16 : cols <= 2048 ? 4 : 1;
+    const int64_t teams = 1024 / backward_lanes(cols);
     return (int)std::min<int64_t>((rows + teams - 1) / teams, kMaxParts);
 }
 int64_t parts_ld(int64_t cols) { return (cols + 7) / 8 * 8; }

@@ -65,6 +65,19 @@ __device__ __forceinline__ void decode8(uint2 w, float s, float v[8]) {
     for (int k = 0; k < 8; ++k) v[k] *= s;
 }
 
+// Codes of eight values of a row at q[c .. c+7], clipped to `cols`.  `fast`:
+// the scale allows the reciprocal quotient.
+template <bool POW2>
+__device__ __forceinline__ void put_codes8(uint8_t* q, int64_t c, int64_t cols, bool fast, const float v[8], float2 sr) {
+    if (fast) {
+        store8(q, c, cols, encode4_sr<POW2>(v[0], v[1], v[2], v[3], sr.x, sr.y),
+               encode4_sr<POW2>(v[4], v[5], v[6], v[7], sr.x, sr.y));
+    } else {
+        const TileScale t = scale_from(sr.x, sr.y);
+        store8(q, c, cols, encode4_any<POW2>(v[0], v[1], v[2], v[3], t), encode4_any<POW2>(v[4], v[5], v[6], v[7], t));
+    }
+}
+
 // Byte of 16-token unit `unit` of column `ch` in a transposed 128x128 tile of
 // codes.  Units are XOR-ed with the column's group of eight, and the columns
 // of the upper half trade places with their neighbours, so that the 16 column
@@ -140,8 +153,8 @@ __global__ __launch_bounds__(64 * W) void swiglu_quantize_kernel(SwigluArgs a) {
         }
     }
     wave_lds_sync();
-    const bool fast = full && wave_all(my_fast);
-    if (!fast && c >= a.cols) return;
+    const bool fast = wave_all(my_fast);
+    if (c >= a.cols) return;
 #pragma unroll
     for (int m = 0; m < M; ++m) {
         uint8_t* q = m == 0 ? a.qh : m == 1 ? a.qg : a.qu;
@@ -155,16 +168,8 @@ __global__ __launch_bounds__(64 * W) void swiglu_quantize_kernel(SwigluArgs a) {
             } else {
                 (m == 1 ? rg[i] : ru[i]).values(v);
             }
-            const float2 sr = s_sr[wave][lane >> 4][R * m + i];
-            uint8_t* to = q + (row0 + i) * ldq;
-            if (fast) {
-                *reinterpret_cast<uint2*>(to + c) = make_uint2(encode4_sr<POW2>(v[0], v[1], v[2], v[3], sr.x, sr.y),
-                                                               encode4_sr<POW2>(v[4], v[5], v[6], v[7], sr.x, sr.y));
-            } else if (row0 + i < a.rows) {
-                const TileScale t = scale_from(sr.x, sr.y);
-                store8(to, c, a.cols, encode4_any<POW2>(v[0], v[1], v[2], v[3], t),
-                       encode4_any<POW2>(v[4], v[5], v[6], v[7], t));
-            }
+            if (full || row0 + i < a.rows)
+                put_codes8<POW2>(q + (row0 + i) * ldq, c, a.cols, fast, v, s_sr[wave][lane >> 4][R * m + i]);
         }
     }
 }
@@ -297,7 +302,8 @@ __global__ __launch_bounds__(512, 4) void swiglu_backward_quantize_kernel(Swiglu
         if (r < a.rows) (cg < kRows ? a.sdg : a.sdu)[tile_c * a.ldsd + r] = ts.s;
     }
     wave_lds_sync();
-    if (full && wave_all(my_fast)) {
+    const bool fast_rows = wave_all(my_fast);
+    if (full && fast_rows) {
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             uint8_t* q = (m == 0 ? a.qdg : a.qdu) + row * a.ldqd + c;
@@ -312,15 +318,11 @@ __global__ __launch_bounds__(512, 4) void swiglu_backward_quantize_kernel(Swiglu
     } else if (c < a.cols) {
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
+            uint8_t* q = (m == 0 ? a.qdg : a.qdu) + row * a.ldqd;
 #pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                if (row + i >= a.rows) break;
-                const float2 sr = s_row[wave][rg & 3][kRows * m + i];
-                const TileScale ts = scale_from(sr.x, sr.y);
-                const float* x = v[m][i];
-                store8((m == 0 ? a.qdg : a.qdu) + (row + i) * a.ldqd, c, a.cols,
-                       encode4_any<POW2>(x[0], x[1], x[2], x[3], ts), encode4_any<POW2>(x[4], x[5], x[6], x[7], ts));
-            }
+            for (int i = 0; i < kRows; ++i)
+                if (row + i < a.rows)
+                    put_codes8<POW2>(q + i * a.ldqd, c, a.cols, fast_rows, v[m][i], s_row[wave][rg & 3][kRows * m + i]);
         }
     }
     __syncthreads();

@@ -238,14 +238,19 @@ __device__ __forceinline__ uint32_t amax8(const float v[8]) {
     return __float_as_uint(m);
 }
 
-// Sum over the 64 lanes of a wave; every lane receives the same bits (each
-// step adds a pair of equal-length partial sums, so the order within a pair
-// does not matter).
-__device__ __forceinline__ float wave_sum(float v) {
+// Sum over the 16 lanes of a DPP row, and over the 64 lanes of a wave; every
+// lane receives the same bits (each step adds a pair of equal-length partial
+// sums, so the order within a pair does not matter).
+__device__ __forceinline__ float row_sum(float v) {
     v += __uint_as_float(row_ror<8>(__float_as_uint(v)));
     v += __uint_as_float(row_ror<4>(__float_as_uint(v)));
     v += __uint_as_float(row_ror<2>(__float_as_uint(v)));
     v += __uint_as_float(row_ror<1>(__float_as_uint(v)));
+    return v;
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+    v = row_sum(v);
     v += __shfl_xor(v, 16);
     v += __shfl_xor(v, 32);
     return v;
