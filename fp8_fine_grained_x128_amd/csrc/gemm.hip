@@ -1118,6 +1118,7 @@ namespace {
 
 constexpr int kBM = 256, kBN = 256, kWM = 2, kWN = 4;
 
+int cu_count();
 
 GemmParams to_params(const GemmArgs& g) {
     GemmParams p;
@@ -1136,6 +1137,15 @@ GemmParams to_params(const GemmArgs& g) {
     p.ldws = 0;
     p.ws_stride = 0;
     return p;
+}
+
+int cu_count() {
+    int dev = 0, cus = 256;
+    if (hipGetDevice(&dev) == hipSuccess) {
+        int v = 0;
+        if (hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess && v > 0) cus = v;
+    }
+    return cus;
 }
 
 // Strips when they finish in fewer 64-column units of work per CU: a round of

@@ -10,16 +10,6 @@ namespace fp8q {
 constexpr int kDtypeF32 = 0;   // FP8Q_F32
 constexpr int kDtypeBF16 = 1;  // FP8Q_BF16
 
-// Compute units of the current device (256 where it cannot be asked).
-inline int cu_count() {
-    int dev = 0, cus = 256;
-    if (hipGetDevice(&dev) == hipSuccess) {
-        int v = 0;
-        if (hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess && v > 0) cus = v;
-    }
-    return cus;
-}
-
 // pow2: 0 fp32 scales fl32(amax/448), 1 power-of-two scales
 hipError_t launch_quantize_1x128(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ldx,
                                  uint8_t* q, int64_t ldq, float* s, int64_t lds, int pow2, hipStream_t st);
@@ -89,6 +79,17 @@ SplitPlan plan_splitk(int64_t M, int64_t N, int64_t K);
 hipError_t launch_grouped_gemm(const GemmArgs& g, hipStream_t st);
 
 // ---- feed-forward operators around the GEMMs
+
+// Compute units of the current device (256 where it cannot be asked).
+inline int compute_units() {
+    int dev = 0, cus = 256;
+    if (hipGetDevice(&dev) == hipSuccess) {
+        int v = 0;
+        if (hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess && v > 0) cus = v;
+    }
+    return cus;
+}
+
 struct LayernormArgs {
     const void* x;
     int x_dtype;

@@ -603,7 +603,7 @@ int64_t moe_decode_bytes(int64_t tokens, int64_t hidden, int64_t inner, int expe
 
 hipError_t launch_moe_decode(const MoeArgs& a, hipStream_t st) {
     const MoeLayout L = moe_layout(a.tokens, a.hidden, a.inner, a.experts, a.top_k);
-    const int cus = cu_count();
+    const int cus = compute_units();
     // A kernel of its own for routing costs 5 us; done by every work-group of
     // the gate and up projections it costs each about 1 us for four tokens.
     const bool fused = a.tokens <= 4 || (a.tokens <= kFusedTokens && a.inner / (8 * kTiles) * L.slots <= 4 * cus);

@@ -510,7 +510,7 @@ void launch_row(const LayernormArgs& a, hipStream_t st) {
 template <typename T, int N, int I, int G>
 void launch_teams(const LayernormArgs& a, hipStream_t st) {
     constexpr int64_t kTeams = kTeamThreads / N;
-    const int64_t groups = G * (int64_t)cu_count();
+    const int64_t groups = G * (int64_t)compute_units();
     const int64_t per = ((a.rows + groups - 1) / groups + kTeams - 1) / kTeams * kTeams;
     const dim3 grid((unsigned)((a.rows + per - 1) / per)), block(kTeamThreads);
     const int n = (int)per;
@@ -524,7 +524,7 @@ void launch_teams(const LayernormArgs& a, hipStream_t st) {
 // each.  Registers and LDS decide how many work-groups share a compute unit.
 template <typename T>
 void launch_forward_for(const LayernormArgs& a, hipStream_t st) {
-    const bool many = a.rows >= 8 * (int64_t)cu_count();
+    const bool many = a.rows >= 8 * (int64_t)compute_units();
     if (a.cols <= 128) launch_teams<T, 16, 1, 4>(a, st);
     else if (a.cols <= 512) launch_teams<T, 64, 1, 4>(a, st);
     else if (a.cols <= 1024 && many) launch_teams<T, 64, 2, 3>(a, st);
