@@ -33,6 +33,16 @@ __device__ __forceinline__ float sigmoid(float x) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -0x1.715476p+0f));
 }
 
+// x / (1 + exp(-x)) with the quotient corrected from its remainder, which
+// leaves about the error of a division.  exp(-x) is held below the largest
+// fp32, so that the remainder exists.  (The forward pass has room for the
+// three instructions; feeding p's rounding back too would cost 4 %.)
+__device__ __forceinline__ float silu(float x) {
+    const float d = 1.0f + __builtin_amdgcn_exp2f(__builtin_fmaxf(x, -87.0f) * -0x1.715476p+0f);
+    const float r = __builtin_amdgcn_rcpf(d), q = x * r;
+    return __builtin_fmaf(__builtin_fmaf(-d, q, x), r, q);
+}
+
 struct SwigluPoint {
     float h, dg, du;
 };
@@ -133,7 +143,7 @@ __global__ __launch_bounds__(64 * W) void swiglu_quantize_kernel(SwigluArgs a) {
         rg[i].values(g);
         ru[i].values(u);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) h[i][k] = g[k] * sigmoid(g[k]) * u[k];
+        for (int k = 0; k < 8; ++k) h[i][k] = silu(g[k]) * u[k];
         const uint32_t amax[3] = {amax8(h[i]), rg[i].amax_bits(), ru[i].amax_bits()};
 #pragma unroll
         for (int m = 0; m < M; ++m) {
