@@ -179,45 +179,51 @@ __global__ __launch_bounds__(64) void moe_route_kernel(MoeArgs a, MoeLayout L) {
 }
 
 // ----------------------------------------------------------------------------
-// Both projections.  A work-group takes 16*NT weight rows (NT row tiles: rows
-// of the hidden size, or NT/2 tiles of gate rows and the up rows that belong
-// to them) of one active expert.  Its four waves take every fourth 128-wide
-// chunk of the contraction, for 16 of the expert's tokens at a time, and join
-// their sums in LDS.
+// Both projections.  A work-group takes kTiles row tiles of 16 weight rows of
+// one active expert: rows of the hidden size, or as many tiles of gate rows as
+// of the up rows that belong to them.  Its four waves take every fourth
+// 128-wide chunk of the contraction, for 16 of the expert's tokens at a time,
+// and join their sums in LDS.
 //   Weights go straight from memory to the matrix operand (16 rows of 64
 // contiguous bytes a load), each one read once.  The row tiles share one read
 // of the tokens, which comes from the caches; lanes of a column without a
 // token read nothing and their results are dropped.
+//   Bound by reading the weights: 64 tokens on 64 experts of 7168/2048 take
+// 322 us for the 1.88 GB of gate and up rows and 190 us for the 0.94 GB of down
+// rows (whose tokens are two halves, and whose pairs leave as fp32 rows); bare
+// reads in the same pattern take 300 and 148, and reads of whole lines or
+// copies into LDS no less.  Two row tiles: 351 and 228.  A chunk loaded ahead
+// in registers, and work-groups that run through the items with the next one's
+// first chunk under way: the same to 10 % slower (fewer work-groups fit).
 // ----------------------------------------------------------------------------
-
-constexpr int kTiles = 4;  // row tiles of a work-group
+constexpr int kTiles = 4;
 
 // A 128-wide chunk.  NB: activation arrays whose sum is multiplied (x, or hi
 // and lo).
-template <int NT, int NB>
+template <int NB>
 struct Chunk {
-    uint4 w[NT][2];
+    uint4 w[kTiles][2];
     uint4 b[NB][4];
     float s[2];  // block scales of the first and of the last half of the row tiles
 };
 
 // Where a work-group's chunks come from.
-template <int NT, int NB>
+template <int NB>
 struct Operands {
-    const uint8_t* w[NT];
+    const uint8_t* w[kTiles];
     const uint16_t* b[NB];
     const float* s[2];
     uint32_t row_offset;  // of the lane in a row tile
     bool live;            // the lane's column has a token
 };
 
-template <int NT, int NB>
-__device__ __forceinline__ void load_chunk(Chunk<NT, NB>& c, const Operands<NT, NB>& o, int kb) {
+template <int NB>
+__device__ __forceinline__ void load_chunk(Chunk<NB>& c, const Operands<NB>& o, int kb) {
     const int64_t k = 128 * (int64_t)kb;
     c.s[0] = o.s[0][kb];
     c.s[1] = o.s[1][kb];
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < kTiles; ++t)
 #pragma unroll
         for (int j = 0; j < 2; ++j) c.w[t][j] = *reinterpret_cast<const uint4*>(o.w[t] + k + 64 * j + o.row_offset);
     if (!o.live) return;
@@ -228,10 +234,10 @@ __device__ __forceinline__ void load_chunk(Chunk<NT, NB>& c, const Operands<NT, 
             c.b[n][j] = *reinterpret_cast<const uint4*>(o.b[n] + k + (NB == 2 ? 32 * j : 64 * (j >> 1) + 8 * (j & 1)));
 }
 
-template <int NT, int NB>
-__device__ __forceinline__ void multiply_chunk(v4f (&acc)[NT], const Chunk<NT, NB>& c) {
+template <int NB>
+__device__ __forceinline__ void multiply_chunk(v4f (&acc)[kTiles], const Chunk<NB>& c) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
+    for (int t = 0; t < kTiles; ++t) {
         v4f p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -242,7 +248,7 @@ __device__ __forceinline__ void multiply_chunk(v4f (&acc)[NT], const Chunk<NT, N
                 p = mfma(w1, __builtin_bit_cast(v8bf, c.b[n][2 * j + 1]), p);
             }
         }
-        const float s = c.s[2 * t / NT];
+        const float s = c.s[2 * t / kTiles];
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[t][i] = __builtin_fmaf(p[i], s, acc[t][i]);
     }
@@ -250,28 +256,27 @@ __device__ __forceinline__ void multiply_chunk(v4f (&acc)[NT], const Chunk<NT, N
 
 // Sums over the chunks wave, wave+4, ..., joined over the waves in LDS:
 // [wave][row tile][token column * 16 + row].
-template <int NT, int NB>
-__device__ __forceinline__ void multiply(float (*sums)[NT][256], const Operands<NT, NB>& o, int chunks, int wave) {
-    v4f acc[NT];
+template <int NB>
+__device__ __forceinline__ void multiply(float (*sums)[kTiles][256], const Operands<NB>& o, int chunks, int wave) {
+    v4f acc[kTiles];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
-    Chunk<NT, NB> c;
+    for (int t = 0; t < kTiles; ++t) acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
+    Chunk<NB> c;
 #pragma unroll
     for (int n = 0; n < NB; ++n)
 #pragma unroll
         for (int j = 0; j < 4; ++j) c.b[n][j] = make_uint4(0, 0, 0, 0);
     for (int kb = wave; kb < chunks; kb += 4) {
-        load_chunk<NT, NB>(c, o, kb);
-        multiply_chunk<NT, NB>(acc, c);
+        load_chunk<NB>(c, o, kb);
+        multiply_chunk<NB>(acc, c);
     }
     const int lane = threadIdx.x & 63;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) *reinterpret_cast<v4f*>(&sums[wave][t][16 * (lane & 15) + 4 * (lane >> 4)]) = acc[t];
+    for (int t = 0; t < kTiles; ++t) *reinterpret_cast<v4f*>(&sums[wave][t][16 * (lane & 15) + 4 * (lane >> 4)]) = acc[t];
     __syncthreads();
 }
 
-template <int NT>
-__device__ __forceinline__ float sum_waves(const float (*s)[NT][256], int t, int at) {
+__device__ __forceinline__ float sum_waves(const float (*s)[kTiles][256], int t, int at) {
     return (s[0][t][at] + s[1][t][at]) + (s[2][t][at] + s[3][t][at]);
 }
 
@@ -326,9 +331,9 @@ __device__ __forceinline__ Chosen choose(const MoeArgs& a, const MoeLayout& L, c
 // Gate and up projections with the SwiGLU.  PL > 0: every work-group routes
 // the (few) tokens for itself, and the first one leaves the result for the
 // kernels that follow; PL == 0: routing has run.
-template <int NT, int PL>
+template <int PL>
 __global__ __launch_bounds__(256, 4) void moe_up_kernel(MoeArgs a, MoeLayout L) {
-    __shared__ __align__(16) float s_sums[4][NT][256];
+    __shared__ __align__(16) float s_sums[4][kTiles][256];
     __shared__ int s_token[kMaxTokens], s_pair[kMaxTokens];
     __shared__ uint64_t s_sets[PL > 0 ? kFusedTokens * PL : 1];
     __shared__ int s_count[kFusedTokens];
@@ -353,14 +358,14 @@ __global__ __launch_bounds__(256, 4) void moe_up_kernel(MoeArgs a, MoeLayout L) 
     __syncthreads();
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, kq = lane >> 4;
-    constexpr int kCols = 8 * NT;  // columns of h
+    constexpr int kCols = 8 * kTiles;  // columns of h
     const int64_t row0 = (int64_t)blockIdx.x * kCols;
-    Operands<NT, 1> o;
+    Operands<1> o;
     const uint8_t* w = a.w_gu + e.expert * a.w_gu_stride + row0 * a.ldw_gu;
 #pragma unroll
-    for (int t = 0; t < NT / 2; ++t) {
+    for (int t = 0; t < kTiles / 2; ++t) {
         o.w[t] = w + 16 * t * a.ldw_gu;
-        o.w[NT / 2 + t] = w + (a.inner + 16 * t) * a.ldw_gu;
+        o.w[kTiles / 2 + t] = w + (a.inner + 16 * t) * a.ldw_gu;
     }
     o.row_offset = (uint32_t)(r * a.ldw_gu) + 16 * kq;
     o.s[0] = a.s_gu + e.expert * a.s_gu_stride + (row0 >> 7) * a.lds_gu;
@@ -368,8 +373,8 @@ __global__ __launch_bounds__(256, 4) void moe_up_kernel(MoeArgs a, MoeLayout L) 
     for (int t0 = 0; t0 < e.count; t0 += 16) {
         o.live = t0 + r < e.count;
         o.b[0] = a.x + (o.live ? s_token[t0 + r] : 0) * a.ldx + 16 * kq;
-        multiply<NT, 1>(s_sums, o, (int)(a.hidden >> 7), wave);
-        constexpr int kPer = NT / 2;  // columns of a thread
+        multiply<1>(s_sums, o, (int)(a.hidden >> 7), wave);
+        constexpr int kPer = kTiles / 2;  // columns of a thread
         const int tok = threadIdx.x >> 4, c = kPer * (threadIdx.x & 15);
         if (t0 + tok < e.count) {
             const int64_t pair = s_pair[t0 + tok];
@@ -380,10 +385,11 @@ __global__ __launch_bounds__(256, 4) void moe_up_kernel(MoeArgs a, MoeLayout L) 
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
                 const int in = tok * 16 + (c & 15) + i;
-                const float g = sum_waves<NT>(s_sums, c >> 4, in), u = sum_waves<NT>(s_sums, NT / 2 + (c >> 4), in);
+                const float g = sum_waves(s_sums, c >> 4, in), u = sum_waves(s_sums, kTiles / 2 + (c >> 4), in);
                 h[i] = g / (1.0f + expf(-g)) * u * p;
                 hi[i] = (uint16_t)pack_bf16(h[i], 0.0f);
-                lo[i] = (uint16_t)pack_bf16(h[i] - bf16_bits_to_f32(hi[i]), 0.0f);
+                const float rest = h[i] - bf16_bits_to_f32(hi[i]);
+                lo[i] = (hi[i] & 0x7f80u) == 0x7f80u ? 0 : (uint16_t)pack_bf16(rest, 0.0f);  // inf has no rest
             }
             uint16_t* to_hi = reinterpret_cast<uint16_t*>(ws + L.hi) + at;
             uint16_t* to_lo = reinterpret_cast<uint16_t*>(ws + L.lo) + at;
@@ -398,9 +404,8 @@ __global__ __launch_bounds__(256, 4) void moe_up_kernel(MoeArgs a, MoeLayout L) 
 }
 
 // Down projection: one fp32 row of the hidden size per pair.
-template <int NT>
 __global__ __launch_bounds__(256, 4) void moe_down_kernel(MoeArgs a, MoeLayout L) {
-    __shared__ __align__(16) float s_sums[4][NT][256];
+    __shared__ __align__(16) float s_sums[4][kTiles][256];
     __shared__ int s_token[kMaxTokens], s_pair[kMaxTokens];
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     const Chosen e = choose(a, L, sets_of(a, L), blockIdx.y, s_token, s_pair);
@@ -408,12 +413,12 @@ __global__ __launch_bounds__(256, 4) void moe_down_kernel(MoeArgs a, MoeLayout L
     __syncthreads();
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, kq = lane >> 4;
-    constexpr int kRows = 16 * NT;
+    constexpr int kRows = 16 * kTiles;
     const int64_t row0 = (int64_t)blockIdx.x * kRows;
-    Operands<NT, 2> o;
+    Operands<2> o;
     const uint8_t* w = a.w_down + e.expert * a.w_down_stride + row0 * a.ldw_down;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) o.w[t] = w + 16 * t * a.ldw_down;
+    for (int t = 0; t < kTiles; ++t) o.w[t] = w + 16 * t * a.ldw_down;
     o.row_offset = (uint32_t)(r * a.ldw_down) + 16 * kq;
     o.s[0] = o.s[1] = a.s_down + e.expert * a.s_down_stride + (row0 >> 7) * a.lds_down;
     for (int t0 = 0; t0 < e.count; t0 += 16) {
@@ -421,11 +426,11 @@ __global__ __launch_bounds__(256, 4) void moe_down_kernel(MoeArgs a, MoeLayout L
         const int64_t from = (int64_t)(o.live ? s_pair[t0 + r] : 0) * a.inner + 8 * kq;
         o.b[0] = reinterpret_cast<const uint16_t*>(ws + L.hi) + from;
         o.b[1] = reinterpret_cast<const uint16_t*>(ws + L.lo) + from;
-        multiply<NT, 2>(s_sums, o, (int)(a.inner >> 7), wave);
+        multiply<2>(s_sums, o, (int)(a.inner >> 7), wave);
         const int c = threadIdx.x % kRows;
         for (int tok = threadIdx.x / kRows; tok < 16 && t0 + tok < e.count; tok += 256 / kRows)
             reinterpret_cast<float*>(ws + L.parts)[s_pair[t0 + tok] * a.hidden + row0 + c] =
-                sum_waves<NT>(s_sums, c >> 4, tok * 16 + (c & 15));
+                sum_waves(s_sums, c >> 4, tok * 16 + (c & 15));
         __syncthreads();
     }
 }
@@ -588,10 +593,10 @@ template <int PL>
 void launch_up(const MoeArgs& a, const MoeLayout& L, bool fused, hipStream_t st) {
     const dim3 grid((unsigned)(a.inner / (8 * kTiles)), (unsigned)L.slots);
     if (fused) {
-        hipLaunchKernelGGL((moe_up_kernel<kTiles, PL>), grid, dim3(256), 0, st, a, L);
+        hipLaunchKernelGGL((moe_up_kernel<PL>), grid, dim3(256), 0, st, a, L);
     } else {
         hipLaunchKernelGGL(moe_route_kernel<PL>, dim3((unsigned)a.tokens), dim3(64), 0, st, a, L);
-        hipLaunchKernelGGL((moe_up_kernel<kTiles, 0>), grid, dim3(256), 0, st, a, L);
+        hipLaunchKernelGGL((moe_up_kernel<0>), grid, dim3(256), 0, st, a, L);
     }
 }
 
@@ -617,7 +622,7 @@ hipError_t launch_moe_decode(const MoeArgs& a, hipStream_t st) {
     if (a.tokens <= kFewTokens && L.slots * 16 * a.inner <= 1 << 18) {
         hipLaunchKernelGGL(moe_down_few_kernel, dim3((unsigned)(a.hidden / 16)), dim3(64 * kFewWaves), 0, st, a, L);
     } else {
-        hipLaunchKernelGGL(moe_down_kernel<kTiles>, dim3((unsigned)(a.hidden / (16 * kTiles)), (unsigned)L.slots),
+        hipLaunchKernelGGL(moe_down_kernel, dim3((unsigned)(a.hidden / (16 * kTiles)), (unsigned)L.slots),
                            dim3(256), 0, st, a, L);
         hipLaunchKernelGGL(moe_join_kernel, dim3((unsigned)((a.hidden + 255) / 256), (unsigned)a.tokens), dim3(256), 0,
                            st, a, L);
