@@ -237,9 +237,9 @@ __global__ __launch_bounds__(512, 4) void swiglu_backward_quantize_kernel(Swiglu
     // than whole rows of tiles or whole columns).
     const uint32_t band = blockIdx.y / 8, height = min(8u, gridDim.y - 8 * band);
     const uint32_t in_band = blockIdx.y % 8 * gridDim.x + blockIdx.x;
-    const int64_t tile_c = in_band / height, tile_r = 8 * band + in_band % height;
-    const int64_t r0 = tile_r * 128, c0 = tile_c * 128;
-    const int64_t c = c0 + 8 * cg, row = r0 + kRows * rg;
+    const uint32_t tile_c = in_band / height, tile_r = 8 * band + in_band % height;
+    const uint32_t r0 = tile_r * 128, c0 = tile_c * 128;  // below 2^31: 32 bits spare registers here
+    const uint32_t c = c0 + 8 * cg, row = r0 + kRows * rg;
     const bool full = r0 + 128 <= a.rows && c0 + 128 <= a.cols;
 
     Raw8<T> raw[kRows];
@@ -308,7 +308,7 @@ __global__ __launch_bounds__(512, 4) void swiglu_backward_quantize_kernel(Swiglu
         const TileScale ts = make_scale_mode<POW2>(mine);
         s_row[wave][rg & 3][cg] = make_float2(ts.s, ts.r);
         my_fast = ts.fast;
-        const int64_t r = row + (cg & (kRows - 1));
+        const uint32_t r = row + (cg & (kRows - 1));
         if (r < a.rows) (cg < kRows ? a.sdg : a.sdu)[tile_c * a.ldsd + r] = ts.s;
     }
     wave_lds_sync();
@@ -364,7 +364,7 @@ __global__ __launch_bounds__(512, 4) void swiglu_backward_quantize_kernel(Swiglu
     __syncthreads();
     // thread t: columns t/8 and t/8 + 64, tokens 16*(t%8) .. +15 of the tile
     const int unit = t & 7;
-    const int64_t tok = r0 + 16 * unit;
+    const uint32_t tok = r0 + 16 * unit;
 #pragma unroll
     for (int m = 0; m < 3; ++m) {
         uint8_t* qt = m == 0 ? a.qdgt : m == 1 ? a.qdut : a.qht;
