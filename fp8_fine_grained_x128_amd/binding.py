@@ -281,12 +281,13 @@ def _ld(t: torch.Tensor) -> int:
     """Row stride in elements.  A single-row tensor may carry any stride (its
     row stride never multiplies a nonzero index), so report the smallest value
     that satisfies the library's 16-byte rule for that dtype."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (shape[1] > 1 and stride[1] != 1):
         raise ValueError("expected a 2-D tensor with unit column stride")
-    if t.shape[0] <= 1:
+    if shape[0] <= 1:
         per16 = max(1, 16 // t.element_size())
-        return max(per16, -(-t.shape[1] // per16) * per16)
-    return t.stride(0)
+        return max(per16, -(-shape[1] // per16) * per16)
+    return stride[0]
 
 
 def _on_device(what: str, *ts: torch.Tensor) -> None:
@@ -566,8 +567,8 @@ def layernorm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Optio
     _check(fp8q_layernorm(x.data_ptr(), _dtype_code(x), rows, cols, _ld(x), _ptr(gamma), _ptr(beta),
                           _dtype_code(given[0]) if given else FP8Q_F32, eps, kind, _ptr(y),
                           FP8Q_F32 if y is None else _dtype_code(y), 0 if y is None else _ld(y), _ptr(q),
-                          0 if q is None else _ld(q), _ptr(s), 0 if s is None else max(s.stride(0), 1), scale_mode,
-                          _ptr(mean), rstd.data_ptr(), _stream()), "fp8q_layernorm")
+                          0 if q is None else _pad16(max(cols, 1)), _ptr(s), max(rows, 1), scale_mode, _ptr(mean),
+                          rstd.data_ptr(), _stream()), "fp8q_layernorm")
     return LayernormOut(q, s, y, mean, rstd)
 
 
@@ -647,18 +648,20 @@ def swiglu_quantize(g: torch.Tensor, u: torch.Tensor, checkpoint: bool = True, s
     and u or None).  g and u are the halves of a fused product, or two tensors with the same row stride."""
     _like("swiglu_quantize", "u", u, g)
     rows, cols = g.shape
-    if _ld(g) != _ld(u):
-        raise ValueError(f"swiglu_quantize: row strides {_ld(g)} and {_ld(u)} differ")
+    ldgu = _ld(g)
+    if ldgu != _ld(u):
+        raise ValueError(f"swiglu_quantize: row strides {ldgu} and {_ld(u)} differ")
     _on_device("swiglu_quantize", g, u)
     dev, groups = g.device, _cdiv(cols, 128)
     qh, sh = _codes(rows, cols, dev), _scales(groups, rows, dev)
     kept = None
     if checkpoint:
         kept = SwigluCheckpoint(*_pair(rows, cols, 16, torch.uint8, dev), *_stack(groups, rows, torch.float32, dev))
-    _check(fp8q_swiglu_quantize(g.data_ptr(), u.data_ptr(), _dtype_code(g), _ld(g), rows, cols, qh.data_ptr(), _ld(qh),
-                                sh.data_ptr(), max(rows, 1), *((None, None, 0, None, None, 0) if kept is None else
-                                                               (kept.qg.data_ptr(), kept.qu.data_ptr(), _ld(kept.qg),
-                                                                kept.sg.data_ptr(), kept.su.data_ptr(), max(rows, 1))),
+    _check(fp8q_swiglu_quantize(g.data_ptr(), u.data_ptr(), _dtype_code(g), ldgu, rows, cols, qh.data_ptr(),
+                                _pad16(max(cols, 1)), sh.data_ptr(), max(rows, 1),
+                                *((None, None, 0, None, None, 0) if kept is None else
+                                  (kept.qg.data_ptr(), kept.qu.data_ptr(), _ld(kept.qg), kept.sg.data_ptr(),
+                                   kept.su.data_ptr(), max(rows, 1))),
                                 scale_mode, _stream()), "fp8q_swiglu_quantize")
     return qh, sh, kept
 

@@ -139,7 +139,7 @@ __device__ __forceinline__ void finish_groups(const LayernormArgs& a, const Raw8
             if (a.y_dtype == kDtypeBF16)
                 store_values8<NT>(static_cast<uint16_t*>(a.y) + row * a.ldy, c, a.cols, v[i]);
             else
-                store_values8<NT>(static_cast<float*>(a.y) + row * a.ldy, c, a.cols, v[i]);
+                store_values8(static_cast<float*>(a.y) + row * a.ldy, c, a.cols, v[i]);
         }
         if (a.q) {
             const uint32_t m = row_max_u32(amax8(v[i]));
@@ -238,9 +238,10 @@ __device__ __forceinline__ void fill_weights(LdsWeights<N>& to, const void* w, i
 // the weights in LDS; a team loads its next row before it works on the current
 // one.  A work-group's rows are consecutive, so the scales that it writes fill
 // whole lines.  Many rows, or narrow ones.  G work-groups are meant to share a
-// compute unit.  (8192x7168 bf16 with codes and values: 60 us, 67 without the
-// non-temporal stores of y; a wave per row needs over 200 registers there and
-// took 85, a work-group per row reads the weights again for every row, 88.)
+// compute unit.  (8192x7168 with codes and values: bf16 60 us, 67 without the
+// non-temporal stores of y; fp32 112 us, 131 with such stores.  bf16: a wave
+// per row needs over 200 registers there and took 85, a work-group per row
+// reads the weights again for every row, 88.)
 constexpr int kTeamThreads = 512;
 
 template <typename T, int N, int I, int G, bool LAYER, bool POW2>
@@ -338,7 +339,7 @@ __global__ __launch_bounds__(1024, 4) void layernorm_backward_kernel(LayernormBa
 #pragma unroll
         for (int i = 0; i < I; ++i) {
             raw[i].zero();
-            if (row < a.rows) load_row8(raw[i], static_cast<const T*>(p) + row * ld, 8 * (t + N * i), cols, false);
+            if (row < a.rows) load_row8<T, sizeof(T) == 2>(raw[i], static_cast<const T*>(p) + row * ld, 8 * (t + N * i), cols, false);
         }
     };
     float dgamma[I][8], dbeta[I][8];
@@ -524,13 +525,14 @@ void launch_teams(const LayernormArgs& a, hipStream_t st) {
 // each.  Registers and LDS decide how many work-groups share a compute unit.
 template <typename T>
 void launch_forward_for(const LayernormArgs& a, hipStream_t st) {
+    constexpr int kShare = sizeof(T) == 2 ? 3 : 2;
     const bool many = a.rows >= 8 * (int64_t)compute_units();
     if (a.cols <= 128) launch_teams<T, 16, 1, 4>(a, st);
     else if (a.cols <= 512) launch_teams<T, 64, 1, 4>(a, st);
-    else if (a.cols <= 1024 && many) launch_teams<T, 64, 2, 3>(a, st);
+    else if (a.cols <= 1024 && many) launch_teams<T, 64, 2, kShare>(a, st);
     else if (a.cols <= 2048 && many) launch_teams<T, 64, 4, 2>(a, st);
     else if (a.cols <= 2048) launch_row<T, 4, 1>(a, st);
-    else if (a.cols <= 4096 && many) launch_teams<T, 256, 2, 3>(a, st);
+    else if (a.cols <= 4096 && many) launch_teams<T, 256, 2, kShare>(a, st);
     else if (a.cols <= 8192 && many) launch_teams<T, 256, 4, 2>(a, st);
     else if (a.cols <= 8192) launch_row<T, 16, 1>(a, st);
     else launch_row<T, 16, 2>(a, st);

@@ -196,7 +196,7 @@ __global__ __launch_bounds__(256) void swiglu_backward_kernel(SwigluBackwardArgs
     if (c >= a.cols) return;
     float g[8], u[8], dh[8], dg[8], du[8];
     Raw8<T> raw;
-    load_row8(raw, static_cast<const T*>(a.dh) + row * a.lddh, c, a.cols, false);
+    load_row8<T, sizeof(T) == 2>(raw, static_cast<const T*>(a.dh) + row * a.lddh, c, a.cols, false);
     raw.values(dh);
     decode8(load_codes8(a.qg + row * a.ldq, c, a.cols), a.sg[(c >> 7) * a.lds + row], g);
     decode8(load_codes8(a.qu + row * a.ldq, c, a.cols), a.su[(c >> 7) * a.lds + row], u);

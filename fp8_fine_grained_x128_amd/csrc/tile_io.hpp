@@ -157,7 +157,12 @@ struct Raw8<float> {
 };
 
 // Loads x[c .. c+8) of a row; elements at or beyond `valid` read as 0.
-// `full` (wave-uniform) says that all 8 are valid.
+// `full` (wave-uniform) says that all 8 are valid.  NT marks the loads
+// non-temporal: right for a lane's 8 bf16 values, one load whose neighbours
+// complete the line; 8 fp32 values are two loads of half a line's bytes each,
+// and where such a kernel waits for memory alone the caches serve the second
+// (layer-norm backward 179 us against 189, SwiGLU backward 153 against 159,
+// both 8192x7168 fp32; the forward kernels are as fast or slower with it).
 template <typename T, bool NT = true>
 __device__ __forceinline__ void load_row8(Raw8<T>& r, const T* row, int64_t c, int64_t valid, bool full) {
     if (full || c + 8 <= valid)
@@ -188,18 +193,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 }
 
 // Stores 8 values of a row at p[c .. c+8), clipped to `valid`; bf16 rows get
-// the nearest-even rounding.  NT marks the store non-temporal.
-template <bool NT = false>
-__device__ __forceinline__ void store16(void* p, uint4 v) {
-    if constexpr (NT) store16_nt(p, v);
-    else *reinterpret_cast<uint4*>(p) = v;
-}
-
-template <bool NT = false>
+// the nearest-even rounding.  NT marks the store non-temporal (a lane's fp32
+// values are two stores, each of half the bytes of every line: those go
+// through the caches).
 __device__ __forceinline__ void store_values8(float* p, int64_t c, int64_t valid, const float v[8]) {
     if (c + 8 <= valid) {
-        store16<NT>(p + c, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
-        store16<NT>(p + c + 4, make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])));
+        *reinterpret_cast<float4*>(p + c) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4*>(p + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -211,7 +211,9 @@ template <bool NT = false>
 __device__ __forceinline__ void store_values8(uint16_t* p, int64_t c, int64_t valid, const float v[8]) {
     const uint32_t w[4] = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
     if (c + 8 <= valid) {
-        store16<NT>(p + c, make_uint4(w[0], w[1], w[2], w[3]));
+        const uint4 v4 = make_uint4(w[0], w[1], w[2], w[3]);
+        if constexpr (NT) store16_nt(p + c, v4);
+        else *reinterpret_cast<uint4*>(p + c) = v4;
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
