@@ -307,7 +307,7 @@ inline int swiglu_backward_quantize(const void* qg, const void* qu, int64_t ldq,
         ldqt % 16 != 0 || !aligned(qht, 16) || ldqht % 16 != 0 || !aligned(sdg, 4) || !aligned(sdu, 4) ||
         !aligned(sdgt, 4) || !aligned(sdut, 4) || !aligned(sht, 4))
         return FP8Q_EALIGN;
-    if (cdiv(rows, 128) > kMaxGridY) return FP8Q_EUNSUPPORTED;
+    if (cdiv(rows, 128) > kMaxGridY || cols >= (int64_t(1) << 30)) return FP8Q_EUNSUPPORTED;  // 2^32 threads along x
     return kLaunch;
 }
 

@@ -96,6 +96,8 @@ def test_swiglu_backward_quantize():
     for kw, status in IN_BAD + more:
         assert c(**kw) == status, kw
     assert c(rows=65536 * 128, lds=1 << 23, ldsd=1 << 23, ldqt=1 << 23, ldqht=1 << 23) == f.FP8Q_EUNSUPPORTED
+    wide = dict(ldq=1 << 30, lddh=1 << 30, ldqd=1 << 30, ldst=1 << 30, ldsht=1 << 30)
+    assert c(cols=1 << 30, **wide) == f.FP8Q_EUNSUPPORTED
     assert c(rows=0) == f.FP8Q_OK
 
 

@@ -191,3 +191,22 @@ def test_rows_past_32_bit_offsets(fp8q):
     a = fp8q.layernorm_backward(d, x, None, far.mean, far.rstd)
     b = fp8q.layernorm_backward(d, v, None, near.mean, near.rstd)
     assert all(torch.equal(i, j) for i, j in zip(a, b))
+
+
+def test_more_rows_than_one_grid_dimension_holds(fp8q):
+    """Wide rows with a work-group of 1024 threads each, past the 2^32 threads of one grid dimension."""
+    say("layernorm: 2^22 + 3 rows")
+    rows, cols = (1 << 22) + 3, 8200
+    if torch.cuda.mem_get_info()[0] < 130 << 30:
+        pytest.skip("needs 130 GB of device memory")
+    x = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")
+    ends = [0, (1 << 20) - 1, 1 << 20, (1 << 22) - 1, 1 << 22, rows - 1]
+    some = torch.randn((len(ends), cols), generator=torch.Generator().manual_seed(5)).to(x)
+    x[ends] = some
+    big, few = fp8q.layernorm(x), fp8q.layernorm(some)
+    for name in ("q", "mean", "rstd"):
+        assert torch.equal(getattr(big, name)[ends], getattr(few, name)), name
+    assert torch.equal(big.s[:, ends], few.s)
+    assert not big.q[1].any() and float(big.rstd[1]) == pytest.approx(1e-5 ** -0.5)
+    del x, big
+    torch.cuda.empty_cache()
