@@ -5,9 +5,10 @@ Two layers, both argument marshalling only:
 * ``fp8q_*`` functions with the C names and C argument lists (device pointers
   as Python ints, ``stream`` as an int handle or None);
 * tensor helpers (``quantize_act``, ``quantize_weight``, ``requant_transpose``,
-  ``gemm``, ``grouped_gemm``) that take torch tensors on the HIP device,
-  allocate outputs with torch, derive leading dimensions from strides and
-  enqueue on torch's current stream.
+  ``gemm``, ``grouped_gemm``; ``layernorm``, ``swiglu_quantize``, their backward
+  passes and ``moe_decode``) that take torch tensors on the HIP device,
+  allocate outputs and workspaces with torch, derive leading dimensions from
+  strides and enqueue on torch's current stream.
 
 Every computation runs in the library's HIP kernels.  If the library is not
 built, importing this module raises: there is no fallback.

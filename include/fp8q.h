@@ -31,8 +31,9 @@
  * Conventions for every entry point:
  *   - all data pointers are DEVICE pointers owned by the caller; the library
  *     never allocates, frees or keeps a pointer after the call returns (the
- *     one kernel that needs scratch memory, split-K, takes it from the
- *     caller as a workspace argument);
+ *     calls that need scratch memory, split-K, the norm's backward pass and
+ *     the mixture-of-experts layer, take it from the caller as a workspace
+ *     argument);
  *   - `stream` is a hipStream_t (NULL = the null stream); work is enqueued
  *     asynchronously on it and the call returns without synchronizing;
  *   - arguments are validated on the host before anything is enqueued; on
@@ -42,7 +43,8 @@
  *   - base pointers of code and input arrays must be 16-byte aligned and
  *     leading dimensions of code/input arrays multiples of 16 bytes; scale
  *     arrays need 4-byte alignment only;
- *   - empty problems (a zero dimension) are valid and launch nothing;
+ *   - empty problems (a zero dimension) are valid and launch nothing
+ *     (fp8q_layernorm_backward of no rows clears the sums it was asked for);
  *   - calls hold no global mutable state and may be made from several host
  *     threads; calls on one stream execute in order;
  *   - a call enqueues kernel launches only (no memset, copy or host
