@@ -325,7 +325,7 @@ def _codes(rows: int, cols: int, device) -> torch.Tensor:
     """uint8 [rows][cols] with a 16-byte-multiple row stride."""
     ld = _pad16(max(cols, 1))
     buf = torch.empty((rows, ld), dtype=torch.uint8, device=device)
-    return buf if ld == cols else buf[:, :cols]
+    return buf if ld == cols else buf.as_strided((rows, cols), (ld, 1))
 
 
 def _cdiv(a: int, b: int) -> int:
@@ -504,7 +504,7 @@ def _rows(rows: int, cols: int, dtype: torch.dtype, device) -> torch.Tensor:
     per16 = 16 // dtype.itemsize
     ld = _cdiv(max(cols, 1), per16) * per16
     buf = torch.empty((rows, ld), dtype=dtype, device=device)
-    return buf if ld == cols else buf[:, :cols]
+    return buf if ld == cols else buf.as_strided((rows, cols), (ld, 1))
 
 
 def _scales(groups: int, n: int, device) -> torch.Tensor:
@@ -623,24 +623,19 @@ class SwigluCheckpoint(NamedTuple):
     su: torch.Tensor
 
 
-def _half(both: torch.Tensor, offset: int, rows: int, cols: int) -> torch.Tensor:
-    return both.as_strided((rows, cols), (both.shape[1], 1), offset)
-
-
-def _pair(rows: int, cols: int, multiple: int, dtype: torch.dtype, device) -> Tuple[torch.Tensor, torch.Tensor]:
-    """Two [rows][cols] halves with one row stride: side by side in one buffer if cols % multiple == 0, else in
-    buffers of their own."""
-    if cols % multiple == 0:
-        both = torch.empty((rows, 2 * cols), dtype=dtype, device=device)
-        return _half(both, 0, rows, cols), _half(both, cols, rows, cols)
-    return _rows(rows, cols, dtype, device), _rows(rows, cols, dtype, device)
+def _pair(rows: int, cols: int, dtype: torch.dtype, device) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Two [rows][cols] halves side by side in one buffer, each row of a half on 16 bytes."""
+    per16 = 16 // dtype.itemsize
+    ld = _cdiv(max(cols, 1), per16) * per16
+    both = torch.empty((rows, 2 * ld), dtype=dtype, device=device)
+    return both.as_strided((rows, cols), (2 * ld, 1)), both.as_strided((rows, cols), (2 * ld, 1), ld)
 
 
 def _stack(groups: int, n: int, dtype: torch.dtype, device) -> Tuple[torch.Tensor, torch.Tensor]:
     """Two [groups][n] halves, one below the other, row stride a multiple of 16 bytes for codes."""
     ld = n if dtype == torch.float32 else _pad16(max(n, 1))
     both = torch.empty((2 * groups, ld), dtype=dtype, device=device)
-    return _half(both, 0, groups, n), _half(both, groups * ld, groups, n)
+    return both.as_strided((groups, n), (ld, 1)), both.as_strided((groups, n), (ld, 1), groups * ld)
 
 
 def swiglu_quantize(g: torch.Tensor, u: torch.Tensor, checkpoint: bool = True, scale_mode: int = FP8Q_SCALE_FP32
@@ -657,7 +652,7 @@ def swiglu_quantize(g: torch.Tensor, u: torch.Tensor, checkpoint: bool = True, s
     qh, sh = _codes(rows, cols, dev), _scales(groups, rows, dev)
     kept = None
     if checkpoint:
-        kept = SwigluCheckpoint(*_pair(rows, cols, 16, torch.uint8, dev), *_stack(groups, rows, torch.float32, dev))
+        kept = SwigluCheckpoint(*_pair(rows, cols, torch.uint8, dev), *_stack(groups, rows, torch.float32, dev))
     _check(fp8q_swiglu_quantize(g.data_ptr(), u.data_ptr(), _dtype_code(g), ldgu, rows, cols, qh.data_ptr(),
                                 _pad16(max(cols, 1)), sh.data_ptr(), max(rows, 1),
                                 *((None, None, 0, None, None, 0) if kept is None else
@@ -668,16 +663,17 @@ def swiglu_quantize(g: torch.Tensor, u: torch.Tensor, checkpoint: bool = True, s
 
 
 def _check_checkpoint(what: str, kept: SwigluCheckpoint, dh: torch.Tensor) -> None:
-    rows, cols = dh.shape
-    for t in (kept.qg, kept.qu):
-        _check_codes(f"{what} checkpoint", t)
-        if tuple(t.shape) != (rows, cols):
-            raise ValueError(f"{what}: checkpoint {tuple(t.shape)}, gradient {tuple(dh.shape)}")
-    for t in (kept.sg, kept.su):
-        _check_scales(f"{what} checkpoint scales (layout [ceil(cols/128)][rows])", t, _cdiv(cols, 128), rows)
-    if _ld(kept.qg) != _ld(kept.qu) or (kept.sg.shape[0] > 1 and kept.sg.stride(0) != kept.su.stride(0)):
+    rows, cols = shape = dh.shape
+    qg, qu, sg, su = kept
+    for t in (qg, qu):
+        _check_codes(what, t)
+        if t.shape != shape:
+            raise ValueError(f"{what}: checkpoint {tuple(t.shape)}, gradient {tuple(shape)}")
+    for t in (sg, su):
+        _check_scales(what, t, _cdiv(cols, 128), rows)
+    if _ld(qg) != _ld(qu) or (sg.shape[0] > 1 and sg.stride(0) != su.stride(0)):
         raise ValueError(f"{what}: the strides of the checkpoint's halves differ")
-    _on_device(what, *kept, dh)
+    _on_device(what, qg, qu, sg, su, dh)
 
 
 def _checkpoint_args(kept: SwigluCheckpoint, dh: torch.Tensor) -> tuple:
@@ -687,11 +683,11 @@ def _checkpoint_args(kept: SwigluCheckpoint, dh: torch.Tensor) -> tuple:
 
 
 def swiglu_backward(kept: SwigluCheckpoint, dh: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
-    """(dg, du) of the SwiGLU at the checkpoint's values, in dh's dtype; halves of one buffer [rows][2*cols] where
-    cols allows it."""
+    """(dg, du) of the SwiGLU at the checkpoint's values, in dh's dtype; halves of one buffer (of [rows][2*cols] where
+    cols * dtype is a multiple of 16 bytes)."""
     _check_checkpoint("swiglu_backward", kept, dh)
     rows, cols = dh.shape
-    dg, du = _pair(rows, cols, 16 // dh.element_size(), dh.dtype, dh.device)
+    dg, du = _pair(rows, cols, dh.dtype, dh.device)
     _check(fp8q_swiglu_backward(*_checkpoint_args(kept, dh), dg.data_ptr(), du.data_ptr(), _ld(dg), _stream()),
            "fp8q_swiglu_backward")
     return dg, du
@@ -733,13 +729,12 @@ def swiglu_backward_quantize(kept: SwigluCheckpoint, dh: torch.Tensor, scale_mod
     dev, groups, tgroups = dh.device, _cdiv(cols, 128), _cdiv(rows, 128)
     ns, nt = groups * rows, tgroups * cols  # scales of one 1x128 and one 128x1 array
     scales = torch.empty(2 * ns + 3 * nt, dtype=torch.float32, device=dev)
-    o = SwigluGrads(*_pair(rows, cols, 16, torch.uint8, dev), scales.as_strided((groups, rows), (rows, 1)),
+    o = SwigluGrads(*_pair(rows, cols, torch.uint8, dev), scales.as_strided((groups, rows), (rows, 1)),
                     scales.as_strided((groups, rows), (rows, 1), ns), *_stack(cols, rows, torch.uint8, dev),
                     scales.as_strided((tgroups, cols), (2 * cols, 1), 2 * ns),
                     scales.as_strided((tgroups, cols), (2 * cols, 1), 2 * ns + cols), _codes(cols, rows, dev),
                     scales.as_strided((tgroups, cols), (cols, 1), 2 * ns + 2 * nt))
-    ldq = cols * 2 if cols % 16 == 0 else _ld(o.qdg)
-    ldt = _pad16(max(rows, 1))
+    ldq, ldt = 2 * _pad16(max(cols, 1)), _pad16(max(rows, 1))
     _check(fp8q_swiglu_backward_quantize(*_checkpoint_args(kept, dh), o.qdg.data_ptr(), o.qdu.data_ptr(), ldq,
                                          o.sdg.data_ptr(), o.sdu.data_ptr(), max(rows, 1), o.qdgt.data_ptr(),
                                          o.qdut.data_ptr(), ldt, o.sdgt.data_ptr(), o.sdut.data_ptr(), 2 * cols,
