@@ -180,106 +180,152 @@ __global__ __launch_bounds__(64) void moe_route_kernel(MoeArgs a, MoeLayout L) {
 }
 
 // ----------------------------------------------------------------------------
-// Both projections.  A work-group takes kTiles row tiles of 16 weight rows of
+// Both projections.  A work-group takes TILES row tiles of 16 weight rows of
 // one active expert: rows of the hidden size, or as many tiles of gate rows as
 // of the up rows that belong to them.  Its four waves take every fourth
-// 128-wide chunk of the contraction, for 16 of the expert's tokens at a time,
-// and join their sums in LDS.
+// 128-wide chunk of the contraction, for NG groups of 16 of the expert's
+// tokens at a time, and join their sums in LDS.
 //   Weights go straight from memory to the matrix operand (16 rows of 64
 // contiguous bytes a load), each one read once.  The row tiles share one read
 // of the tokens, which comes from the caches; lanes of a column without a
 // token read nothing and their results are dropped.
 //   Bound by reading the weights: 64 tokens on 64 experts of 7168/2048 take
-// 322 us for the 1.88 GB of gate and up rows and 190 us for the 0.94 GB of down
+// 313 us for the 1.88 GB of gate and up rows and 175 us for the 0.94 GB of down
 // rows (whose tokens are two halves, and whose pairs leave as fp32 rows); bare
 // reads in the same pattern take 300 and 148, and reads of whole lines or
-// copies into LDS no less.  Two row tiles: 351 and 228.  A chunk loaded ahead
-// in registers, and work-groups that run through the items with the next one's
-// first chunk under way: the same to 10 % slower (fewer work-groups fit).
+// copies into LDS no less.  Not faster: a chunk loaded ahead in registers,
+// work-groups that run through the items with the next one's first chunk under
+// way, an expert's work-groups on one XCD (2 % slower), tokens in LDS for waves
+// that share the chunks and split the rows (a barrier per chunk: 60 % slower).
+//   Row tiles and groups trade registers (work-groups per compute unit) for
+// reads of the tokens and of the weights; expert_variant() chooses.
 // ----------------------------------------------------------------------------
-constexpr int kTiles = 4;
 
-// A 128-wide chunk.  NB: activation arrays whose sum is multiplied (x, or hi
-// and lo).
-template <int NB>
-struct Chunk {
-    uint4 w[kTiles][2];
-    uint4 b[NB][4];
+// ----------------------------------------------------------------------------
+// A 128-wide chunk of TILES row tiles.
+template <int TILES>
+struct Weights {
+    uint4 w[TILES][2];
     float s[2];  // block scales of the first and of the last half of the row tiles
 };
 
-// Where a work-group's chunks come from.
+// The same chunk of a lane's token.  NB: activation arrays whose sum is
+// multiplied (x, or hi and lo).
 template <int NB>
-struct Operands {
-    const uint8_t* w[kTiles];
-    const uint16_t* b[NB];
-    const float* s[2];
-    uint32_t row_offset;  // of the lane in a row tile
-    bool live;            // the lane's column has a token
+struct Tokens {
+    uint4 b[NB][4];
 };
 
-template <int NB>
-__device__ __forceinline__ void load_chunk(Chunk<NB>& c, const Operands<NB>& o, int kb) {
+// Where a work-group's chunks come from.
+template <int TILES, int NG>
+struct Operands {
+    const uint8_t* w[TILES];
+    const float* s[2];
+    uint32_t row_offset;    // of the lane in a row tile
+    const uint16_t* b[NG];  // the lane's token in every group; null: none
+    int64_t lo;             // elements from the first to the second activation array
+};
+
+template <int TILES, int NG>
+__device__ __forceinline__ void load_weights(Weights<TILES>& c, const Operands<TILES, NG>& o, int kb) {
     const int64_t k = 128 * (int64_t)kb;
     c.s[0] = o.s[0][kb];
     c.s[1] = o.s[1][kb];
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t)
+    for (int t = 0; t < TILES; ++t)
 #pragma unroll
         for (int j = 0; j < 2; ++j) c.w[t][j] = *reinterpret_cast<const uint4*>(o.w[t] + k + 64 * j + o.row_offset);
-    if (!o.live) return;
+}
+
+// Keeps the codes and not the bf16 values made of them, which take twice the
+// registers, from one group of tokens to the next.
+template <int TILES>
+__device__ __forceinline__ void forget(Weights<TILES>& c) {
+#pragma unroll
+    for (int t = 0; t < TILES; ++t)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            opaque(c.w[t][j].x);
+            opaque(c.w[t][j].y);
+            opaque(c.w[t][j].z);
+            opaque(c.w[t][j].w);
+        }
+}
+
+template <int NB>
+__device__ __forceinline__ void load_tokens(Tokens<NB>& c, const uint16_t* b, int64_t lo, int kb) {
+    if (b == nullptr) return;
+    const int64_t k = 128 * (int64_t)kb;
 #pragma unroll
     for (int n = 0; n < NB; ++n)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            c.b[n][j] = *reinterpret_cast<const uint4*>(o.b[n] + k + (NB == 2 ? 32 * j : 64 * (j >> 1) + 8 * (j & 1)));
+            c.b[n][j] = *reinterpret_cast<const uint4*>(b + n * lo + k + (NB == 2 ? 32 * j : 64 * (j >> 1) + 8 * (j & 1)));
 }
 
-template <int NB>
-__device__ __forceinline__ void multiply_chunk(v4f (&acc)[kTiles], const Chunk<NB>& c) {
+template <int NB, int TILES>
+__device__ __forceinline__ void multiply_chunk(v4f (&acc)[TILES], const Weights<TILES>& c, const Tokens<NB>& x) {
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
+    for (int t = 0; t < TILES; ++t) {
         v4f p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const v8bf w0 = bf16_of_codes(c.w[t][j].x, c.w[t][j].y), w1 = bf16_of_codes(c.w[t][j].z, c.w[t][j].w);
 #pragma unroll
             for (int n = NB - 1; n >= 0; --n) {
-                p = mfma(w0, __builtin_bit_cast(v8bf, c.b[n][2 * j]), p);
-                p = mfma(w1, __builtin_bit_cast(v8bf, c.b[n][2 * j + 1]), p);
+                p = mfma(w0, __builtin_bit_cast(v8bf, x.b[n][2 * j]), p);
+                p = mfma(w1, __builtin_bit_cast(v8bf, x.b[n][2 * j + 1]), p);
             }
         }
-        const float s = c.s[2 * t / kTiles];
+        const float s = c.s[2 * t / TILES];
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[t][i] = __builtin_fmaf(p[i], s, acc[t][i]);
     }
 }
 
-// Sums over the chunks wave, wave+4, ..., joined over the waves in LDS:
-// [wave][row tile][token column * 16 + row].
-template <int NB>
-__device__ __forceinline__ void multiply(float (*sums)[kTiles][256], const Operands<NB>& o, int chunks, int wave) {
-    v4f acc[kTiles];
+// Sums of a wave over its chunks wave, wave+4, ..., for the first `groups`
+// groups of 16 tokens.
+template <int NB, int TILES, int NG>
+__device__ __forceinline__ void multiply(v4f (&acc)[NG][TILES], const Operands<TILES, NG>& o, int chunks, int wave,
+                                         int groups) {
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
-    Chunk<NB> c;
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) acc[g][t] = v4f{0.f, 0.f, 0.f, 0.f};
+    Weights<TILES> w;
+    Tokens<NB> x;
 #pragma unroll
     for (int n = 0; n < NB; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c.b[n][j] = make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < 4; ++j) x.b[n][j] = make_uint4(0, 0, 0, 0);
     for (int kb = wave; kb < chunks; kb += 4) {
-        load_chunk<NB>(c, o, kb);
-        multiply_chunk<NB>(acc, c);
+        load_weights(w, o, kb);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            if (g > 0 && g >= groups) continue;
+            load_tokens<NB>(x, o.b[g], o.lo, kb);
+            multiply_chunk<NB>(acc[g], w, x);
+            if (g + 1 < NG) forget(w);
+        }
     }
+}
+
+// Joins the waves' sums of a group in LDS: [wave][row tile][token column * 16 + row].
+template <int TILES>
+__device__ __forceinline__ void join_waves(float (*sums)[TILES][256], const v4f (&acc)[TILES], int wave) {
     const int lane = threadIdx.x & 63;
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) *reinterpret_cast<v4f*>(&sums[wave][t][16 * (lane & 15) + 4 * (lane >> 4)]) = acc[t];
+    for (int t = 0; t < TILES; ++t) *reinterpret_cast<v4f*>(&sums[wave][t][16 * (lane & 15) + 4 * (lane >> 4)]) = acc[t];
     __syncthreads();
 }
 
-__device__ __forceinline__ float sum_waves(const float (*s)[kTiles][256], int t, int at) {
+template <int TILES>
+__device__ __forceinline__ float sum_waves(const float (*s)[TILES][256], int t, int at) {
     return (s[0][t][at] + s[1][t][at]) + (s[2][t][at] + s[3][t][at]);
 }
+
+// Waves per SIMD that the registers of a variant leave.
+constexpr int waves_of(int tiles, int groups) { return tiles * groups <= 4 ? 4 : tiles * groups <= 8 ? 3 : 2; }
 
 // Where column k of h is stored in its row: inside each 128-wide chunk, column
 // 64*j + 16*kq + 8*i + n (the bytes of a 16-byte load of the weights) lies at
@@ -332,9 +378,9 @@ __device__ __forceinline__ Chosen choose(const MoeArgs& a, const MoeLayout& L, c
 // Gate and up projections with the SwiGLU.  PL > 0: every work-group routes
 // the (few) tokens for itself, and the first one leaves the result for the
 // kernels that follow; PL == 0: routing has run.
-template <int PL>
-__global__ __launch_bounds__(256, 4) void moe_up_kernel(MoeArgs a, MoeLayout L) {
-    __shared__ __align__(16) float s_sums[4][kTiles][256];
+template <int PL, int TILES, int NG>
+__global__ __launch_bounds__(256, waves_of(TILES, NG)) void moe_up_kernel(MoeArgs a, MoeLayout L) {
+    __shared__ __align__(16) float s_sums[4][TILES][256];
     __shared__ int s_token[kMaxTokens], s_pair[kMaxTokens];
     __shared__ uint64_t s_sets[PL > 0 ? kFusedTokens * PL : 1];
     __shared__ int s_count[kFusedTokens];
@@ -359,54 +405,66 @@ __global__ __launch_bounds__(256, 4) void moe_up_kernel(MoeArgs a, MoeLayout L) 
     __syncthreads();
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, kq = lane >> 4;
-    constexpr int kCols = 8 * kTiles;  // columns of h
+    constexpr int kCols = 8 * TILES;  // columns of h
     const int64_t row0 = (int64_t)blockIdx.x * kCols;
-    Operands<1> o;
+    Operands<TILES, NG> o;
     const uint8_t* w = a.w_gu + e.expert * a.w_gu_stride + row0 * a.ldw_gu;
 #pragma unroll
-    for (int t = 0; t < kTiles / 2; ++t) {
+    for (int t = 0; t < TILES / 2; ++t) {
         o.w[t] = w + 16 * t * a.ldw_gu;
-        o.w[kTiles / 2 + t] = w + (a.inner + 16 * t) * a.ldw_gu;
+        o.w[TILES / 2 + t] = w + (a.inner + 16 * t) * a.ldw_gu;
     }
     o.row_offset = (uint32_t)(r * a.ldw_gu) + 16 * kq;
     o.s[0] = a.s_gu + e.expert * a.s_gu_stride + (row0 >> 7) * a.lds_gu;
     o.s[1] = o.s[0] + (a.inner >> 7) * a.lds_gu;
-    for (int t0 = 0; t0 < e.count; t0 += 16) {
-        o.live = t0 + r < e.count;
-        o.b[0] = a.x + (o.live ? s_token[t0 + r] : 0) * a.ldx + 16 * kq;
-        multiply<1>(s_sums, o, (int)(a.hidden >> 7), wave);
-        constexpr int kPer = kTiles / 2;  // columns of a thread
-        const int tok = threadIdx.x >> 4, c = kPer * (threadIdx.x & 15);
-        if (t0 + tok < e.count) {
-            const int64_t pair = s_pair[t0 + tok];
-            const float p = prob[pair];
-            const int64_t at = pair * a.inner + h_place(row0 + c);
-            float h[kPer];
-            uint16_t hi[kPer], lo[kPer];
+    o.lo = 0;
+    for (int t0 = 0; t0 < e.count; t0 += 16 * NG) {
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int in = tok * 16 + (c & 15) + i;
-                const float g = sum_waves(s_sums, c >> 4, in), u = sum_waves(s_sums, kTiles / 2 + (c >> 4), in);
-                h[i] = g / (1.0f + expf(-g)) * u * p;
-                hi[i] = (uint16_t)pack_bf16(h[i], 0.0f);
-                const float rest = h[i] - bf16_bits_to_f32(hi[i]);
-                lo[i] = (hi[i] & 0x7f80u) == 0x7f80u ? 0 : (uint16_t)pack_bf16(rest, 0.0f);  // inf has no rest
-            }
-            uint16_t* to_hi = reinterpret_cast<uint16_t*>(ws + L.hi) + at;
-            uint16_t* to_lo = reinterpret_cast<uint16_t*>(ws + L.lo) + at;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                to_hi[i] = hi[i];
-                to_lo[i] = lo[i];
-            }
+        for (int g = 0; g < NG; ++g) {
+            const int t = t0 + 16 * g + r;
+            o.b[g] = t < e.count ? a.x + s_token[t] * a.ldx + 16 * kq : nullptr;
         }
-        __syncthreads();
+        const int groups = min(NG, (e.count - t0 + 15) / 16);
+        v4f acc[NG][TILES];
+        multiply<1>(acc, o, (int)(a.hidden >> 7), wave, groups);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            if (g >= groups) continue;
+            join_waves(s_sums, acc[g], wave);
+            constexpr int kPer = TILES / 2;  // columns of a thread
+            const int tok = threadIdx.x >> 4, c = kPer * (threadIdx.x & 15);
+            if (t0 + 16 * g + tok < e.count) {
+                const int64_t pair = s_pair[t0 + 16 * g + tok];
+                const float p = prob[pair];
+                const int64_t at = pair * a.inner + h_place(row0 + c);
+                float h[kPer];
+                uint16_t hi[kPer], lo[kPer];
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    const int in = tok * 16 + (c & 15) + i;
+                    const float gate = sum_waves(s_sums, c >> 4, in), up = sum_waves(s_sums, TILES / 2 + (c >> 4), in);
+                    h[i] = gate / (1.0f + expf(-gate)) * up * p;
+                    hi[i] = (uint16_t)pack_bf16(h[i], 0.0f);
+                    const float rest = h[i] - bf16_bits_to_f32(hi[i]);
+                    lo[i] = (hi[i] & 0x7f80u) == 0x7f80u ? 0 : (uint16_t)pack_bf16(rest, 0.0f);  // inf has no rest
+                }
+                uint16_t* to_hi = reinterpret_cast<uint16_t*>(ws + L.hi) + at;
+                uint16_t* to_lo = reinterpret_cast<uint16_t*>(ws + L.lo) + at;
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    to_hi[i] = hi[i];
+                    to_lo[i] = lo[i];
+                }
+            }
+            __syncthreads();
+        }
     }
 }
 
 // Down projection: one fp32 row of the hidden size per pair.
-__global__ __launch_bounds__(256, 4) void moe_down_kernel(MoeArgs a, MoeLayout L) {
-    __shared__ __align__(16) float s_sums[4][kTiles][256];
+template <int TILES, int NG>
+__global__ __launch_bounds__(256, waves_of(TILES, NG)) void moe_down_kernel(MoeArgs a, MoeLayout L) {
+    __shared__ __align__(16) float s_sums[4][TILES][256];
     __shared__ int s_token[kMaxTokens], s_pair[kMaxTokens];
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     const Chosen e = choose(a, L, sets_of(a, L), blockIdx.y, s_token, s_pair);
@@ -414,25 +472,34 @@ __global__ __launch_bounds__(256, 4) void moe_down_kernel(MoeArgs a, MoeLayout L
     __syncthreads();
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, kq = lane >> 4;
-    constexpr int kRows = 16 * kTiles;
+    constexpr int kRows = 16 * TILES;
     const int64_t row0 = (int64_t)blockIdx.x * kRows;
-    Operands<2> o;
+    Operands<TILES, NG> o;
     const uint8_t* w = a.w_down + e.expert * a.w_down_stride + row0 * a.ldw_down;
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) o.w[t] = w + 16 * t * a.ldw_down;
+    for (int t = 0; t < TILES; ++t) o.w[t] = w + 16 * t * a.ldw_down;
     o.row_offset = (uint32_t)(r * a.ldw_down) + 16 * kq;
     o.s[0] = o.s[1] = a.s_down + e.expert * a.s_down_stride + (row0 >> 7) * a.lds_down;
-    for (int t0 = 0; t0 < e.count; t0 += 16) {
-        o.live = t0 + r < e.count;
-        const int64_t from = (int64_t)(o.live ? s_pair[t0 + r] : 0) * a.inner + 8 * kq;
-        o.b[0] = reinterpret_cast<const uint16_t*>(ws + L.hi) + from;
-        o.b[1] = reinterpret_cast<const uint16_t*>(ws + L.lo) + from;
-        multiply<2>(s_sums, o, (int)(a.inner >> 7), wave);
-        const int c = threadIdx.x % kRows;
-        for (int tok = threadIdx.x / kRows; tok < 16 && t0 + tok < e.count; tok += 256 / kRows)
-            reinterpret_cast<float*>(ws + L.parts)[s_pair[t0 + tok] * a.hidden + row0 + c] =
-                sum_waves(s_sums, c >> 4, tok * 16 + (c & 15));
-        __syncthreads();
+    o.lo = (L.lo - L.hi) / 2;
+    for (int t0 = 0; t0 < e.count; t0 += 16 * NG) {
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            const int t = t0 + 16 * g + r;
+            o.b[g] = t < e.count ? reinterpret_cast<const uint16_t*>(ws + L.hi) + s_pair[t] * a.inner + 8 * kq : nullptr;
+        }
+        const int groups = min(NG, (e.count - t0 + 15) / 16);
+        v4f acc[NG][TILES];
+        multiply<2>(acc, o, (int)(a.inner >> 7), wave, groups);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            if (g >= groups) continue;
+            join_waves(s_sums, acc[g], wave);
+            const int c = threadIdx.x % kRows, first = t0 + 16 * g;
+            for (int tok = threadIdx.x / kRows; tok < 16 && first + tok < e.count; tok += 256 / kRows)
+                reinterpret_cast<float*>(ws + L.parts)[s_pair[first + tok] * a.hidden + row0 + c] =
+                    sum_waves(s_sums, c >> 4, tok * 16 + (c & 15));
+            __syncthreads();
+        }
     }
 }
 
@@ -595,15 +662,64 @@ MoeLayout moe_layout(int64_t tokens, int64_t hidden, int64_t inner, int experts,
     return L;
 }
 
+// Row tiles and token groups of the projections, for the mean number of
+// tokens of an expert.
+struct Variant {
+    int tiles, groups;
+};
+
+// `tiles`: row tiles of an expert.
+//   Groups: with more tokens than one group of 16 holds, a second group saves
+// reading the weights again (64 tokens, 8 of 24 experts 7168/2048: 246 us,
+// 375 without), where an expert has few it only costs registers (8 of 64: 505
+// against 500; 8 of 64 experts 2048/512: 58 against 56).  Four groups pay where
+// nearly all tokens share the experts (8 of 8 experts 7168/2048: 174, two groups
+// of eight tiles 179; 8 of 24: 286 against 246).
+//   Eight tiles halve the reads of the tokens, which matter from about four
+// tokens per expert (64 tokens, 8 of 64 experts 7168/2048: 500 us against 528,
+// 16 tokens: 430 against 425), if there are still two work-groups for every
+// compute unit (8 of 8 experts 2048/1024, half a work-group: 65 against 49).
+Variant expert_variant(const MoeArgs& a, const MoeLayout& L, int64_t tiles) {
+    const int64_t pairs = a.tokens * a.top_k;
+    if (pairs >= 32 * L.slots) return {4, 4};
+    const bool wide = pairs >= 4 * L.slots && tiles / 8 * L.slots >= 2 * compute_units();
+    return {wide ? 8 : 4, pairs > 8 * L.slots && a.tokens > 16 ? 2 : 1};
+}
+
+template <int TILES, int NG>
+void launch_up(const MoeArgs& a, const MoeLayout& L, hipStream_t st) {
+    hipLaunchKernelGGL((moe_up_kernel<0, TILES, NG>), dim3((unsigned)(a.inner / (8 * TILES)), (unsigned)L.slots),
+                       dim3(256), 0, st, a, L);
+}
+
+template <int TILES, int NG>
+void launch_down(const MoeArgs& a, const MoeLayout& L, hipStream_t st) {
+    hipLaunchKernelGGL((moe_down_kernel<TILES, NG>), dim3((unsigned)(a.hidden / (16 * TILES)), (unsigned)L.slots),
+                       dim3(256), 0, st, a, L);
+}
+
+void launch_up(const MoeArgs& a, const MoeLayout& L, hipStream_t st) {
+    const Variant v = expert_variant(a, L, a.inner / 8);  // gate and up tiles
+    if (v.groups == 4) launch_up<4, 4>(a, L, st);
+    else if (v.tiles == 8) v.groups == 2 ? launch_up<8, 2>(a, L, st) : launch_up<8, 1>(a, L, st);
+    else v.groups == 2 ? launch_up<4, 2>(a, L, st) : launch_up<4, 1>(a, L, st);
+}
+
+void launch_down(const MoeArgs& a, const MoeLayout& L, hipStream_t st) {
+    const Variant v = expert_variant(a, L, a.hidden / 16);
+    if (v.groups == 4) launch_down<4, 4>(a, L, st);
+    else if (v.tiles == 8) v.groups == 2 ? launch_down<8, 2>(a, L, st) : launch_down<8, 1>(a, L, st);
+    else v.groups == 2 ? launch_down<4, 2>(a, L, st) : launch_down<4, 1>(a, L, st);
+}
+
+// Routing, alone or (fused) in the gate and up projections.
 template <int PL>
-void launch_up(const MoeArgs& a, const MoeLayout& L, bool fused, hipStream_t st) {
-    const dim3 grid((unsigned)(a.inner / (8 * kTiles)), (unsigned)L.slots);
-    if (fused) {
-        hipLaunchKernelGGL((moe_up_kernel<PL>), grid, dim3(256), 0, st, a, L);
-    } else {
+void launch_route(const MoeArgs& a, const MoeLayout& L, bool fused, hipStream_t st) {
+    if (fused)
+        hipLaunchKernelGGL((moe_up_kernel<PL, 4, 1>), dim3((unsigned)(a.inner / 32), (unsigned)L.slots), dim3(256), 0,
+                           st, a, L);
+    else
         hipLaunchKernelGGL(moe_route_kernel<PL>, dim3((unsigned)a.tokens), dim3(64), 0, st, a, L);
-        hipLaunchKernelGGL((moe_up_kernel<0>), grid, dim3(256), 0, st, a, L);
-    }
 }
 
 }  // namespace
@@ -617,10 +733,11 @@ hipError_t launch_moe_decode(const MoeArgs& a, hipStream_t st) {
     const int cus = compute_units();
     // A kernel of its own for routing costs 5 us; done by every work-group of
     // the gate and up projections it costs each about 1 us for four tokens.
-    const bool fused = a.tokens <= 4 || (a.tokens <= kFusedTokens && a.inner / (8 * kTiles) * L.slots <= 4 * cus);
-    if (a.experts <= 64) launch_up<1>(a, L, fused, st);
-    else if (a.experts <= 256) launch_up<4>(a, L, fused, st);
-    else launch_up<kMaxExperts / 64>(a, L, fused, st);
+    const bool fused = a.tokens <= 4 || (a.tokens <= kFusedTokens && a.inner / 32 * L.slots <= 4 * cus);
+    if (a.experts <= 64) launch_route<1>(a, L, fused, st);
+    else if (a.experts <= 256) launch_route<4>(a, L, fused, st);
+    else launch_route<kMaxExperts / 64>(a, L, fused, st);
+    if (!fused) launch_up(a, L, st);
     // All experts in one work-group where that is little to read for each: a
     // kernel less is worth 2 to 5 us, but the work-groups do not fill the
     // chip evenly (one token of 64 experts 7168/2048, 256 KiB each: 72 against
@@ -628,8 +745,7 @@ hipError_t launch_moe_decode(const MoeArgs& a, hipStream_t st) {
     if (a.tokens <= kFewTokens && L.slots * 16 * a.inner <= 1 << 18) {
         hipLaunchKernelGGL(moe_down_few_kernel, dim3((unsigned)(a.hidden / 16)), dim3(64 * kFewWaves), 0, st, a, L);
     } else {
-        hipLaunchKernelGGL(moe_down_kernel, dim3((unsigned)(a.hidden / (16 * kTiles)), (unsigned)L.slots),
-                           dim3(256), 0, st, a, L);
+        launch_down(a, L, st);
         hipLaunchKernelGGL(moe_join_kernel, dim3((unsigned)((a.hidden + 255) / 256), (unsigned)a.tokens), dim3(256), 0,
                            st, a, L);
     }

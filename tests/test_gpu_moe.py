@@ -56,6 +56,24 @@ def test_against_reference(fp8q, T, E, top_k, H, I):
     _check(fp8q, layer, top_k, renormalize=bool((T + top_k) % 2))
 
 
+@pytest.mark.parametrize("T,top_k", [(19, 14), (32, 8), (33, 20), (64, 8), (64, 17)])
+def test_enough_work_for_the_wide_variants(fp8q, T, top_k):
+    """64 experts of 1024/512 are two work-groups of eight row tiles for every compute unit."""
+    say(f"moe wide T={T} k={top_k}")
+    _check(fp8q, _layer(T + top_k, T, 64, 1024, 512, pad=T % 2), top_k, T % 2 == 0)
+
+
+@pytest.mark.parametrize("T", [17, 32, 33, 48, 49, 64])
+def test_full_and_partial_token_groups(fp8q, T):
+    """Every token on each of the experts: two to four groups of 16, the last one full or not."""
+    say(f"moe groups T={T}")
+    for E in (2, 6):
+        _check(fp8q, _layer(T, T, E, 384, 256), E, True)
+    layer = _layer(T, T, 12, 256, 384)  # one expert for all, the others few tokens each
+    layer[1][:, 5] = 60.0
+    _check(fp8q, layer, 3, False)
+
+
 @pytest.mark.parametrize("T", [1, 16, 64])
 def test_bf16_output(fp8q, T):
     say(f"moe bf16 T={T}")
