@@ -498,6 +498,8 @@ def grouped_gemm(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.T
 
 
 # ------------------------------------------------------------------ feed-forward block
+# Calls of few rows take as long as their host code: the library's functions
+# are called without the wrappers above.
 
 def _rows(rows: int, cols: int, dtype: torch.dtype, device) -> torch.Tensor:
     """[rows][cols] whose row stride is a multiple of 16 bytes."""
@@ -565,11 +567,11 @@ def layernorm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Optio
     s = small.as_strided((groups, rows), (rows, 1)) if quantize else None
     rstd = small.as_strided((rows,), (1,), groups * rows)
     mean = small.as_strided((rows,), (1,), (groups + 1) * rows) if kind == FP8Q_NORM_LAYER else None
-    _check(fp8q_layernorm(x.data_ptr(), _dtype_code(x), rows, cols, _ld(x), _ptr(gamma), _ptr(beta),
-                          _dtype_code(given[0]) if given else FP8Q_F32, eps, kind, _ptr(y),
-                          FP8Q_F32 if y is None else _dtype_code(y), 0 if y is None else _ld(y), _ptr(q),
-                          0 if q is None else _pad16(max(cols, 1)), _ptr(s), max(rows, 1), scale_mode, _ptr(mean),
-                          rstd.data_ptr(), _stream()), "fp8q_layernorm")
+    _check(_lib.fp8q_layernorm(x.data_ptr(), _dtype_code(x), rows, cols, _ld(x), _ptr(gamma), _ptr(beta),
+                               _dtype_code(given[0]) if given else FP8Q_F32, eps, kind, _ptr(y),
+                               FP8Q_F32 if y is None else _dtype_code(y), 0 if y is None else _ld(y), _ptr(q),
+                               0 if q is None else _pad16(max(cols, 1)), _ptr(s), max(rows, 1), scale_mode, _ptr(mean),
+                               rstd.data_ptr(), _stream()), "fp8q_layernorm")
     return LayernormOut(q, s, y, mean, rstd)
 
 
@@ -604,13 +606,13 @@ def layernorm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: Optional[torch.
     _on_device("layernorm_backward", dy, x, rstd,
                *(t for t in (gamma, mean, skip, dgamma, dbeta) if t is not None))
     dx = _rows(rows, cols, x.dtype, dev)
-    need = fp8q_layernorm_backward_workspace(rows, cols)
+    need = _lib.fp8q_layernorm_backward_workspace(rows, cols)
     ws, base = _workspace(need, dev)
-    _check(fp8q_layernorm_backward(dy.data_ptr(), _ld(dy), x.data_ptr(), _ld(x), _dtype_code(x), rows, cols,
-                                   _ptr(gamma), FP8Q_F32 if gamma is None else _dtype_code(gamma),
-                                   _ptr(mean) if kind == FP8Q_NORM_LAYER else None, rstd.data_ptr(), kind,
-                                   _ptr(skip), 0 if skip is None else _ld(skip), dx.data_ptr(), _ld(dx),
-                                   dgamma.data_ptr(), _ptr(dbeta), 1 if accumulate else 0, base, need, _stream()),
+    _check(_lib.fp8q_layernorm_backward(dy.data_ptr(), _ld(dy), x.data_ptr(), _ld(x), _dtype_code(x), rows, cols,
+                                        _ptr(gamma), FP8Q_F32 if gamma is None else _dtype_code(gamma),
+                                        _ptr(mean) if kind == FP8Q_NORM_LAYER else None, rstd.data_ptr(), kind,
+                                        _ptr(skip), 0 if skip is None else _ld(skip), dx.data_ptr(), _ld(dx),
+                                        dgamma.data_ptr(), _ptr(dbeta), 1 if accumulate else 0, base, need, _stream()),
            "fp8q_layernorm_backward")
     return dx, dgamma, dbeta
 
@@ -653,12 +655,12 @@ def swiglu_quantize(g: torch.Tensor, u: torch.Tensor, checkpoint: bool = True, s
     kept = None
     if checkpoint:
         kept = SwigluCheckpoint(*_pair(rows, cols, torch.uint8, dev), *_stack(groups, rows, torch.float32, dev))
-    _check(fp8q_swiglu_quantize(g.data_ptr(), u.data_ptr(), _dtype_code(g), ldgu, rows, cols, qh.data_ptr(),
-                                _pad16(max(cols, 1)), sh.data_ptr(), max(rows, 1),
-                                *((None, None, 0, None, None, 0) if kept is None else
-                                  (kept.qg.data_ptr(), kept.qu.data_ptr(), _ld(kept.qg), kept.sg.data_ptr(),
-                                   kept.su.data_ptr(), max(rows, 1))),
-                                scale_mode, _stream()), "fp8q_swiglu_quantize")
+    _check(_lib.fp8q_swiglu_quantize(g.data_ptr(), u.data_ptr(), _dtype_code(g), ldgu, rows, cols, qh.data_ptr(),
+                                     _pad16(max(cols, 1)), sh.data_ptr(), max(rows, 1),
+                                     *((None, None, 0, None, None, 0) if kept is None else
+                                       (kept.qg.data_ptr(), kept.qu.data_ptr(), _ld(kept.qg), kept.sg.data_ptr(),
+                                        kept.su.data_ptr(), max(rows, 1))),
+                                     scale_mode, _stream()), "fp8q_swiglu_quantize")
     return qh, sh, kept
 
 
@@ -688,7 +690,7 @@ def swiglu_backward(kept: SwigluCheckpoint, dh: torch.Tensor) -> Tuple[torch.Ten
     _check_checkpoint("swiglu_backward", kept, dh)
     rows, cols = dh.shape
     dg, du = _pair(rows, cols, dh.dtype, dh.device)
-    _check(fp8q_swiglu_backward(*_checkpoint_args(kept, dh), dg.data_ptr(), du.data_ptr(), _ld(dg), _stream()),
+    _check(_lib.fp8q_swiglu_backward(*_checkpoint_args(kept, dh), dg.data_ptr(), du.data_ptr(), _ld(dg), _stream()),
            "fp8q_swiglu_backward")
     return dg, du
 
@@ -735,10 +737,11 @@ def swiglu_backward_quantize(kept: SwigluCheckpoint, dh: torch.Tensor, scale_mod
                     scales.as_strided((tgroups, cols), (2 * cols, 1), 2 * ns + cols), _codes(cols, rows, dev),
                     scales.as_strided((tgroups, cols), (cols, 1), 2 * ns + 2 * nt))
     ldq, ldt = 2 * _pad16(max(cols, 1)), _pad16(max(rows, 1))
-    _check(fp8q_swiglu_backward_quantize(*_checkpoint_args(kept, dh), o.qdg.data_ptr(), o.qdu.data_ptr(), ldq,
-                                         o.sdg.data_ptr(), o.sdu.data_ptr(), max(rows, 1), o.qdgt.data_ptr(),
-                                         o.qdut.data_ptr(), ldt, o.sdgt.data_ptr(), o.sdut.data_ptr(), 2 * cols,
-                                         o.qht.data_ptr(), ldt, o.sht.data_ptr(), max(cols, 1), scale_mode, _stream()),
+    _check(_lib.fp8q_swiglu_backward_quantize(*_checkpoint_args(kept, dh), o.qdg.data_ptr(), o.qdu.data_ptr(), ldq,
+                                              o.sdg.data_ptr(), o.sdu.data_ptr(), max(rows, 1), o.qdgt.data_ptr(),
+                                              o.qdut.data_ptr(), ldt, o.sdgt.data_ptr(), o.sdut.data_ptr(), 2 * cols,
+                                              o.qht.data_ptr(), ldt, o.sht.data_ptr(), max(cols, 1), scale_mode,
+                                              _stream()),
            "fp8q_swiglu_backward_quantize")
     return o
 
@@ -773,12 +776,12 @@ def moe_decode(x: torch.Tensor, logits: torch.Tensor, w_gu: torch.Tensor, s_gu: 
     _check_experts("moe_decode w_down", w_down, s_down, (experts, hidden, inner))
     _on_device("moe_decode", x, logits, w_gu, s_gu, w_down, s_down)
     y = torch.empty((tokens, hidden), dtype=out_dtype, device=x.device)
-    need = fp8q_moe_decode_workspace(tokens, hidden, inner, experts, top_k)
+    need = _lib.fp8q_moe_decode_workspace(tokens, hidden, inner, experts, top_k)
     ws, base = _workspace(need, x.device)
-    _check(fp8q_moe_decode(x.data_ptr(), _ld(x), tokens, hidden, logits.data_ptr(),
-                           max(logits.stride(0), experts) if tokens <= 1 else logits.stride(0), experts, top_k,
-                           1 if renormalize else 0, inner, w_gu.data_ptr(), w_gu.stride(1),
-                           w_gu.stride(0), s_gu.data_ptr(), s_gu.stride(1), s_gu.stride(0), w_down.data_ptr(),
-                           w_down.stride(1), w_down.stride(0), s_down.data_ptr(), s_down.stride(1), s_down.stride(0),
-                           y.data_ptr(), _dtype_code(y), _ld(y), base, need, _stream()), "fp8q_moe_decode")
+    _check(_lib.fp8q_moe_decode(x.data_ptr(), _ld(x), tokens, hidden, logits.data_ptr(),
+                                max(logits.stride(0), experts) if tokens <= 1 else logits.stride(0), experts, top_k,
+                                1 if renormalize else 0, inner, w_gu.data_ptr(), w_gu.stride(1),
+                                w_gu.stride(0), s_gu.data_ptr(), s_gu.stride(1), s_gu.stride(0), w_down.data_ptr(),
+                                w_down.stride(1), w_down.stride(0), s_down.data_ptr(), s_down.stride(1),
+                                s_down.stride(0), y.data_ptr(), _dtype_code(y), _ld(y), base, need, _stream()), "fp8q_moe_decode")
     return y
