@@ -507,8 +507,9 @@ __global__ __launch_bounds__(256, waves_of(TILES, NG)) void moe_down_kernel(MoeA
 // 16 rows of the hidden size and all active experts, so y needs no partial
 // results.  Matrix columns 0..7 are the tokens' hi halves of h, columns 8..15
 // their lo halves (half the loads and products of separate operands); a token
-// that did not choose the expert multiplies zeros.  The eight waves share the
-// (expert, chunk) pairs; weights are loaded three of them ahead, h one ahead.
+// that did not choose the expert takes nothing of it (its NaN neither).  The
+// eight waves share the (expert, chunk) pairs; weights are loaded three of
+// them ahead, h one ahead.
 //   One token of 8 experts of 7168/2048 (117 MB): 28 us, of which 19 are the
 // reads at the rate of the general kernel's probe and the rest the start (the
 // experts' sets come before the first weights) and 448 work-groups on 256
@@ -558,6 +559,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void moe_down_few_kernel(MoeArgs
     const uint16_t* half = reinterpret_cast<const uint16_t*>(ws + (r < kFewTokens ? L.hi : L.lo));
     uint4 w[4][2], h[2][4];
     float scale[4];
+    bool takes[2];  // the lane's token chose the expert
     auto load_w = [&](const Item& i, int slot) {
         if (i.idx >= active) return;
         const int e = __builtin_amdgcn_readfirstlane(s_expert[i.idx]);
@@ -568,6 +570,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void moe_down_few_kernel(MoeArgs
     };
     auto load_h = [&](const Item& i, int slot) {
         const int pair = i.idx < active ? s_pair[i.idx][r % kFewTokens] : -1;
+        takes[slot] = pair >= 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) h[slot][j] = make_uint4(0, 0, 0, 0);
         if (pair < 0) return;
@@ -601,7 +604,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void moe_down_few_kernel(MoeArgs
                 p = mfma(bf16_of_codes(w[u][j].z, w[u][j].w), __builtin_bit_cast(v8bf, h[u & 1][2 * j + 1]), p);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(p[i], scale[u], acc[i]);
+            for (int i = 0; i < 4; ++i) acc[i] = takes[u & 1] ? __builtin_fmaf(p[i], scale[u], acc[i]) : acc[i];
             advance(now);
         }
     }

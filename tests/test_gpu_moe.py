@@ -89,6 +89,22 @@ def test_every_token_on_the_same_experts(fp8q, T):
     _check(fp8q, layer, 2, True)
 
 
+@pytest.mark.parametrize("T", [2, 8, 9, 40])
+def test_an_experts_nan_reaches_only_its_tokens(fp8q, T):
+    say(f"moe NaN weights T={T}")
+    x, logits, w_gu, s_gu, w_down, s_down = _layer(T, T, 8, 256, 256)
+    logits[:, 2:4] = -np.inf
+    logits[0, 2:4] = 5.0
+    lt = torch.from_numpy(logits).cuda()
+    clean = fp8q.moe_decode(x, lt, w_gu, s_gu, w_down, s_down, 2)
+    w_gu[2, 7, 3] = 0x7f
+    w_down[2, 5, 9] = 0xff
+    s_down[3, 1, 1] = float("inf")
+    y = fp8q.moe_decode(x, lt, w_gu, s_gu, w_down, s_down, 2)
+    assert bool(torch.isnan(y[0]).any())
+    assert torch.equal(y[1:], clean[1:])
+
+
 def test_ties_masks_and_empty_rows(fp8q):
     """Equal logits (all of them, and around the last place), -0 beside 0, masked experts, fewer candidates than
     top_k, rows of -inf, the lowest finite values."""
