@@ -88,25 +88,27 @@ template <int I>
 __device__ __forceinline__ void forget(Raw8<float> (&)[I]) {}
 
 // Sum of a row's deviations from `mean`, squared, times shrink^2.  Zeros
-// beyond the row's end stay out.
-template <typename T, int N, int I>
+// beyond the row's end stay out.  (shrink is a power of two: one rounding,
+// that of the difference.)  WHOLE: the row is whole groups of eight columns.
+template <typename T, int N, int I, bool WHOLE>
 __device__ __forceinline__ float sum_squares(const Raw8<T> (&raw)[I], int t, int64_t cols, float mean, float shrink) {
+    const float shift = -mean * shrink;
     float sq = 0.0f;
 #pragma unroll
     for (int i = 0; i < I; ++i) {
         const int64_t c = 8 * (t + N * i);
         float v[8];
         raw[i].values(v);
-        if (c + 8 <= cols) {
+        if (WHOLE ? c < cols : c + 8 <= cols) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const float d = (v[k] - mean) * shrink;
+                const float d = __builtin_fmaf(v[k], shrink, shift);
                 sq = __builtin_fmaf(d, d, sq);
             }
-        } else {
+        } else if (!WHOLE) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const float d = c + k < cols ? (v[k] - mean) * shrink : 0.0f;
+                const float d = c + k < cols ? __builtin_fmaf(v[k], shrink, shift) : 0.0f;
                 sq = __builtin_fmaf(d, d, sq);
             }
         }
@@ -117,7 +119,7 @@ __device__ __forceinline__ float sum_squares(const Raw8<T> (&raw)[I], int t, int
 // Results of G groups of a row: y from the row's statistics, its values and
 // codes to memory.  One lane per tile computes the scale (lane i of a DPP row
 // for group i).  weights(i, gm, bt) gives the weights of group i.
-template <typename T, int N, int G, bool POW2, bool NT, typename Weights>
+template <typename T, int N, int G, bool POW2, bool NT, bool WHOLE, typename Weights>
 __device__ __forceinline__ void finish_groups(const LayernormArgs& a, const Raw8<T>* raw, int i0, int t, int64_t row,
                                               float mean, float rstd, const Weights& weights) {
     const int sub = t & 15;
@@ -126,20 +128,26 @@ __device__ __forceinline__ void finish_groups(const LayernormArgs& a, const Raw8
 #pragma unroll
     for (int i = 0; i < G; ++i) {
         const int64_t c = 8 * (t + N * (i0 + i));
-        float gm[8], bt[8];
-        weights(i0 + i, gm, bt);
-        raw[i].values(v[i]);
+        if (!WHOLE || c < a.cols) {
+            float gm[8], bt[8];
+            weights(i0 + i, gm, bt);
+            raw[i].values(v[i]);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[i][k] = __builtin_fmaf((v[i][k] - mean) * rstd, gm[k], bt[k]);
-        if (c + 8 > a.cols) {
+            for (int k = 0; k < 8; ++k) v[i][k] = __builtin_fmaf((v[i][k] - mean) * rstd, gm[k], bt[k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[i][k] = 0.0f;
+        }
+        if (!WHOLE && c + 8 > a.cols) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[i][k] = c + k < a.cols ? v[i][k] : 0.0f;
         }
         if (a.y && c < a.cols) {
+            const int64_t valid = WHOLE ? c + 8 : a.cols;
             if (a.y_dtype == kDtypeBF16)
-                store_values8<NT>(static_cast<uint16_t*>(a.y) + row * a.ldy, c, a.cols, v[i]);
+                store_values8<NT>(static_cast<uint16_t*>(a.y) + row * a.ldy, c, valid, v[i]);
             else
-                store_values8(static_cast<float*>(a.y) + row * a.ldy, c, a.cols, v[i]);
+                store_values8(static_cast<float*>(a.y) + row * a.ldy, c, valid, v[i]);
         }
         if (a.q) {
             const uint32_t m = row_max_u32(amax8(v[i]));
@@ -160,13 +168,13 @@ __device__ __forceinline__ void finish_groups(const LayernormArgs& a, const Raw8
 #pragma unroll
     for (int i = 0; i < G; ++i) {
         const int64_t c = 8 * (t + N * (i0 + i));
-        if (fast && c + 8 <= a.cols) {
+        if (fast && (WHOLE ? c < a.cols : c + 8 <= a.cols)) {
             *reinterpret_cast<uint2*>(q + c) =
                 make_uint2(encode4_sr<POW2>(v[i][0], v[i][1], v[i][2], v[i][3], s[i], r[i]),
                            encode4_sr<POW2>(v[i][4], v[i][5], v[i][6], v[i][7], s[i], r[i]));
         } else if (c < a.cols) {
             const TileScale tt = scale_from(s[i], r[i]);
-            store8(q, c, a.cols, encode4_any<POW2>(v[i][0], v[i][1], v[i][2], v[i][3], tt),
+            store8(q, c, WHOLE ? c + 8 : a.cols, encode4_any<POW2>(v[i][0], v[i][1], v[i][2], v[i][3], tt),
                    encode4_any<POW2>(v[i][4], v[i][5], v[i][6], v[i][7], tt));
         }
     }
@@ -199,14 +207,14 @@ __global__ __launch_bounds__(64 * W) void layernorm_row_kernel(LayernormArgs a) 
         block_sum<W, 1>(sum, s_red[0]);
         mean = sum[0] / n;
     }
-    float sq[1] = {sum_squares<T, 64 * W, I>(raw, t, cols, mean, a.shrink)};
+    float sq[1] = {sum_squares<T, 64 * W, I, false>(raw, t, cols, mean, a.shrink)};
     block_sum<W, 1>(sq, s_red[1]);
     const float rstd = 1.0f / sqrtf(sq[0] / (n * a.shrink * a.shrink) + a.eps);
     if (t == 0) {
         if (LAYER && a.mean) a.mean[row] = mean;
         if (a.rstd) a.rstd[row] = rstd;
     }
-    finish_groups<T, 64 * W, I, POW2, false>(a, raw, 0, t, row, mean, rstd, [&](int i, float gm[8], float bt[8]) {
+    finish_groups<T, 64 * W, I, POW2, false, false>(a, raw, 0, t, row, mean, rstd, [&](int i, float gm[8], float bt[8]) {
         load_weights8(a.gamma, a.w_dtype, 8 * (t + 64 * W * i), cols, 1.0f, gm);
         load_weights8(a.beta, a.w_dtype, 8 * (t + 64 * W * i), cols, 0.0f, bt);
     });
@@ -241,13 +249,15 @@ __device__ __forceinline__ void fill_weights(LdsWeights<N>& to, const void* w, i
 // the weights in LDS; a team loads its next row before it works on the current
 // one.  A work-group's rows are consecutive, so the scales that it writes fill
 // whole lines.  Many rows, or narrow ones.  G work-groups are meant to share a
-// compute unit.  (8192x7168 with codes and values: bf16 60 us, 67 without the
-// non-temporal stores of y; fp32 112 us, 131 with such stores.  bf16: a wave
-// per row needs over 200 registers there and took 85, a work-group per row
-// reads the weights again for every row, 88.)
+// compute unit.  (8192x7168: RMS norm in bf16 with codes and values 56 us (5.3
+// TB/s), codes alone 40, layer norm 58 and 49; fp32 100 and 64.  Non-temporal
+// stores of y are worth 7 us in bf16 and cost 19 in fp32.  A wave per row
+// needs over 200 registers there and took 85, a work-group per row reads the
+// weights again for every row, 88.  Bound by memory with values, by vector
+// instructions and the wait for two sums with codes alone.)
 constexpr int kTeamThreads = 512;
 
-template <typename T, int N, int I, int G, bool LAYER, bool POW2>
+template <typename T, int N, int I, int G, bool LAYER, bool POW2, bool WHOLE>
 __global__ __launch_bounds__(kTeamThreads, 2 * G) void layernorm_team_kernel(LayernormArgs a, int rows_per_group) {
     constexpr int kTeams = kTeamThreads / N, W = N / 64;
     __shared__ LdsWeights<8 * N * I> s_gamma, s_beta;
@@ -258,8 +268,11 @@ __global__ __launch_bounds__(kTeamThreads, 2 * G) void layernorm_team_kernel(Lay
     const float n = (float)cols;
     auto load = [&](Raw8<T> (&raw)[I], int64_t row) {
 #pragma unroll
-        for (int i = 0; i < I; ++i)
-            if (row < end) load_row8(raw[i], static_cast<const T*>(a.x) + row * a.ldx, 8 * (t + N * i), cols, false);
+        for (int i = 0; i < I; ++i) {
+            const int64_t c = 8 * (t + N * i);
+            if (row < end && (!WHOLE || c < cols))
+                load_row8(raw[i], static_cast<const T*>(a.x) + row * a.ldx, c, cols, WHOLE);
+        }
     };
     auto team_sum = [&](float v, int phase) {
         if constexpr (N == 16) return row_sum(v);
@@ -300,7 +313,7 @@ __global__ __launch_bounds__(kTeamThreads, 2 * G) void layernorm_team_kernel(Lay
             forget(raw);
         }
         // a layer norm's two sums have a buffer each, an RMS norm's sums take turns
-        const float sq = team_sum(sum_squares<T, N, I>(raw, t, cols, mean, a.shrink), LAYER ? 1 : phase);
+        const float sq = team_sum(sum_squares<T, N, I, WHOLE>(raw, t, cols, mean, a.shrink), LAYER ? 1 : phase);
         phase ^= 1;
         forget(raw);
         const float rstd = 1.0f / sqrtf(sq / (n * a.shrink * a.shrink) + a.eps);
@@ -309,7 +322,7 @@ __global__ __launch_bounds__(kTeamThreads, 2 * G) void layernorm_team_kernel(Lay
             if (LAYER && a.mean) a.mean[row] = mean;
             if (a.rstd) a.rstd[row] = rstd;
         }
-        finish_groups<T, N, I, POW2, true>(a, raw, 0, t, row, mean, rstd, [&](int i, float gm[8], float bt[8]) {
+        finish_groups<T, N, I, POW2, true, WHOLE>(a, raw, 0, t, row, mean, rstd, [&](int i, float gm[8], float bt[8]) {
             s_gamma.get(8 * (t + N * i), gm);
             s_beta.get(8 * (t + N * i), bt);
         });
@@ -519,14 +532,30 @@ void launch_teams(const LayernormArgs& a, hipStream_t st) {
     const int64_t per = ((a.rows + groups - 1) / groups + kTeams - 1) / kTeams * kTeams;
     const dim3 grid((unsigned)((a.rows + per - 1) / per)), block(kTeamThreads);
     const int n = (int)per;
-    if (a.layer && a.pow2) hipLaunchKernelGGL((layernorm_team_kernel<T, N, I, G, true, true>), grid, block, 0, st, a, n);
-    else if (a.layer) hipLaunchKernelGGL((layernorm_team_kernel<T, N, I, G, true, false>), grid, block, 0, st, a, n);
-    else if (a.pow2) hipLaunchKernelGGL((layernorm_team_kernel<T, N, I, G, false, true>), grid, block, 0, st, a, n);
-    else hipLaunchKernelGGL((layernorm_team_kernel<T, N, I, G, false, false>), grid, block, 0, st, a, n);
+    // Rows of whole groups of eight columns go without the masks of a partial
+    // one, which pay from four groups per lane on (8192x7168 bf16, codes: 50
+    // against 61 us; with one or two groups the time is the same).
+    auto launch = [&](auto whole) {
+        constexpr bool kWhole = decltype(whole)::value;
+        if (a.layer && a.pow2)
+            hipLaunchKernelGGL((layernorm_team_kernel<T, N, I, G, true, true, kWhole>), grid, block, 0, st, a, n);
+        else if (a.layer)
+            hipLaunchKernelGGL((layernorm_team_kernel<T, N, I, G, true, false, kWhole>), grid, block, 0, st, a, n);
+        else if (a.pow2)
+            hipLaunchKernelGGL((layernorm_team_kernel<T, N, I, G, false, true, kWhole>), grid, block, 0, st, a, n);
+        else
+            hipLaunchKernelGGL((layernorm_team_kernel<T, N, I, G, false, false, kWhole>), grid, block, 0, st, a, n);
+    };
+    if constexpr (I >= 4) {
+        if (a.cols % 8 == 0) return launch(std::true_type{});
+    }
+    launch(std::false_type{});
 }
 
 // Many rows, and narrow ones, go to teams; few wide rows get a work-group
-// each.  Registers and LDS decide how many work-groups share a compute unit.
+// each.  Four groups per lane carry a row's fixed work best (16384x4096 bf16,
+// codes: 51 us with 128 lanes a row, 56 with 256 lanes of two groups).
+// Registers and LDS decide how many work-groups share a compute unit.
 template <typename T>
 void launch_forward_for(const LayernormArgs& a, hipStream_t st) {
     constexpr int kShare = sizeof(T) == 2 ? 3 : 2;
@@ -536,7 +565,7 @@ void launch_forward_for(const LayernormArgs& a, hipStream_t st) {
     else if (a.cols <= 1024 && many) launch_teams<T, 64, 2, kShare>(a, st);
     else if (a.cols <= 2048 && many) launch_teams<T, 64, 4, 2>(a, st);
     else if (a.cols <= 2048) launch_row<T, 4, 1>(a, st);
-    else if (a.cols <= 4096 && many) launch_teams<T, 256, 2, kShare>(a, st);
+    else if (a.cols <= 4096 && many) launch_teams<T, 128, 4, 2>(a, st);
     else if (a.cols <= 8192 && many) launch_teams<T, 256, 4, 2>(a, st);
     else if (a.cols <= 8192) launch_row<T, 16, 1>(a, st);
     else launch_row<T, 16, 2>(a, st);
