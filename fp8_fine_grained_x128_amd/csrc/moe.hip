@@ -682,11 +682,14 @@ struct Variant {
 // tokens per expert (64 tokens, 8 of 64 experts 7168/2048: 500 us against 528,
 // 16 tokens: 430 against 425), if there are still two work-groups for every
 // compute unit (8 of 8 experts 2048/1024, half a work-group: 65 against 49).
+// Two tiles where four give less than one (one token, 2 experts 4096/14336: 82
+// us, 91 with four; elsewhere they are slower, 16 tokens above 452).
 Variant expert_variant(const MoeArgs& a, const MoeLayout& L, int64_t tiles) {
     const int64_t pairs = a.tokens * a.top_k;
     if (pairs >= 32 * L.slots) return {4, 4};
-    const bool wide = pairs >= 4 * L.slots && tiles / 8 * L.slots >= 2 * compute_units();
-    return {wide ? 8 : 4, pairs > 8 * L.slots && a.tokens > 16 ? 2 : 1};
+    const int cus = compute_units(), groups = pairs > 8 * L.slots && a.tokens > 16 ? 2 : 1;
+    if (pairs >= 4 * L.slots && tiles / 8 * L.slots >= 2 * cus) return {8, groups};
+    return {groups == 1 && tiles / 4 * L.slots < cus ? 2 : 4, groups};
 }
 
 template <int TILES, int NG>
@@ -705,14 +708,16 @@ void launch_up(const MoeArgs& a, const MoeLayout& L, hipStream_t st) {
     const Variant v = expert_variant(a, L, a.inner / 8);  // gate and up tiles
     if (v.groups == 4) launch_up<4, 4>(a, L, st);
     else if (v.tiles == 8) v.groups == 2 ? launch_up<8, 2>(a, L, st) : launch_up<8, 1>(a, L, st);
-    else v.groups == 2 ? launch_up<4, 2>(a, L, st) : launch_up<4, 1>(a, L, st);
+    else if (v.groups == 2) launch_up<4, 2>(a, L, st);
+    else v.tiles == 4 ? launch_up<4, 1>(a, L, st) : launch_up<2, 1>(a, L, st);
 }
 
 void launch_down(const MoeArgs& a, const MoeLayout& L, hipStream_t st) {
     const Variant v = expert_variant(a, L, a.hidden / 16);
     if (v.groups == 4) launch_down<4, 4>(a, L, st);
     else if (v.tiles == 8) v.groups == 2 ? launch_down<8, 2>(a, L, st) : launch_down<8, 1>(a, L, st);
-    else v.groups == 2 ? launch_down<4, 2>(a, L, st) : launch_down<4, 1>(a, L, st);
+    else if (v.groups == 2) launch_down<4, 2>(a, L, st);
+    else v.tiles == 4 ? launch_down<4, 1>(a, L, st) : launch_down<2, 1>(a, L, st);
 }
 
 // Routing, alone or (fused) in the gate and up projections.
