@@ -260,6 +260,10 @@ constexpr int kTeamThreads = 512;
 template <typename T, int N, int I, int G, bool LAYER, bool POW2, bool WHOLE>
 __global__ __launch_bounds__(kTeamThreads, 2 * G) void layernorm_team_kernel(LayernormArgs a, int rows_per_group) {
     constexpr int kTeams = kTeamThreads / N, W = N / 64;
+    // Through the caches, narrow rows come faster (20000x1024 bf16, codes and
+    // values: 22 us, 26 non-temporal) and wide ones slower
+    // (8192x7168 fp32: 102 against 96).
+    constexpr bool kNT = N >= 256;
     __shared__ LdsWeights<8 * N * I> s_gamma, s_beta;
     __shared__ float s_red[2][kTeams][W > 1 ? W : 1];
     const int64_t cols = a.cols;
@@ -271,7 +275,7 @@ __global__ __launch_bounds__(kTeamThreads, 2 * G) void layernorm_team_kernel(Lay
         for (int i = 0; i < I; ++i) {
             const int64_t c = 8 * (t + N * i);
             if (row < end && (!WHOLE || c < cols))
-                load_row8(raw[i], static_cast<const T*>(a.x) + row * a.ldx, c, cols, WHOLE);
+                load_row8<T, kNT>(raw[i], static_cast<const T*>(a.x) + row * a.ldx, c, cols, WHOLE);
         }
     };
     auto team_sum = [&](float v, int phase) {
@@ -345,6 +349,7 @@ template <typename T, int N, int I, bool LAYER>
 __global__ __launch_bounds__(1024, 4) void layernorm_backward_kernel(LayernormBackwardArgs a) {
     constexpr int kTeams = 1024 / N, kCols = 8 * N * I, W = N / 64;
     constexpr bool kAhead = I == 1;
+    constexpr bool kNT = sizeof(T) == 2 && N == 1024;  // as in the forward pass (30000x331 bf16: 37 us, 48 non-temporal)
     __shared__ LdsWeights<kCols> s_gamma;
     __shared__ float s_red[2][2][16];
     __shared__ float s_team[kTeams > 1 ? kTeams : 1][kTeams > 1 ? kCols : 1];
@@ -355,7 +360,8 @@ __global__ __launch_bounds__(1024, 4) void layernorm_backward_kernel(LayernormBa
 #pragma unroll
         for (int i = 0; i < I; ++i) {
             raw[i].zero();
-            if (row < a.rows) load_row8<T, sizeof(T) == 2>(raw[i], static_cast<const T*>(p) + row * ld, 8 * (t + N * i), cols, false);
+            if (row < a.rows)
+                load_row8<T, kNT>(raw[i], static_cast<const T*>(p) + row * ld, 8 * (t + N * i), cols, false);
         }
     };
     float dgamma[I][8], dbeta[I][8];
