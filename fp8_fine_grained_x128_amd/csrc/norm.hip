@@ -274,8 +274,9 @@ __global__ __launch_bounds__(kTeamThreads, 2 * G) void layernorm_team_kernel(Lay
 #pragma unroll
         for (int i = 0; i < I; ++i) {
             const int64_t c = 8 * (t + N * i);
-            if (row < end && (!WHOLE || c < cols))
-                load_row8<T, kNT>(raw[i], static_cast<const T*>(a.x) + row * a.ldx, c, cols, WHOLE);
+            const T* x = row < end ? static_cast<const T*>(a.x) + row * a.ldx : nullptr;
+            if (!WHOLE) load_row8_ahead<T, kNT>(raw[i], x, c, cols);
+            else if (x != nullptr && c < cols) raw[i].template load_full<kNT>(x + c);
         }
     };
     auto team_sum = [&](float v, int phase) {
@@ -359,9 +360,8 @@ __global__ __launch_bounds__(1024, 4) void layernorm_backward_kernel(LayernormBa
     auto load = [&](Raw8<T> (&raw)[I], const void* p, int64_t ld, int64_t row) {
 #pragma unroll
         for (int i = 0; i < I; ++i) {
-            raw[i].zero();
-            if (row < a.rows)
-                load_row8<T, kNT>(raw[i], static_cast<const T*>(p) + row * ld, 8 * (t + N * i), cols, false);
+            const T* from = row < a.rows ? static_cast<const T*>(p) + row * ld : nullptr;
+            load_row8_ahead<T, kNT>(raw[i], from, 8 * (t + N * i), cols);
         }
     };
     float dgamma[I][8], dbeta[I][8];
