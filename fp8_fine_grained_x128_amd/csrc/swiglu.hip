@@ -33,14 +33,28 @@ __device__ __forceinline__ float sigmoid(float x) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -0x1.715476p+0f));
 }
 
-// x / (1 + exp(-x)) with the quotient corrected from its remainder, which
-// leaves about the error of a division.  exp(-x) is held below the largest
-// fp32, so that the remainder exists.  (The forward pass has room for the
-// three instructions; feeding p's rounding back too would cost 4 %.)
-__device__ __forceinline__ float silu(float x) {
-    const float d = 1.0f + __builtin_amdgcn_exp2f(__builtin_fmaxf(x, -87.0f) * -0x1.715476p+0f);
+// Up to here exp(x) and exp(-x) and their reciprocals are normal numbers.
+constexpr float kNear = 87.0f;
+
+// w with w * w = exp(x) for x < 0.  The two factors keep exp(x) and x exp(x)
+// down to the subnormal numbers, where 2^p itself is flushed to zero.
+__device__ __forceinline__ float root_exp(float x) { return __builtin_amdgcn_exp2f(x * 0x1.715476p-1f); }
+
+// x / (1 + exp(-x)) for |x| <= kNear, with the quotient corrected from its
+// remainder, which leaves about the error of a division.  (The forward pass
+// has room for the two instructions; feeding p's rounding back too would cost
+// 4 %.)
+__device__ __forceinline__ float silu_near(float x) {
+    const float d = 1.0f + __builtin_amdgcn_exp2f(x * -0x1.715476p+0f);
     const float r = __builtin_amdgcn_rcpf(d), q = x * r;
     return __builtin_fmaf(__builtin_fmaf(-d, q, x), r, q);
+}
+
+// For any x, with the bits of silu_near where that holds: beyond, the
+// denominator (of x exp(x) / (1 + exp(x)) for x < 0) is 1.
+__device__ __forceinline__ float silu(float x) {
+    const float w = root_exp(x), q = silu_near(x);
+    return x < -kNear ? x * w * w : x > kNear ? x : q;
 }
 
 struct SwigluPoint {
@@ -144,9 +158,17 @@ __global__ __launch_bounds__(64 * W) void swiglu_quantize_kernel(SwigluArgs a) {
         float g[8], u[8];
         rg[i].values(g);
         ru[i].values(u);
+        const uint32_t amax_g = rg[i].amax_bits();
+        // gates beyond kNear are rare: without them twelve instructions an
+        // element are eight (8192x7168 bf16: 73 us, 80 otherwise)
+        if (wave_all(amax_g <= __float_as_uint(kNear))) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) h[i][k] = silu(g[k]) * u[k];
-        const uint32_t amax[3] = {amax8(h[i]), rg[i].amax_bits(), ru[i].amax_bits()};
+            for (int k = 0; k < 8; ++k) h[i][k] = silu_near(g[k]) * u[k];
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) h[i][k] = silu(g[k]) * u[k];
+        }
+        const uint32_t amax[3] = {amax8(h[i]), amax_g, ru[i].amax_bits()};
 #pragma unroll
         for (int m = 0; m < M; ++m) {
             const uint32_t x = row_max_u32(amax[m]);

@@ -1,0 +1,65 @@
+"""SwiGLU at the ends of the number range against 64-bit references: tiles whose
+gates are all closed (down to the lowest finite value), and infinite gates."""
+import numpy as np
+import pytest
+import torch
+
+from tests import ffn_ref as R
+from tests.parity import say
+
+pytestmark = pytest.mark.gpu
+DTYPES = [torch.bfloat16, torch.float32]
+MODES = [0, 1]  # fp32 and power-of-two scales
+CLOSED = [-60.0, -86.5, -87.0, -87.5, -88.0, -88.5, -89.0, -92.0, -100.0, -104.0, -200.0, -1e4, -1e30, -1e38]
+U = R.U
+
+
+def _silu(g):
+    with np.errstate(over="ignore"):
+        return g / (1.0 + np.exp(-g))
+
+
+def _room(h, g, u):
+    """The fp32 bound of ffn_ref.swiglu, and an absolute one that does not grow with the gate: a result or a factor
+    below the smallest normal number 2^-126 may be off by that much, times u."""
+    return np.abs(h) * (8 + 2 * np.minimum(np.abs(g), 200.0)) * U + 2.0 ** -125 * (1 + np.abs(u))
+
+
+def _closed(dtype, lowest=True):
+    gates = CLOSED + [-3.3e38, float(torch.finfo(dtype).min)] if lowest else CLOSED
+    rng = np.random.default_rng(1)
+    u = rng.standard_normal((len(gates), 256))
+    u[:, 128:] *= 1e6
+    return R.place(np.repeat(np.array(gates)[:, None], 256, axis=1), dtype), R.place(u, dtype)
+
+
+@pytest.mark.parametrize("mode", MODES, ids=["fp32", "pow2"])
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+def test_closed_gates_forward(fp8q, dtype, mode):
+    """Every gate of a tile far below zero: h goes to zero with exp(g), it does not grow with g."""
+    say(f"swiglu closed gates {dtype} mode {mode}")
+    g, u = _closed(dtype)
+    qh, sh, _ = fp8q.swiglu_quantize(g, u, scale_mode=mode)
+    g64, u64 = R.f64(g), R.f64(u)
+    h = _silu(g64) * u64
+    R.assert_codes_of(qh, sh, h, _room(h, g64, u64), mode == 1, "h")
+    q2, s2, _ = fp8q.swiglu_quantize(g, u, checkpoint=False, scale_mode=mode)
+    assert torch.equal(q2, qh) and torch.equal(s2, sh)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+def test_infinite_gates_forward(fp8q, dtype):
+    """g = +inf gives h = inf * u, which its tile's scale shows; every other tile keeps its bits."""
+    say(f"swiglu infinite gates {dtype}")
+    rng = np.random.default_rng(2)
+    g, u = R.place(rng.standard_normal((9, 384)), dtype), R.place(rng.uniform(0.5, 2.0, (9, 384)), dtype)
+    clean = fp8q.swiglu_quantize(g, u)
+    g[4, 200] = float("inf")
+    for checkpoint in (True, False):
+        qh, sh, _ = fp8q.swiglu_quantize(g, u, checkpoint=checkpoint)
+        assert float(sh[1, 4]) == float("inf")
+        others = torch.ones((3, 9), dtype=torch.bool, device="cuda")
+        others[1, 4] = False
+        assert torch.equal(sh[others], clean[1][others])
+        tiles = others.t().repeat_interleave(128, dim=1)
+        assert torch.equal(qh[tiles], clean[0][tiles])
