@@ -24,21 +24,32 @@ namespace fp8q {
 
 namespace {
 
-// 1 / (1 + exp(-x)) from the hardware's 2^p and reciprocal, each good to a
-// unit in the last place; with the rounding of p = -x log2(e) the relative
-// error stays below (5 + 1.3 |x|) 2^-24.  exp(-x) beyond the largest fp32
-// gives 0.  (Against expf and a division, or a corrected p and a Newton step:
-// 7 to 25 instructions fewer per element, in kernels that issue 35 to 55.)
-__device__ __forceinline__ float sigmoid(float x) {
-    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -0x1.715476p+0f));
-}
-
 // Up to here exp(x) and exp(-x) and their reciprocals are normal numbers.
 constexpr float kNear = 87.0f;
 
 // w with w * w = exp(x) for x < 0.  The two factors keep exp(x) and x exp(x)
 // down to the subnormal numbers, where 2^p itself is flushed to zero.
 __device__ __forceinline__ float root_exp(float x) { return __builtin_amdgcn_exp2f(x * 0x1.715476p-1f); }
+
+// 1 / (1 + exp(-x)) for x >= -kNear from the hardware's 2^p and reciprocal,
+// each good to a unit in the last place; with the rounding of p = -x log2(e),
+// which the sum with 1 weighs down, the relative error stays below
+// (5 + 1.3 |x| (1 - sigma)) 2^-24: 6 2^-24 of the sigmoid for open gates, and
+// never more than that of 1.  Both backward forms use it, so that the codes of
+// one are the quantizer's codes of the other's gradients bit for bit.  (Against
+// expf and a division, or a corrected p and a Newton step: 7 to 25
+// instructions fewer per element, in kernels that issue 35 to 55; the form
+// into FP8 operands takes 6 % longer with them, the gradients themselves are of
+// inputs that 8 bits hold.)
+__device__ __forceinline__ float sigmoid_near(float x) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -0x1.715476p+0f));
+}
+
+// For any x, with the bits of sigmoid_near where that holds.
+__device__ __forceinline__ float sigmoid(float x) {
+    const float w = root_exp(x), s = sigmoid_near(x);
+    return x < -kNear ? w * w : s;
+}
 
 // x / (1 + exp(-x)) for |x| <= kNear, with the quotient corrected from its
 // remainder, which leaves about the error of a division.  (The forward pass
@@ -61,15 +72,27 @@ struct SwigluPoint {
     float h, dg, du;
 };
 
-// The three results at one element.
+// The three results at one element.  NEAR: |g| <= kNear.
+template <bool NEAR>
 __device__ __forceinline__ SwigluPoint swiglu_point(float g, float u, float dh) {
-    const float sg = sigmoid(g);
+    const float sg = NEAR ? sigmoid_near(g) : sigmoid(g);
     const float a = g * sg;  // silu(g)
     SwigluPoint p;
     p.h = a * u;
     p.du = dh * a;
     p.dg = dh * u * sg * __builtin_fmaf(g, 1.0f - sg, 1.0f);
     return p;
+}
+
+// Whether all checkpoint values of a tile with this scale are within kNear.
+__device__ __forceinline__ bool near_scale(float s) { return s * kE4M3Max <= kNear; }
+
+// Hides a wave-uniform pointer's value from the optimizer.
+template <typename P>
+__device__ __forceinline__ void opaque_uniform(P& p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile("" : "+s"(p));
+#endif
 }
 
 // Eight checkpoint values at column c of a row: codes times the row's scale.
@@ -224,14 +247,19 @@ __global__ __launch_bounds__(256) void swiglu_backward_kernel(SwigluBackwardArgs
     Raw8<T> raw;
     load_row8<T, sizeof(T) == 2>(raw, static_cast<const T*>(a.dh) + row * a.lddh, c, a.cols, false);
     raw.values(dh);
-    decode8(load_codes8(a.qg + row * a.ldq, c, a.cols), a.sg[(c >> 7) * a.lds + row], g);
+    const float sg = a.sg[(c >> 7) * a.lds + row];
+    decode8(load_codes8(a.qg + row * a.ldq, c, a.cols), sg, g);
     decode8(load_codes8(a.qu + row * a.ldq, c, a.cols), a.su[(c >> 7) * a.lds + row], u);
+    auto points = [&](auto near) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const SwigluPoint p = swiglu_point(g[k], u[k], dh[k]);
-        dg[k] = p.dg;
-        du[k] = p.du;
-    }
+        for (int k = 0; k < 8; ++k) {
+            const SwigluPoint p = swiglu_point<decltype(near)::value>(g[k], u[k], dh[k]);
+            dg[k] = p.dg;
+            du[k] = p.du;
+        }
+    };
+    if (wave_all(near_scale(sg))) points(std::true_type{});
+    else points(std::false_type{});
     store_values8(static_cast<T*>(a.dg) + row * a.ldd, c, a.cols, dg);
     store_values8(static_cast<T*>(a.du) + row * a.ldd, c, a.cols, du);
 }
@@ -301,26 +329,53 @@ __global__ __launch_bounds__(512, 4) void swiglu_backward_quantize_kernel(Swiglu
         }
     }
     float v[3][kRows][8];  // dg, du, h
-    uint32_t mine = 0;     // lane 4*m + i of a row group: maximum of row i of dg (m = 0) or du
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
+    bool my_near = true;
+    auto points = [&](auto near, int i, uint2 qg, uint2 qu, float sg, float su, const Raw8<T>& raw) {
         float g[8], u[8], dh[8];
-        decode8(qg[i], sg[i], g);
-        decode8(qu[i], su[i], u);
-        raw[i].values(dh);
+        decode8(qg, sg, g);
+        decode8(qu, su, u);
+        raw.values(dh);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const SwigluPoint p = swiglu_point(g[k], u[k], dh[k]);
+            const SwigluPoint p = swiglu_point<decltype(near)::value>(g[k], u[k], dh[k]);
             v[0][i][k] = p.dg;
             v[1][i][k] = p.du;
             v[2][i][k] = p.h;
         }
+    };
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
+    for (int i = 0; i < kRows; ++i) {
+        points(std::true_type{}, i, qg[i], qu[i], sg[i], su[i], raw[i]);
+        my_near = my_near && near_scale(sg[i]);
+    }
+    if (!wave_all(my_near)) {
+        // Rare.  The inputs are loaded again: held until here, or a choice of
+        // two ways in the loop above, they would be spilled registers (200 us
+        // against 105 at 8192x7168 bf16; a sigmoid for any gate 111).
+        SwigluBackwardArgs b = a;
+        opaque_uniform(b.qg);
+        opaque_uniform(b.qu);
+        opaque_uniform(b.sg);
+        opaque_uniform(b.su);
+        opaque_uniform(b.dh);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            if (row + i >= a.rows || c >= a.cols) continue;
+            Raw8<T> d;
+            load_row8(d, static_cast<const T*>(b.dh) + (row + i) * a.lddh, c, a.cols, false);
+            points(std::false_type{}, i, load_codes8(b.qg + (row + i) * a.ldq, c, a.cols),
+                   load_codes8(b.qu + (row + i) * a.ldq, c, a.cols), b.sg[tile_c * a.lds + row + i],
+                   b.su[tile_c * a.lds + row + i], d);
+        }
+    }
+    uint32_t mine = 0;  // lane 4*m + i of a row group: maximum of row i of dg (m = 0) or du
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
             const uint32_t x = row_max_u32(amax8(v[m][i]));
             mine = cg == kRows * m + i ? x : mine;
         }
-    }
 #pragma unroll
     for (int m = 0; m < 3; ++m) {
         float x[8];

@@ -1,5 +1,6 @@
 """SwiGLU at the ends of the number range against 64-bit references: tiles whose
-gates are all closed (down to the lowest finite value), and infinite gates."""
+gates are all closed (down to the lowest finite value) in both passes, and
+infinite gates."""
 import numpy as np
 import pytest
 import torch
@@ -63,3 +64,37 @@ def test_infinite_gates_forward(fp8q, dtype):
         assert torch.equal(sh[others], clean[1][others])
         tiles = others.t().repeat_interleave(128, dim=1)
         assert torch.equal(qh[tiles], clean[0][tiles])
+
+
+def _backward_bounds(g, u, dh):
+    """dg, du, h in 64 bits and bounds: those of ffn_ref with an absolute part that does not grow with the gate beyond
+    the factors g, u and dh that the formula itself multiplies by."""
+    s = R._sigmoid(g)
+    h, du, dg = g * s * u, dh * g * s, dh * u * s * (1 + g * (1 - s))
+    es = (6 + 2 * np.minimum(np.abs(g), 200.0)) * U
+    tiny = 2.0 ** -124
+    e_du = np.abs(du) * (es + 2 * U) + tiny * (1 + np.abs(dh))
+    e_dg = np.abs(dh * u) * s * ((1 + np.abs(g) * (1 - s)) * (es + 6 * U) + np.abs(g) * (s * es + 2 * U)) + tiny * (
+        1 + np.abs(dh)) * (1 + np.abs(u))
+    return (dg, e_dg), (du, e_du), (h, np.abs(h) * (es + 2 * U) + tiny * (1 + np.abs(u)))
+
+
+@pytest.mark.parametrize("mode", MODES, ids=["fp32", "pow2"])
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+def test_closed_gates_backward(fp8q, dtype, mode):
+    """The backward pass at closed gates, with gradients large enough that dg and du are normal numbers where the sigmoid
+    is barely one; the recomputed h is the forward pass's at the checkpoint's values."""
+    say(f"swiglu closed gates backward {dtype} mode {mode}")
+    g, u = _closed(dtype, lowest=False)
+    kept = fp8q.swiglu_quantize(g, u, scale_mode=mode)[2]
+    dh = R.place(np.random.default_rng(3).standard_normal(tuple(g.shape)) * 1e6, dtype)
+    g64, u64 = R.checkpoint_values(kept.qg, kept.sg), R.checkpoint_values(kept.qu, kept.su)
+    assert np.isfinite(g64).all()
+    want_dg, want_du, want_h = _backward_bounds(g64, u64, R.f64(dh))
+    dg, du = fp8q.swiglu_backward(kept, dh)
+    R.assert_close(dg, *want_dg, "dg")
+    R.assert_close(du, *want_du, "du")
+    o = fp8q.swiglu_backward_quantize(kept, dh, scale_mode=mode)
+    R.assert_codes_of(o.qdg, o.sdg, *want_dg, mode == 1, "dg codes")
+    R.assert_codes_of(o.qdu, o.sdu, *want_du, mode == 1, "du codes")
+    R.assert_codes_of(o.qht, o.sht, *(np.ascontiguousarray(a.T) for a in want_h), mode == 1, "h transposed")
