@@ -381,7 +381,7 @@ __global__ __launch_bounds__(512, 4) void swiglu_backward_quantize_kernel(Swiglu
         float x[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            x[k] = max_abs3(__builtin_fmaxf(__builtin_fabsf(v[m][0][k]), __builtin_fabsf(v[m][1][k])), v[m][2][k], v[m][3][k]);
+            x[k] = max_abs3(max_abs2(v[m][0][k], v[m][1][k]), v[m][2][k], v[m][3][k]);
         float4* part = reinterpret_cast<float4*>(&s_part[m][rg][8 * cg]);
         part[0] = make_float4(x[0], x[1], x[2], x[3]);
         part[1] = make_float4(x[4], x[5], x[6], x[7]);

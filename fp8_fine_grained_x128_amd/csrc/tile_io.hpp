@@ -287,12 +287,17 @@ __device__ __forceinline__ void row_broadcast(std::integer_sequence<int, N...>, 
 
 // Magnitude maxima: the absolute value is an operand modifier and three
 // operands go into one maximum.  The bits of the result order like the number.
+// A NaN operand gives NaN (IEEE 754-2019 maximum), whose bits are the largest:
+// a tile that holds one has a NaN scale, as in the quantizers.
+__device__ __forceinline__ float max_abs2(float a, float b) {
+    return __builtin_elementwise_maximum(__builtin_fabsf(a), __builtin_fabsf(b));
+}
 __device__ __forceinline__ float max_abs3(float m, float a, float b) {
-    return __builtin_fmaxf(__builtin_fmaxf(m, __builtin_fabsf(a)), __builtin_fabsf(b));
+    return __builtin_elementwise_maximum(__builtin_elementwise_maximum(m, __builtin_fabsf(a)), __builtin_fabsf(b));
 }
 
 __device__ __forceinline__ uint32_t amax8(const float v[8]) {
-    float m = __builtin_fmaxf(__builtin_fabsf(v[0]), __builtin_fabsf(v[1]));
+    float m = max_abs2(v[0], v[1]);
 #pragma unroll
     for (int k = 2; k < 8; k += 2) m = max_abs3(m, v[k], v[k + 1]);
     return __float_as_uint(m);

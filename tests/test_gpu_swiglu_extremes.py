@@ -1,6 +1,6 @@
 """SwiGLU at the ends of the number range against 64-bit references: tiles whose
-gates are all closed (down to the lowest finite value) in both passes, and
-infinite gates."""
+gates are all closed (down to the lowest finite value), infinite gates, NaN and
+infinities beside tiles of zeros, and the agreement of the two passes."""
 import numpy as np
 import pytest
 import torch
@@ -98,3 +98,68 @@ def test_closed_gates_backward(fp8q, dtype, mode):
     R.assert_codes_of(o.qdg, o.sdg, *want_dg, mode == 1, "dg codes")
     R.assert_codes_of(o.qdu, o.sdu, *want_du, mode == 1, "du codes")
     R.assert_codes_of(o.qht, o.sht, *(np.ascontiguousarray(a.T) for a in want_h), mode == 1, "h transposed")
+
+
+def _shown(q, s):
+    """[rows][cols] of truth values: where codes times scale are no finite numbers (1x128 tiles of q[rows][cols])."""
+    v = q.contiguous().view(torch.float8_e4m3fn).float() * s.t().repeat_interleave(128, dim=1)[:, : q.shape[1]]
+    return ~torch.isfinite(v)
+
+
+@pytest.mark.parametrize("value", [float("nan"), -float("nan"), float("inf")], ids=["nan", "-nan", "inf"])
+@pytest.mark.parametrize("mode", MODES, ids=["fp32", "pow2"])
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+def test_nonfinite_shows_forward(fp8q, dtype, mode, value):
+    """One NaN or infinity in u beside tiles of zeros (a padded token): its tile's codes and scale show it, with a
+    checkpoint and without; every other tile keeps its bits."""
+    say(f"swiglu non-finite forward {dtype} mode {mode} {value}")
+    rng = np.random.default_rng(4)
+    g, u = R.place(rng.standard_normal((12, 512)), dtype), R.place(rng.standard_normal((12, 512)), dtype)
+    g[5], u[5] = 0, 0
+    g[:, 128:256], u[:, 128:256] = 0, 0
+    clean = fp8q.swiglu_quantize(g, u, scale_mode=mode)
+    u[4, 300] = value
+    others = torch.ones((4, 12), dtype=torch.bool, device="cuda")
+    others[2, 4] = False
+    tiles = others.t().repeat_interleave(128, dim=1)
+    for checkpoint in (True, False):
+        qh, sh, kept = fp8q.swiglu_quantize(g, u, checkpoint=checkpoint, scale_mode=mode)
+        shown = _shown(qh, sh)
+        assert bool(shown[4, 300]) and not bool(shown[tiles].any())
+        assert torch.equal(sh[others], clean[1][others]) and torch.equal(qh[tiles], clean[0][tiles])
+        if mode == 0:
+            assert not bool(torch.isfinite(sh[2, 4]))
+        if kept is not None:
+            assert bool(_shown(kept.qu, kept.su)[4, 300])
+            assert torch.equal(kept.su[others], clean[2].su[others]) and torch.equal(kept.qg, clean[2].qg)
+
+
+@pytest.mark.parametrize("value", [float("nan"), -float("nan"), float("inf")], ids=["nan", "-nan", "inf"])
+@pytest.mark.parametrize("mode", MODES, ids=["fp32", "pow2"])
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+def test_nonfinite_shows_backward(fp8q, dtype, mode, value):
+    """One NaN or infinity in the incoming gradient beside zero gradients: every operand's tile that holds it shows it,
+    in both orientations; the recomputed h and every other tile keep their bits."""
+    say(f"swiglu non-finite backward {dtype} mode {mode} {value}")
+    rng = np.random.default_rng(5)
+    g, u = R.place(rng.standard_normal((140, 384)), dtype), R.place(rng.standard_normal((140, 384)), dtype)
+    dh = R.place(rng.standard_normal((140, 384)), dtype)
+    dh[8:12] = 0
+    dh[:, 40] = 0
+    kept = fp8q.swiglu_quantize(g, u)[2]
+    clean = fp8q.swiglu_backward_quantize(kept, dh, scale_mode=mode)
+    dh[9, 200] = value
+    plain = fp8q.swiglu_backward(kept, dh)
+    o = fp8q.swiglu_backward_quantize(kept, dh, scale_mode=mode)
+    assert torch.equal(o.qht, clean.qht) and torch.equal(o.sht, clean.sht)
+    for p, q, s, qt, st, cq, cs, cqt, cst in (
+            (plain[0], o.qdg, o.sdg, o.qdgt, o.sdgt, clean.qdg, clean.sdg, clean.qdgt, clean.sdgt),
+            (plain[1], o.qdu, o.sdu, o.qdut, o.sdut, clean.qdu, clean.sdu, clean.qdut, clean.sdut)):
+        assert not bool(torch.isfinite(p[9, 200])) and int((~torch.isfinite(p)).sum()) == 1
+        for a, b, ca, cb, at in ((q, s, cq, cs, (9, 200)), (qt, st, cqt, cst, (200, 9))):
+            others = torch.ones(b.shape, dtype=torch.bool, device="cuda")
+            others[at[1] // 128, at[0]] = False
+            tiles = others.t().repeat_interleave(128, dim=1)[:, : a.shape[1]]
+            shown = _shown(a, b)
+            assert bool(shown[at]) and not bool(shown[tiles].any())
+            assert torch.equal(b[others], cb[others]) and torch.equal(a[tiles], ca[tiles])
