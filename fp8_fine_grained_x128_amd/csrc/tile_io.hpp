@@ -314,7 +314,13 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
+__device__ __forceinline__ double row_sum(double v) {
+    for (int off = 8; off; off >>= 1) v += __shfl_xor(v, off);
+    return v;
+}
+
+template <typename S>
+__device__ __forceinline__ S wave_sum(S v) {
     v = row_sum(v);
     v += __shfl_xor(v, 16);
     v += __shfl_xor(v, 32);

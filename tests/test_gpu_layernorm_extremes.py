@@ -1,4 +1,5 @@
-"""Norms at the ends of the number range: NaN and infinities beside rows of zeros."""
+"""Norms at the ends of the number range: tiny and huge rows with eps = 0, and
+NaN and infinities beside rows of zeros."""
 import numpy as np
 import pytest
 import torch
@@ -15,6 +16,24 @@ SHAPES = [(40, 100), (14, 400), (2100, 700), (2100, 1800), (2100, 2504), (2100, 
 
 def _kind(fp8q, kind):
     return fp8q.FP8Q_NORM_LAYER if kind == "layer" else fp8q.FP8Q_NORM_RMS
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-37])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", SHAPES)
+def test_rows_of_any_magnitude(fp8q, rows, cols, dtype, kind, eps):
+    """Rows of 2^-115 to 2^100, whose squares leave the range of fp32 on either side: the statistics do not."""
+    say(f"layernorm magnitudes {rows}x{cols} {dtype} {kind} eps={eps}")
+    rng = np.random.default_rng(cols)
+    x = rng.standard_normal((rows, cols))
+    for i, e in enumerate((-115, -90, -70, -60, -50, -20, 0, 50, 60, 64, 80, 100)):
+        x[i if rows < 100 else 170 * i] *= 2.0 ** e
+    x = R.place(x, dtype)
+    o = fp8q.layernorm(x, eps=eps, kind=_kind(fp8q, kind), out_dtype=torch.float32)
+    y, _, rstd, e_y, _, e_r = R.layernorm(R.f64(x), np.ones(cols), np.zeros(cols), float(np.float32(eps)), kind == "layer")
+    R.assert_close(o.rstd, rstd, e_r, "rstd")
+    R.assert_close(o.y, y, e_y, "y")
 
 
 @pytest.mark.parametrize("mode", [0, 1], ids=["fp32", "pow2"])
