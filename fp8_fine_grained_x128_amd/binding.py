@@ -564,6 +564,8 @@ def layernorm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Optio
     q = _codes(rows, cols, dev) if quantize else None
     y = _rows(rows, cols, out_dtype, dev) if out_dtype is not None else None
     small = torch.empty((groups + 2) * rows, dtype=torch.float32, device=dev)  # scales, rstd, mean
+    if cols == 0:  # nothing is launched: the statistics of nothing
+        small.fill_(float("nan"))
     s = small.as_strided((groups, rows), (rows, 1)) if quantize else None
     rstd = small.as_strided((rows,), (1,), groups * rows)
     mean = small.as_strided((rows,), (1,), (groups + 1) * rows) if kind == FP8Q_NORM_LAYER else None

@@ -1,5 +1,5 @@
-"""Norms at the ends of the number range: tiny and huge rows with eps = 0, and
-NaN and infinities beside rows of zeros."""
+"""Norms at the ends of the number range: tiny and huge rows with eps = 0, NaN
+and infinities beside rows of zeros, no columns at all."""
 import numpy as np
 import pytest
 import torch
@@ -56,3 +56,12 @@ def test_nonfinite_shows(fp8q, rows, cols, kind, value, mode):
     assert bool((~torch.isfinite(v[5]))[bad[5]].all())
     keep = torch.arange(rows, device="cuda") != 5
     assert torch.equal(o.q[keep], clean.q[keep]) and torch.equal(o.s[:, keep], clean.s[:, keep])
+
+
+def test_no_columns(fp8q):
+    """Rows without columns have no mean and no variance: NaN, as the mean of nothing is, and never what the memory held."""
+    say("layernorm: no columns")
+    torch.full((1 << 16,), 7.0, device="cuda")
+    o = fp8q.layernorm(torch.empty((300, 0), dtype=torch.float32, device="cuda"), out_dtype=torch.float32)
+    assert o.q.shape == (300, 0) and o.s.shape == (0, 300) and o.y.shape == (300, 0)
+    assert bool(torch.isnan(o.mean).all()) and bool(torch.isnan(o.rstd).all())
