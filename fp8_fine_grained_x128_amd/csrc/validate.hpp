@@ -232,8 +232,9 @@ inline int layernorm_backward(const void* dy, int64_t lddy, const void* x, int64
     const bool weights = dgamma || dbeta;
     if (!aligned(dgamma, 4) || !aligned(dbeta, 4)) return FP8Q_EALIGN;
     if (rows == 0) return weights && !accumulate ? kLaunch : FP8Q_OK;
-    if (!dy || !x || !rstd || !dx || (kind == FP8Q_NORM_LAYER && !mean) || (weights && !workspace)) return FP8Q_EINVAL;
-    if (cols > kMaxNormCols) return FP8Q_EUNSUPPORTED;
+    if (!dy || !x || !rstd || !dx || (kind == FP8Q_NORM_LAYER && !mean)) return FP8Q_EINVAL;
+    if (cols > kMaxNormCols) return FP8Q_EUNSUPPORTED;  // no workspace holds its sums: `need` is 0
+    if (weights && !workspace) return FP8Q_EINVAL;
     if (weights && workspace_bytes < need) return FP8Q_ESHAPE;
     if (!row_aligned(dy, lddy, dtype) || !row_aligned(x, ldx, dtype) || !row_aligned(dx, lddx, dtype) ||
         (skip && !row_aligned(skip, ldskip, dtype)) || !aligned(gamma, 16) || !aligned(mean, 4) ||
