@@ -4,6 +4,7 @@
 // of the split-K scratch array below, looked up once per device.
 #include <stdint.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "../../include/fp8q.h"
@@ -357,7 +358,7 @@ int fp8q_swiglu_backward_quantize(const uint8_t* qg, const uint8_t* qu, int64_t 
 
 int64_t fp8q_moe_decode_workspace(int64_t tokens, int64_t hidden, int64_t inner, int experts, int top_k) {
     if (tokens == 0 || fp8q::check::moe_sizes(tokens, hidden, inner, experts, top_k) != kLaunch) return 0;
-    return fp8q::moe_decode_bytes(tokens, hidden, inner, experts, top_k);
+    return fp8q::moe_decode_bytes(tokens, hidden, inner, experts, std::min(top_k, experts));
 }
 
 int fp8q_moe_decode(const void* x, int64_t ldx, int64_t tokens, int64_t hidden, const float* logits, int64_t ldl,
@@ -375,7 +376,7 @@ int fp8q_moe_decode(const void* x, int64_t ldx, int64_t tokens, int64_t hidden, 
     fp8q::MoeArgs a{};
     a.x = static_cast<const uint16_t*>(x); a.ldx = ldx;
     a.tokens = (int)tokens; a.hidden = hidden; a.inner = inner;
-    a.logits = logits; a.ldl = ldl; a.experts = experts; a.top_k = top_k; a.renormalize = renormalize ? 1 : 0;
+    a.logits = logits; a.ldl = ldl; a.experts = experts; a.top_k = std::min(top_k, experts); a.renormalize = renormalize ? 1 : 0;
     a.w_gu = w_gu; a.ldw_gu = ldw_gu; a.w_gu_stride = w_gu_stride;
     a.s_gu = s_gu; a.lds_gu = lds_gu; a.s_gu_stride = s_gu_stride;
     a.w_down = w_down; a.ldw_down = ldw_down; a.w_down_stride = w_down_stride;

@@ -200,7 +200,7 @@ struct MoeArgs {
     int64_t hidden, inner;
     const float* logits;
     int64_t ldl;
-    int experts, top_k, renormalize;
+    int experts, top_k, renormalize;  // top_k <= experts: a token has no more pairs
     const uint8_t* w_gu;  // [experts][2*inner][hidden], gate rows first
     int64_t ldw_gu, w_gu_stride;
     const float* s_gu;
