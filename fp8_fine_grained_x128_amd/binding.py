@@ -682,8 +682,9 @@ def _check_checkpoint(what: str, kept: SwigluCheckpoint, dh: torch.Tensor) -> No
 
 def _checkpoint_args(kept: SwigluCheckpoint, dh: torch.Tensor) -> tuple:
     rows, cols = dh.shape
-    return (kept.qg.data_ptr(), kept.qu.data_ptr(), _ld(kept.qg), kept.sg.data_ptr(), kept.su.data_ptr(),
-            max(kept.sg.stride(0), rows), dh.data_ptr(), _dtype_code(dh), _ld(dh), rows, cols)
+    lds = kept.sg.stride(0) if kept.sg.shape[0] > 1 else rows  # one group may carry any stride
+    return (kept.qg.data_ptr(), kept.qu.data_ptr(), _ld(kept.qg), kept.sg.data_ptr(), kept.su.data_ptr(), lds,
+            dh.data_ptr(), _dtype_code(dh), _ld(dh), rows, cols)
 
 
 def swiglu_backward(kept: SwigluCheckpoint, dh: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
