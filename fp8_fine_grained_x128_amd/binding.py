@@ -760,14 +760,11 @@ def _check_experts(what: str, w: torch.Tensor, s: torch.Tensor, shape: Tuple[int
                          f"[{E}][{_cdiv(N, 128)}][{_cdiv(K, 128)}] with unit inner stride")
 
 
-def _expert_strides(w: torch.Tensor, s: torch.Tensor) -> Tuple[int, int, int, int]:
-    """(row stride and expert stride of the codes, the same of the scales).  An axis of one element may carry any
-    stride (it never multiplies a nonzero index): reported as that of a dense array."""
-    experts, rows, cols = w.shape
-    ldw = w.stride(1)  # 2 * inner and hidden are 128 at least
-    sw, ss = s.stride(), s.shape
-    lds = sw[1] if ss[1] > 1 else ss[2]
-    return ldw, w.stride(0) if experts > 1 else rows * ldw, lds, sw[0] if experts > 1 else ss[1] * lds
+def _dense_singles(t: torch.Tensor) -> torch.Tensor:
+    """[E][rows][cols] with the strides of a dense array along axes of one element (which may carry any)."""
+    se, sr, sc = t.stride()
+    sr = sr if t.shape[1] > 1 else t.shape[2]
+    return t.as_strided(t.shape, (se if t.shape[0] > 1 else t.shape[1] * sr, sr, sc))
 
 
 def moe_decode(x: torch.Tensor, logits: torch.Tensor, w_gu: torch.Tensor, s_gu: torch.Tensor, w_down: torch.Tensor,
@@ -788,15 +785,16 @@ def moe_decode(x: torch.Tensor, logits: torch.Tensor, w_gu: torch.Tensor, s_gu: 
     _check_experts("moe_decode w_gu", w_gu, s_gu, (experts, 2 * inner, hidden))
     _check_experts("moe_decode w_down", w_down, s_down, (experts, hidden, inner))
     _on_device("moe_decode", x, logits, w_gu, s_gu, w_down, s_down)
-    ldw_gu, w_gu_stride, lds_gu, s_gu_stride = _expert_strides(w_gu, s_gu)
-    ldw_down, w_down_stride, lds_down, s_down_stride = _expert_strides(w_down, s_down)
+    if experts == 1 or hidden == 128:
+        w_gu, s_gu, w_down, s_down = (_dense_singles(t) for t in (w_gu, s_gu, w_down, s_down))
     y = torch.empty((tokens, hidden), dtype=out_dtype, device=x.device)
     need = _lib.fp8q_moe_decode_workspace(tokens, hidden, inner, experts, top_k)
     ws, base = _workspace(need, x.device)
     _check(_lib.fp8q_moe_decode(x.data_ptr(), _ld(x), tokens, hidden, logits.data_ptr(),
                                 experts if tokens <= 1 else logits.stride(0), experts, top_k,
-                                1 if renormalize else 0, inner, w_gu.data_ptr(), ldw_gu, w_gu_stride, s_gu.data_ptr(),
-                                lds_gu, s_gu_stride, w_down.data_ptr(), ldw_down, w_down_stride, s_down.data_ptr(),
-                                lds_down, s_down_stride, y.data_ptr(), _dtype_code(y), _ld(y), base, need, _stream()),
+                                1 if renormalize else 0, inner, w_gu.data_ptr(), w_gu.stride(1),
+                                w_gu.stride(0), s_gu.data_ptr(), s_gu.stride(1), s_gu.stride(0), w_down.data_ptr(),
+                                w_down.stride(1), w_down.stride(0), s_down.data_ptr(), s_down.stride(1),
+                                s_down.stride(0), y.data_ptr(), _dtype_code(y), _ld(y), base, need, _stream()),
            "fp8q_moe_decode")
     return y
