@@ -747,11 +747,18 @@ hipError_t launch_moe_decode(const MoeArgs& a, hipStream_t st) {
     else if (a.experts <= 256) launch_route<4>(a, L, fused, st);
     else launch_route<kMaxExperts / 64>(a, L, fused, st);
     if (!fused) launch_up(a, L, st);
-    // All experts in one work-group where that is little to read for each: a
-    // kernel less is worth 2 to 5 us, but the work-groups do not fill the
-    // chip evenly (one token of 64 experts 7168/2048, 256 KiB each: 72 against
-    // 73 us; two tokens 130 against 124).
-    if (a.tokens <= kFewTokens && L.slots * 16 * a.inner <= 1 << 18) {
+    // All experts in one work-group where they are few, or little to read.  A
+    // kernel less is worth 2 to 3 us to a caller that waits for its launches
+    // and 1 to 5 us of the kernels' own time; but each expert costs its start
+    // there, and the work-groups do not fill the chip evenly.  (This kernel
+    // against the general one and its join, kernels' time: one token on 8 of 64
+    // experts 2048/512 16.6 and 18.9 us, 7168/2048 76.3 and 76.7, on 2 of 8
+    // experts 4096/14336 82 and 87; two tokens on 8 of 64 experts 2048/512 20.6
+    // and 21.2, 7168/2048 139 and 132; four 30.1 and 27.3.  A call of three
+    // tokens on 4 of 24 experts 1024/512: 19.9 and 22.3; six on 4 of 64: 22.7
+    // and 22.1.)
+    const bool few = L.slots <= 8 || L.slots * 16 * a.inner <= 1 << 17;
+    if (a.tokens <= kFewTokens && few) {
         hipLaunchKernelGGL(moe_down_few_kernel, dim3((unsigned)(a.hidden / 16)), dim3(64 * kFewWaves), 0, st, a, L);
     } else {
         launch_down(a, L, st);
