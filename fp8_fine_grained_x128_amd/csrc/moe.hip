@@ -15,8 +15,9 @@
 // Numerics: codes are converted to bf16 (exact) and multiplied by bf16
 // activations on the matrix cores, products exact and sums fp32; each
 // 128-wide chunk's sum is multiplied by its block scale into an fp32 total.
-// h is held as two bf16 numbers hi + lo (16 significant bits), so the second
-// product sees it with a relative error below 2^-16.
+// h is held as a sum of bf16 numbers: for a bf16 result two, hi + lo (16
+// significant bits: a relative error below 2^-16, the result's own rounding is
+// 2^-9), for an fp32 result three, hi + lo + rest, which hold all of its 24.
 //
 // MFMA 16x16x32 (bf16): A: lane l holds row l%16, 8 values of the K step;
 // B: column l%16, the same 8; D: lane l, element r is row 4*(l/16) + r,
@@ -49,7 +50,7 @@ struct MoeLayout {
     int64_t sets;   // uint64[tokens][words]
     int64_t count;  // int[tokens]: experts of the token; -1: its logits hold NaN or +inf
     int64_t prob;   // float[pairs]
-    int64_t hi, lo; // bf16[pairs][inner]: h
+    int64_t hi, lo, rest;  // bf16[pairs][inner], equally far apart: h
     int64_t parts;  // float[pairs][hidden]
     int64_t total;
 };
@@ -210,7 +211,7 @@ struct Weights {
 };
 
 // The same chunk of a lane's token.  NB: activation arrays whose sum is
-// multiplied (x, or hi and lo).
+// multiplied (x, or hi and lo, or hi, lo and rest).
 template <int NB>
 struct Tokens {
     uint4 b[NB][4];
@@ -223,7 +224,7 @@ struct Operands {
     const float* s[2];
     uint32_t row_offset;    // of the lane in a row tile
     const uint16_t* b[NG];  // the lane's token in every group; null: none
-    int64_t lo;             // elements from the first to the second activation array
+    int64_t lo;             // elements from one activation array to the next
 };
 
 template <int TILES, int NG>
@@ -260,7 +261,7 @@ __device__ __forceinline__ void load_tokens(Tokens<NB>& c, const uint16_t* b, in
     for (int n = 0; n < NB; ++n)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            c.b[n][j] = *reinterpret_cast<const uint4*>(b + n * lo + k + (NB == 2 ? 32 * j : 64 * (j >> 1) + 8 * (j & 1)));
+            c.b[n][j] = *reinterpret_cast<const uint4*>(b + n * lo + k + (NB > 1 ? 32 * j : 64 * (j >> 1) + 8 * (j & 1)));
 }
 
 template <int NB, int TILES>
@@ -437,16 +438,18 @@ __global__ __launch_bounds__(256, waves_of(TILES, NG)) void moe_up_kernel(MoeArg
                 const int64_t pair = s_pair[t0 + 16 * g + tok];
                 const float p = prob[pair];
                 const int64_t at = pair * a.inner + h_place(row0 + c);
-                float h[kPer];
-                uint16_t hi[kPer], lo[kPer];
+                const bool three = a.y_dtype == kDtypeF32;
+                uint16_t hi[kPer], lo[kPer], rest[kPer];
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) {
                     const int in = tok * 16 + (c & 15) + i;
                     const float gate = sum_waves(s_sums, c >> 4, in), up = sum_waves(s_sums, TILES / 2 + (c >> 4), in);
-                    h[i] = gate / (1.0f + expf(-gate)) * up * p;
-                    hi[i] = (uint16_t)pack_bf16(h[i], 0.0f);
-                    const float rest = h[i] - bf16_bits_to_f32(hi[i]);
-                    lo[i] = (hi[i] & 0x7f80u) == 0x7f80u ? 0 : (uint16_t)pack_bf16(rest, 0.0f);  // inf has no rest
+                    const float h = gate / (1.0f + expf(-gate)) * up * p;
+                    hi[i] = (uint16_t)pack_bf16(h, 0.0f);
+                    // both differences are exact; an infinite h has none
+                    const float l = (hi[i] & 0x7f80u) == 0x7f80u ? 0.0f : h - bf16_bits_to_f32(hi[i]);
+                    lo[i] = (uint16_t)pack_bf16(l, 0.0f);
+                    rest[i] = (uint16_t)pack_bf16(l - bf16_bits_to_f32(lo[i]), 0.0f);
                 }
                 uint16_t* to_hi = reinterpret_cast<uint16_t*>(ws + L.hi) + at;
                 uint16_t* to_lo = reinterpret_cast<uint16_t*>(ws + L.lo) + at;
@@ -455,14 +458,20 @@ __global__ __launch_bounds__(256, waves_of(TILES, NG)) void moe_up_kernel(MoeArg
                     to_hi[i] = hi[i];
                     to_lo[i] = lo[i];
                 }
+                if (three) {
+                    uint16_t* to_rest = reinterpret_cast<uint16_t*>(ws + L.rest) + at;
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) to_rest[i] = rest[i];
+                }
             }
             __syncthreads();
         }
     }
 }
 
-// Down projection: one fp32 row of the hidden size per pair.
-template <int TILES, int NG>
+// Down projection: one fp32 row of the hidden size per pair.  NB: arrays whose
+// sum is h.
+template <int NB, int TILES, int NG>
 __global__ __launch_bounds__(256, waves_of(TILES, NG)) void moe_down_kernel(MoeArgs a, MoeLayout L) {
     __shared__ __align__(16) float s_sums[4][TILES][256];
     __shared__ int s_token[kMaxTokens], s_pair[kMaxTokens];
@@ -489,7 +498,7 @@ __global__ __launch_bounds__(256, waves_of(TILES, NG)) void moe_down_kernel(MoeA
         }
         const int groups = min(NG, (e.count - t0 + 15) / 16);
         v4f acc[NG][TILES];
-        multiply<2>(acc, o, (int)(a.inner >> 7), wave, groups);
+        multiply<NB>(acc, o, (int)(a.inner >> 7), wave, groups);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             if (g >= groups) continue;
@@ -506,8 +515,9 @@ __global__ __launch_bounds__(256, waves_of(TILES, NG)) void moe_down_kernel(MoeA
 // Down projection and weighted sum of at most eight tokens: a work-group takes
 // 16 rows of the hidden size and all active experts, so y needs no partial
 // results.  Matrix columns 0..7 are the tokens' hi halves of h, columns 8..15
-// their lo halves (half the loads and products of separate operands); a token
-// that did not choose the expert takes nothing of it (its NaN neither).  The
+// their lo halves (half the loads and products of separate operands); an fp32
+// result's rests are a second operand; a token that did not choose the expert
+// takes nothing of it (its NaN neither).  The
 // eight waves share the (expert, chunk) pairs; weights are loaded three of
 // them ahead, h one ahead.
 //   One token of 8 experts of 7168/2048 (117 MB): 28 us, of which 19 are the
@@ -516,6 +526,7 @@ __global__ __launch_bounds__(256, waves_of(TILES, NG)) void moe_down_kernel(MoeA
 // compute units.
 constexpr int kFewWaves = 8;
 
+template <bool REST>
 __global__ __launch_bounds__(64 * kFewWaves, 4) void moe_down_few_kernel(MoeArgs a, MoeLayout L) {
     constexpr int kSlots = kFewTokens * FP8Q_MOE_MAX_TOP_K;
     __shared__ __align__(16) float s_sums[kFewWaves][256];
@@ -557,7 +568,8 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void moe_down_few_kernel(MoeArgs
     const uint32_t row_offset = (uint32_t)(r * a.ldw_down) + 16 * kq;
     const float* s_rows = a.s_down + (row0 >> 7) * a.lds_down;
     const uint16_t* half = reinterpret_cast<const uint16_t*>(ws + (r < kFewTokens ? L.hi : L.lo));
-    uint4 w[4][2], h[2][4];
+    const uint16_t* rests = reinterpret_cast<const uint16_t*>(ws + L.rest);
+    uint4 w[4][2], h[2][4], rest[2][REST ? 4 : 1];
     float scale[4];
     bool takes[2];  // the lane's token chose the expert
     auto load_w = [&](const Item& i, int slot) {
@@ -573,10 +585,19 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void moe_down_few_kernel(MoeArgs
         takes[slot] = pair >= 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) h[slot][j] = make_uint4(0, 0, 0, 0);
-        if (pair < 0) return;
-        const uint16_t* p = half + (int64_t)pair * a.inner + 128 * (int64_t)i.kb + 8 * kq;
+        if constexpr (REST) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h[slot][j] = *reinterpret_cast<const uint4*>(p + 32 * j);
+            for (int j = 0; j < 4; ++j) rest[slot][j] = make_uint4(0, 0, 0, 0);
+        }
+        if (pair < 0) return;
+        const int64_t at = (int64_t)pair * a.inner + 128 * (int64_t)i.kb + 8 * kq;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[slot][j] = *reinterpret_cast<const uint4*>(half + at + 32 * j);
+        if constexpr (REST) {
+            if (r >= kFewTokens) return;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) rest[slot][j] = *reinterpret_cast<const uint4*>(rests + at + 32 * j);
+        }
     };
     Item now{0, wave - kFewWaves}, next_h, next_w;
     advance(now);
@@ -600,8 +621,13 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void moe_down_few_kernel(MoeArgs
             v4f p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                p = mfma(bf16_of_codes(w[u][j].x, w[u][j].y), __builtin_bit_cast(v8bf, h[u & 1][2 * j]), p);
-                p = mfma(bf16_of_codes(w[u][j].z, w[u][j].w), __builtin_bit_cast(v8bf, h[u & 1][2 * j + 1]), p);
+                const v8bf w0 = bf16_of_codes(w[u][j].x, w[u][j].y), w1 = bf16_of_codes(w[u][j].z, w[u][j].w);
+                if constexpr (REST) {
+                    p = mfma(w0, __builtin_bit_cast(v8bf, rest[u & 1][2 * j]), p);
+                    p = mfma(w1, __builtin_bit_cast(v8bf, rest[u & 1][2 * j + 1]), p);
+                }
+                p = mfma(w0, __builtin_bit_cast(v8bf, h[u & 1][2 * j]), p);
+                p = mfma(w1, __builtin_bit_cast(v8bf, h[u & 1][2 * j + 1]), p);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[i] = takes[u & 1] ? __builtin_fmaf(p[i], scale[u], acc[i]) : acc[i];
@@ -660,6 +686,7 @@ MoeLayout moe_layout(int64_t tokens, int64_t hidden, int64_t inner, int experts,
     L.prob = take(4 * pairs);
     L.hi = take(2 * pairs * inner);
     L.lo = take(2 * pairs * inner);
+    L.rest = take(2 * pairs * inner);
     L.parts = take(4 * pairs * hidden);
     L.total = at;
     return L;
@@ -701,8 +728,9 @@ void launch_up(const MoeArgs& a, const MoeLayout& L, hipStream_t st) {
 
 template <int TILES, int NG>
 void launch_down(const MoeArgs& a, const MoeLayout& L, hipStream_t st) {
-    hipLaunchKernelGGL((moe_down_kernel<TILES, NG>), dim3((unsigned)(a.hidden / (16 * TILES)), (unsigned)L.slots),
-                       dim3(256), 0, st, a, L);
+    const dim3 grid((unsigned)(a.hidden / (16 * TILES)), (unsigned)L.slots);
+    if (a.y_dtype == kDtypeF32) hipLaunchKernelGGL((moe_down_kernel<3, TILES, NG>), grid, dim3(256), 0, st, a, L);
+    else hipLaunchKernelGGL((moe_down_kernel<2, TILES, NG>), grid, dim3(256), 0, st, a, L);
 }
 
 void launch_up(const MoeArgs& a, const MoeLayout& L, hipStream_t st) {
@@ -756,10 +784,15 @@ hipError_t launch_moe_decode(const MoeArgs& a, hipStream_t st) {
     // experts 4096/14336 82 and 87; two tokens on 8 of 64 experts 2048/512 20.6
     // and 21.2, 7168/2048 139 and 132; four 30.1 and 27.3.  A call of three
     // tokens on 4 of 24 experts 1024/512: 19.9 and 22.3; six on 4 of 64: 22.7
-    // and 22.1.)
-    const bool few = L.slots <= 8 || L.slots * 16 * a.inner <= 1 << 17;
+    // and 22.1.  With the rests of an fp32 result: one token on 8 of 64 experts
+    // 2048/512 19.3 and 21.4, 7168/2048 85 and 76; four on 2 of 16 experts
+    // 2048/1024 22.9 and 21.0.)
+    const int64_t bytes = L.slots * 16 * a.inner;
+    const bool few = a.y_dtype == kDtypeF32 ? bytes <= 1 << 16 : L.slots <= 8 || bytes <= 1 << 17;
     if (a.tokens <= kFewTokens && few) {
-        hipLaunchKernelGGL(moe_down_few_kernel, dim3((unsigned)(a.hidden / 16)), dim3(64 * kFewWaves), 0, st, a, L);
+        const dim3 grid((unsigned)(a.hidden / 16)), block(64 * kFewWaves);
+        if (a.y_dtype == kDtypeF32) hipLaunchKernelGGL(moe_down_few_kernel<true>, grid, block, 0, st, a, L);
+        else hipLaunchKernelGGL(moe_down_few_kernel<false>, grid, block, 0, st, a, L);
     } else {
         launch_down(a, L, st);
         hipLaunchKernelGGL(moe_join_kernel, dim3((unsigned)((a.hidden + 255) / 256), (unsigned)a.tokens), dim3(256), 0,

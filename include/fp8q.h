@@ -467,8 +467,9 @@ int fp8q_swiglu_backward_quantize(const uint8_t *qg, const uint8_t *qu, int64_t 
  * An empty S_t gives a zero row (an empty slot of a batch); a token with a
  * NaN or +inf logit gives a row of NaN, as its softmax would.
  * y[tokens][hidden] (y_dtype, stride ldy).  Weights and x are multiplied
- * exactly and summed in fp32; the SwiGLU's result is held to 16 significant
- * bits between the products.  Repeated calls give the same bits.
+ * exactly and summed in fp32; the SwiGLU's result is held between the products
+ * to the 24 significant bits of an fp32 y, or to 16 for a bf16 one.  Repeated
+ * calls give the same bits.
  * hidden and inner are multiples of 128; tokens <= FP8Q_MOE_MAX_TOKENS,
  * top_k <= FP8Q_MOE_MAX_TOP_K, experts <= 1024 (else FP8Q_EUNSUPPORTED).
  * workspace: at least fp8q_moe_decode_workspace(...) bytes (0 for sizes that
