@@ -265,9 +265,15 @@ def _check(status: int, what: str) -> None:
         raise Fp8qError(status, what)
 
 
+# Not a documented function of torch; the documented one makes a Stream object, 3 us a call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream() -> int:
-    """Handle of torch's current stream (the raw handle: a Stream object costs 3 us a call)."""
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    """Handle of torch's current stream."""
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _dtype_code(t: torch.Tensor) -> int:
