@@ -202,7 +202,6 @@ __global__ __launch_bounds__(64) void moe_route_kernel(MoeArgs a, MoeLayout L) {
 // reads of the tokens and of the weights; expert_variant() chooses.
 // ----------------------------------------------------------------------------
 
-// ----------------------------------------------------------------------------
 // A 128-wide chunk of TILES row tiles.
 template <int TILES>
 struct Weights {
