@@ -708,9 +708,9 @@ struct Variant {
 // tokens per expert (64 tokens, 8 of 64 experts 7168/2048: 500 us against 528,
 // 16 tokens: 430 against 425), if there are still two work-groups for every
 // compute unit (8 of 8 experts 2048/1024, half a work-group: 65 against 49).
-// Two tiles where four give less than one (one token, 2 experts 4096/14336: 82
-// us, 91 with four; with enough of them they are slower: 16 tokens, 8 of 64
-// experts 7168/2048, 452 against 427).
+// Two tiles where four give less than one (12 tokens, 2 experts 4096/14336: 96
+// us, 108 with four; 16 tokens, 4 experts 2048/8192: 61 and 68; with enough of
+// them they are slower: 16 tokens, 8 of 64 experts 7168/2048, 452 against 427).
 Variant expert_variant(const MoeArgs& a, const MoeLayout& L, int64_t tiles) {
     const int64_t pairs = a.tokens * a.top_k;
     if (pairs >= 32 * L.slots) return {4, 4};

@@ -256,7 +256,7 @@ __device__ __forceinline__ void fill_weights(LdsWeights<N>& to, const void* w, i
 // one.  A work-group's rows are consecutive, so the scales that it writes fill
 // whole lines.  Many rows, or narrow ones.  G work-groups are meant to share a
 // compute unit.  (8192x7168: RMS norm in bf16 with codes and values 56 us (5.3
-// TB/s), codes alone 40, layer norm 58 and 49; fp32 100 and 64.  Non-temporal
+// TB/s), codes alone 40, layer norm 58 and 46; fp32 100 and 64.  Non-temporal
 // stores of y are worth 7 us in bf16 and cost 19 in fp32.  A wave per row
 // needs over 200 registers there and took 85, a work-group per row reads the
 // weights again for every row, 88.  Bound by memory with values, by vector

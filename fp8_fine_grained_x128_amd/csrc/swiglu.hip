@@ -273,8 +273,9 @@ __global__ __launch_bounds__(256) void swiglu_backward_kernel(SwigluBackwardArgs
 // 8*(t%16) .. +7 of rows 4*(t/16) .. +3, so a row's tile maximum is a DPP row
 // maximum and a column's goes through LDS.  The codes of the 128x1 tiles are
 // transposed in LDS (tile_place).
-//   8192x7168 bf16 moves 541 MB, the bytes it cannot do without, in 106 to
-// 125 us (4.3 to 5.1 TB/s, run by run).  Memory and arithmetic share the
+//   8192x7168 bf16 moves 541 MB, the bytes it cannot do without, in 105 to
+// 120 us (4.5 to 5.1 TB/s, run by run), with power-of-two scales in 95; fp32
+// 659 MB in 140.  Memory and arithmetic share the
 // bound: 48 instructions per element keep the vector units busy for two
 // thirds of that, and 128 registers hold 16 waves on a compute unit.
 // ----------------------------------------------------------------------------

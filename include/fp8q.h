@@ -354,7 +354,9 @@ int fp8q_clock_probe(uint64_t *out, int64_t ticks, void *stream);
  * Operators around the GEMMs of a feed-forward block: the norm in front of
  * it, the SwiGLU between its GEMMs, and the whole mixture-of-experts layer
  * for the few tokens of a decode step.  The conventions above hold; sums,
- * statistics and everything between the stored types are fp32.
+ * statistics and everything between the stored types are fp32.  A result that
+ * is NaN or infinite shows in its tile, whose scale is NaN or infinite (or, with
+ * FP8Q_SCALE_POW2, whose code is NaN); other tiles are not touched by it.
  * ---------------------------------------------------------------------------
  */
 
