@@ -355,8 +355,8 @@ int fp8q_clock_probe(uint64_t *out, int64_t ticks, void *stream);
  * it, the SwiGLU between its GEMMs, and the whole mixture-of-experts layer
  * for the few tokens of a decode step.  The conventions above hold; sums,
  * statistics and everything between the stored types are fp32.  A result that
- * is NaN or infinite shows in its tile, whose scale is NaN or infinite (or, with
- * FP8Q_SCALE_POW2, whose code is NaN); other tiles are not touched by it.
+ * is NaN or infinite shows: its tile's scale, or with FP8Q_SCALE_POW2 its own
+ * dequantized value, is no finite number; other tiles are not touched by it.
  * ---------------------------------------------------------------------------
  */
 
