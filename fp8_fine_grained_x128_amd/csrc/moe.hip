@@ -774,20 +774,26 @@ hipError_t launch_moe_decode(const MoeArgs& a, hipStream_t st) {
     else if (a.experts <= 256) launch_route<4>(a, L, fused, st);
     else launch_route<kMaxExperts / 64>(a, L, fused, st);
     if (!fused) launch_up(a, L, st);
-    // All experts in one work-group where they are few, or little to read.  A
-    // kernel less is worth 2 to 3 us to a caller that waits for its launches
-    // and 1 to 5 us of the kernels' own time; but each expert costs its start
-    // there, and the work-groups do not fill the chip evenly.  (This kernel
-    // against the general one and its join, kernels' time: one token on 8 of 64
-    // experts 2048/512 16.6 and 18.9 us, 7168/2048 76.3 and 76.7, on 2 of 8
-    // experts 4096/14336 82 and 87; two tokens on 8 of 64 experts 2048/512 20.6
-    // and 21.2, 7168/2048 139 and 132; four 30.1 and 27.3.  A call of three
-    // tokens on 4 of 24 experts 1024/512: 19.9 and 22.3; six on 4 of 64: 22.7
-    // and 22.1.  With the rests of an fp32 result: one token on 8 of 64 experts
+    // All experts in one work-group where they are little to read, or few for
+    // few tokens.  A kernel less is worth 2 to 3 us to a caller that waits for
+    // its launches and 1 to 10 us of the kernels' own time; but each expert
+    // costs its start there, and there are only hidden / 16 work-groups.  (This
+    // kernel against the general one and its join, kernels' time.  Hidden 2048,
+    // half a work-group for each compute unit: one token on 8 of 64 experts
+    // 2048/512 16.6 and 18.9 us, two 20.6 and 21.2, four 30.1 and 27.3, eight on
+    // 2 of 8 experts 2048/8192 104 and 84.  Hidden 4096 and 7168: one token on
+    // 8 of 64 experts 7168/2048 76.3 and 76.7, on 2 of 8 experts 4096/14336 82
+    // and 87; four on 8 experts 195 and 205; two on 8 of 64 experts 7168/2048
+    // 139 and 132; eight on 2 of 8 experts 4096/2048 51 and 54, 4096/14336 261
+    // and 254.  A call of three tokens on 4 of 24 experts 1024/512: 19.9 and
+    // 22.3.  With the rests of an fp32 result: one token on 8 of 64 experts
     // 2048/512 19.3 and 21.4, 7168/2048 85 and 76; four on 2 of 16 experts
     // 2048/1024 22.9 and 21.0.)
     const int64_t bytes = L.slots * 16 * a.inner;
-    const bool few = a.y_dtype == kDtypeF32 ? bytes <= 1 << 16 : L.slots <= 8 || bytes <= 1 << 17;
+    const bool wide = a.hidden / 16 >= cus;
+    const bool few = a.y_dtype == kDtypeF32
+                         ? bytes <= 1 << 16
+                         : bytes <= 1 << 17 || (wide && (bytes <= 1 << 18 || (a.tokens <= 4 && L.slots <= 8)));
     if (a.tokens <= kFewTokens && few) {
         const dim3 grid((unsigned)(a.hidden / 16)), block(64 * kFewWaves);
         if (a.y_dtype == kDtypeF32) hipLaunchKernelGGL(moe_down_few_kernel<true>, grid, block, 0, st, a, L);
