@@ -569,18 +569,23 @@ void launch_teams(const LayernormArgs& a, hipStream_t st) {
     launch(std::false_type{});
 }
 
+// Rows per compute unit from which teams are faster than a work-group per row.
+// (bf16 with values, then fp32 layer norm into codes, teams against work-groups
+// in us, at 1300 and 1800 rows on 256 compute units: 1024 columns 4.4 and 4.6,
+// 4.5 and 5.5; 4.5 and 5.0, 4.6 and 5.6; 2048 columns 5.5 and 5.2, 6.0 and 6.4;
+// 6.7 and 5.8, 7.5 and 7.0; 4096 columns 8.6 and 12.2, 9.6 and 15.5; 10.2 and
+// 13.7, 11.2 and 17.8; 8192 columns 16.1 and 16.1, 18.5 and 20.2; 21.4 and 20.0,
+// 22.4 and 25.7.  512x4096: 5.8 and 5.6; 6.4 and 6.1.)
+int rows_for_teams(int64_t cols) { return cols <= 1024 ? 5 : cols <= 2048 ? 8 : cols <= 4096 ? 4 : 6; }
+
 // Many rows, and narrow ones, go to teams; few wide rows get a work-group
-// each.  They change places at about four rows per compute unit (bf16 with
-// values, teams against a work-group a row: 512 rows of 2000 columns 5.2 and
-// 4.0 us, of 4096 5.8 and 5.6, of 7168 7.4 and 6.6; 1024 rows 5.5 and 4.7, 6.8
-// and 9.6, 10.5 and 11.4; 2048 rows 6.4 and 7.0, 10.0 and 16.1, 18.2 and 20.9;
-// fp32 codes: 512x4096 6.4 and 6.1, 1024x4096 8.2 and 10.9).  Four groups per lane carry a row's fixed work best (16384x4096 bf16,
+// each.  Four groups per lane carry a row's fixed work best (16384x4096 bf16,
 // codes: 51 us with 128 lanes a row, 56 with 256 lanes of two groups).
 // Registers and LDS decide how many work-groups share a compute unit.
 template <typename T>
 void launch_forward_for(const LayernormArgs& a, hipStream_t st) {
     constexpr int kShare = sizeof(T) == 2 ? 3 : 2;
-    const bool many = a.rows >= 4 * (int64_t)compute_units();
+    const bool many = a.rows >= rows_for_teams(a.cols) * (int64_t)compute_units();
     if (a.cols <= 128) launch_teams<float, T, 16, 1, 4>(a, st);
     else if (a.cols <= 512) launch_teams<float, T, 64, 1, 4>(a, st);
     else if (a.cols <= 1024 && many) launch_teams<float, T, 64, 2, kShare>(a, st);
