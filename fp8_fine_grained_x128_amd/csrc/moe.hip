@@ -437,8 +437,8 @@ __global__ __launch_bounds__(256, waves_of(TILES, NG)) void moe_up_kernel(MoeArg
                 const int64_t pair = s_pair[t0 + 16 * g + tok];
                 const float p = prob[pair];
                 const int64_t at = pair * a.inner + h_place(row0 + c);
-                const bool three = a.y_dtype == kDtypeF32;
-                uint16_t hi[kPer], lo[kPer], rest[kPer];
+                float rest[kPer];
+                uint16_t hi[kPer], lo[kPer];
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) {
                     const int in = tok * 16 + (c & 15) + i;
@@ -448,7 +448,7 @@ __global__ __launch_bounds__(256, waves_of(TILES, NG)) void moe_up_kernel(MoeArg
                     // both differences are exact; an infinite h has none
                     const float l = (hi[i] & 0x7f80u) == 0x7f80u ? 0.0f : h - bf16_bits_to_f32(hi[i]);
                     lo[i] = (uint16_t)pack_bf16(l, 0.0f);
-                    rest[i] = (uint16_t)pack_bf16(l - bf16_bits_to_f32(lo[i]), 0.0f);
+                    rest[i] = l - bf16_bits_to_f32(lo[i]);
                 }
                 uint16_t* to_hi = reinterpret_cast<uint16_t*>(ws + L.hi) + at;
                 uint16_t* to_lo = reinterpret_cast<uint16_t*>(ws + L.lo) + at;
@@ -457,10 +457,10 @@ __global__ __launch_bounds__(256, waves_of(TILES, NG)) void moe_up_kernel(MoeArg
                     to_hi[i] = hi[i];
                     to_lo[i] = lo[i];
                 }
-                if (three) {
+                if (a.y_dtype == kDtypeF32) {
                     uint16_t* to_rest = reinterpret_cast<uint16_t*>(ws + L.rest) + at;
 #pragma unroll
-                    for (int i = 0; i < kPer; ++i) to_rest[i] = rest[i];
+                    for (int i = 0; i < kPer; ++i) to_rest[i] = (uint16_t)pack_bf16(rest[i], 0.0f);
                 }
             }
             __syncthreads();
