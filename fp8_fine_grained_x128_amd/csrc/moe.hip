@@ -50,10 +50,12 @@ struct MoeLayout {
     int64_t sets;   // uint64[tokens][words]
     int64_t count;  // int[tokens]: experts of the token; -1: its logits hold NaN or +inf
     int64_t prob;   // float[pairs]
-    int64_t hi, lo, rest;  // bf16[pairs][inner], equally far apart: h
+    int64_t hi, lo;  // bf16[pairs][inner], and a third, as far on, for rest: h
     int64_t parts;  // float[pairs][hidden]
     int64_t total;
 };
+
+__device__ __forceinline__ int64_t rest_of(const MoeLayout& L) { return 2 * L.lo - L.hi; }
 
 __device__ __forceinline__ v8bf bf16_of_codes(uint32_t w0, uint32_t w1) {
     v8bf r;
@@ -403,6 +405,10 @@ __global__ __launch_bounds__(256, waves_of(TILES, NG)) void moe_up_kernel(MoeArg
     }
     if (e.expert < 0) return;
     __syncthreads();
+    int y_dtype = __builtin_amdgcn_readfirstlane(a.y_dtype);
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile("" : "+s"(y_dtype));  // loaded here: where it is used its load would be waited for (0.2 us)
+#endif
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, kq = lane >> 4;
     constexpr int kCols = 8 * TILES;  // columns of h
@@ -457,8 +463,8 @@ __global__ __launch_bounds__(256, waves_of(TILES, NG)) void moe_up_kernel(MoeArg
                     to_hi[i] = hi[i];
                     to_lo[i] = lo[i];
                 }
-                if (a.y_dtype == kDtypeF32) {
-                    uint16_t* to_rest = reinterpret_cast<uint16_t*>(ws + L.rest) + at;
+                if (y_dtype == kDtypeF32) {
+                    uint16_t* to_rest = reinterpret_cast<uint16_t*>(ws + rest_of(L)) + at;
 #pragma unroll
                     for (int i = 0; i < kPer; ++i) to_rest[i] = (uint16_t)pack_bf16(rest[i], 0.0f);
                 }
@@ -567,7 +573,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void moe_down_few_kernel(MoeArgs
     const uint32_t row_offset = (uint32_t)(r * a.ldw_down) + 16 * kq;
     const float* s_rows = a.s_down + (row0 >> 7) * a.lds_down;
     const uint16_t* half = reinterpret_cast<const uint16_t*>(ws + (r < kFewTokens ? L.hi : L.lo));
-    const uint16_t* rests = reinterpret_cast<const uint16_t*>(ws + L.rest);
+    const uint16_t* rests = reinterpret_cast<const uint16_t*>(ws + rest_of(L));
     uint4 w[4][2], h[2][4], rest[2][REST ? 4 : 1];
     float scale[4];
     bool takes[2];  // the lane's token chose the expert
@@ -685,7 +691,7 @@ MoeLayout moe_layout(int64_t tokens, int64_t hidden, int64_t inner, int experts,
     L.prob = take(4 * pairs);
     L.hi = take(2 * pairs * inner);
     L.lo = take(2 * pairs * inner);
-    L.rest = take(2 * pairs * inner);
+    take(2 * pairs * inner);
     L.parts = take(4 * pairs * hidden);
     L.total = at;
     return L;
@@ -781,7 +787,8 @@ hipError_t launch_moe_decode(const MoeArgs& a, hipStream_t st) {
     // kernel against the general one and its join, kernels' time.  Hidden 2048,
     // half a work-group for each compute unit: one token on 8 of 64 experts
     // 2048/512 16.6 and 18.9 us, two 20.6 and 21.2, four 30.1 and 27.3, eight on
-    // 2 of 8 experts 2048/8192 104 and 84.  Hidden 4096 and 7168: one token on
+    // 2 of 8 experts 2048/8192 104 and 84; one token on 7 experts 1280/1408 20.4
+    // and 20.9, five on 8 experts 512/1280 21.8 and 18.6.  Hidden 4096 and 7168: one token on
     // 8 of 64 experts 7168/2048 76.3 and 76.7, on 2 of 8 experts 4096/14336 82
     // and 87; four on 8 experts 195 and 205; two on 8 of 64 experts 7168/2048
     // 139 and 132; eight on 2 of 8 experts 4096/2048 51 and 54, 4096/14336 261
@@ -790,10 +797,9 @@ hipError_t launch_moe_decode(const MoeArgs& a, hipStream_t st) {
     // 2048/512 19.3 and 21.4, 7168/2048 85 and 76; four on 2 of 16 experts
     // 2048/1024 22.9 and 21.0.)
     const int64_t bytes = L.slots * 16 * a.inner;
-    const bool wide = a.hidden / 16 >= cus;
-    const bool few = a.y_dtype == kDtypeF32
-                         ? bytes <= 1 << 16
-                         : bytes <= 1 << 17 || (wide && (bytes <= 1 << 18 || (a.tokens <= 4 && L.slots <= 8)));
+    const bool wide = a.hidden / 16 >= cus, light = a.tokens <= 4 && L.slots <= 8;
+    const bool few = a.y_dtype == kDtypeF32 ? bytes <= 1 << 16
+                                            : bytes <= (wide || light ? 1 << 18 : 1 << 17) || (wide && light);
     if (a.tokens <= kFewTokens && few) {
         const dim3 grid((unsigned)(a.hidden / 16)), block(64 * kFewWaves);
         if (a.y_dtype == kDtypeF32) hipLaunchKernelGGL(moe_down_few_kernel<true>, grid, block, 0, st, a, L);
