@@ -47,10 +47,10 @@ WARMUP_FLOOR_MS = 300.0
 # HBM-side bytes per launch of the fprop GEMM, from two rocprofv3 PMC passes
 # (FETCH_SIZE, WRITE_SIZE) over this bench, each scaled by what the same counter
 # reads for a plain 1 GiB device copy (FETCH x2.0, WRITE x1.0).  The figure is
-# tied to the GEMM source it was taken on: once gemm.hip changes it is reported
-# as null until the counters are taken again (the digest covers the source and
-# its extra compiler flags).
-GEMM_PMC = {"src_sha256_16": "fcec57018796cfe0", "read_bytes": 346_732_544, "write_bytes": 59_249_664}
+# tied to the GEMM source it was taken on: once gemm.hip or gemm_tile.hpp
+# changes it is reported as null until the counters are taken again (the digest
+# covers both sources and their extra compiler flags).
+GEMM_PMC = {"src_sha256_16": "f806ad272ea8654f", "read_bytes": 346_732_544, "write_bytes": 59_249_664}
 
 
 def _parse():
@@ -73,10 +73,12 @@ def _parse():
 
 def _gemm_traffic():
     import hashlib
-    src = os.path.join(ROOT, "fp8_fine_grained_x128_amd", "csrc", "gemm.hip")
     from fp8_fine_grained_x128_amd._build import SOURCE_FLAGS
-    with open(src, "rb") as f:
-        text = f.read() + " ".join(SOURCE_FLAGS.get("gemm.hip", [])).encode()
+    text = b""
+    for name in ("gemm.hip", "gemm_tile.hpp"):
+        with open(os.path.join(ROOT, "fp8_fine_grained_x128_amd", "csrc", name), "rb") as f:
+            text += f.read()
+    text += " ".join(SOURCE_FLAGS.get("gemm.hip", [])).encode()
     digest = hashlib.sha256(text).hexdigest()[:16]
     if digest != GEMM_PMC["src_sha256_16"]:
         return None
