@@ -20,6 +20,10 @@ from .binding import (  # noqa: F401
     SwigluGrads, fp8q_layernorm, fp8q_layernorm_backward, fp8q_layernorm_backward_workspace, fp8q_moe_decode,
     fp8q_moe_decode_workspace, fp8q_swiglu_backward, fp8q_swiglu_backward_quantize, fp8q_swiglu_quantize, layernorm,
     layernorm_backward, moe_decode, swiglu_backward, swiglu_backward_quantize, swiglu_quantize,
+    AdamwState, AdamwTensors, GroupedOperand, WeightCodes, adamw, adamw_state, adamw_tensors, fp8q_adamw,
+    fp8q_adamw_config, fp8q_adamw_tensor, fp8q_grouped_padded_rows, fp8q_grouped_quantize_act,
+    fp8q_grouped_requant_transpose, fp8q_grouped_wgrad, fp8q_grouped_wgrad_workspace, grouped_quantize_act,
+    grouped_requant_transpose, grouped_wgrad, weight_codes,
 )
 
-__version__ = "0.3.0"
+__version__ = "0.4.0"

@@ -14,8 +14,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfp8q.so")
-SOURCES = ["quantize.hip", "gemm.hip", "transpose.hip", "norm.hip", "swiglu.hip", "moe.hip", "fp8q_api.hip",
-           "clock_probe.hip"]
+SOURCES = ["quantize.hip", "gemm.hip", "grouped_wgrad.hip", "adamw.hip", "transpose.hip", "norm.hip", "swiglu.hip",
+           "moe.hip", "fp8q_api.hip", "clock_probe.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [
@@ -29,6 +29,7 @@ HIPCC_FLAGS = [
 # plain GEMM and 3 % on the grouped GEMM, with bit-identical outputs.
 SOURCE_FLAGS = {
     "gemm.hip": ["-mllvm", "-amdgpu-sched-strategy=iterative-ilp"],
+    "grouped_wgrad.hip": ["-mllvm", "-amdgpu-sched-strategy=iterative-ilp"],
 }
 
 

@@ -6,9 +6,10 @@ Two layers, both argument marshalling only:
   as Python ints, ``stream`` as an int handle or None);
 * tensor helpers (``quantize_act``, ``quantize_weight``, ``requant_transpose``,
   ``gemm``, ``grouped_gemm``; ``layernorm``, ``swiglu_quantize``, their backward
-  passes and ``moe_decode``) that take torch tensors on the HIP device,
-  allocate outputs and workspaces with torch, derive leading dimensions from
-  strides and enqueue on torch's current stream.
+  passes and ``moe_decode``; ``grouped_quantize_act``,
+  ``grouped_requant_transpose``, ``grouped_wgrad`` and ``adamw``) that take
+  torch tensors on the HIP device, allocate outputs and workspaces with torch,
+  derive leading dimensions from strides and enqueue on torch's current stream.
 
 Every computation runs in the library's HIP kernels.  If the library is not
 built, importing this module raises: there is no fallback.
@@ -17,7 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import NamedTuple, Optional, Tuple
+from typing import NamedTuple, Optional, Sequence, Tuple, Union
 
 import torch
 
@@ -49,8 +50,10 @@ EXPORTS = ("fp8q_quantize_act", "fp8q_quantize_weight", "fp8q_requant_transpose"
            "fp8q_quantize_weight_ex", "fp8q_requant_transpose_ex", "fp8q_transpose_weight",
            "fp8q_gather_quantize_act", "fp8q_gemm_splitk", "fp8q_gemm_splitk_noalloc", "fp8q_clock_probe",
            "fp8q_layernorm", "fp8q_layernorm_backward", "fp8q_swiglu_quantize", "fp8q_swiglu_backward",
-           "fp8q_swiglu_backward_quantize", "fp8q_moe_decode", "fp8q_layernorm_backward_workspace",
-           "fp8q_moe_decode_workspace", "fp8q_gemm_splitk_workspace", "fp8q_strerror", "fp8q_version")
+           "fp8q_swiglu_backward_quantize", "fp8q_moe_decode", "fp8q_grouped_quantize_act",
+           "fp8q_grouped_requant_transpose", "fp8q_grouped_wgrad", "fp8q_adamw", "fp8q_grouped_padded_rows",
+           "fp8q_grouped_wgrad_workspace", "fp8q_layernorm_backward_workspace", "fp8q_moe_decode_workspace",
+           "fp8q_gemm_splitk_workspace", "fp8q_strerror", "fp8q_version")
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is not built; run __graft_entry__.build() (hipcc, gfx950)")
@@ -92,11 +95,31 @@ _lib.fp8q_swiglu_backward_quantize.argtypes = [_p, _p, _i64, _p, _p, _i64, _p, _
 _lib.fp8q_moe_decode_workspace.argtypes = [_i64, _i64, _i64, _i32, _i32]
 _lib.fp8q_moe_decode.argtypes = [_p, _i64, _i64, _i64, _p, _i64, _i32, _i32, _i32, _i64, _p, _i64, _i64, _p, _i64,
                                  _i64, _p, _i64, _i64, _p, _i64, _i64, _p, _i32, _i64, _p, _i64, _p]
+_lib.fp8q_grouped_padded_rows.argtypes = [_i64, _i32]
+_lib.fp8q_grouped_quantize_act.argtypes = [_p, _i32, _i64, _i64, _i64, _p, _i32, _p, _i64, _p, _i64, _i32, _p]
+_lib.fp8q_grouped_requant_transpose.argtypes = [_p, _i64, _i64, _i64, _p, _i64, _p, _i32, _p, _i64, _p, _i64, _i32, _p]
+_lib.fp8q_grouped_wgrad_workspace.argtypes = [_i64, _i32, _i64, _i64]
+_lib.fp8q_grouped_wgrad.argtypes = [_p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i32, _i64, _i64, _i64, _p, _i32, _i64,
+                                    _i64, _i32, _u32, _p, _i64, _p]
+_f64 = ctypes.c_double
+
+
+class fp8q_adamw_tensor(ctypes.Structure):
+    _fields_ = [("n", _i64), ("p", _p), ("g", _p), ("m", _p), ("v", _p), ("sm", _p), ("sv", _p), ("N", _i64),
+                ("K", _i64), ("q", _p), ("s", _p), ("qt", _p), ("st", _p)]
+
+
+class fp8q_adamw_config(ctypes.Structure):
+    _fields_ = [("lr", _f64), ("beta1", _f64), ("beta2", _f64), ("eps", _f64), ("weight_decay", _f64), ("step", _i64),
+                ("lr_dev", _p), ("step_dev", _p), ("grad_scale", _p), ("seed", ctypes.c_uint32)]
+
+
+_lib.fp8q_adamw.argtypes = [_p, _i32, _i32, _i32, _p, _i32, _p]
 _lib.fp8q_strerror.argtypes = [_i32]
 _lib.fp8q_strerror.restype = ctypes.c_char_p
 _lib.fp8q_version.argtypes = []
 for _n in EXPORTS[:-3]:
-    getattr(_lib, _n).restype = _i64 if _n.endswith("_workspace") else _i32
+    getattr(_lib, _n).restype = _i64 if _n.endswith(("_workspace", "_padded_rows")) else _i32
 
 
 def library() -> ctypes.CDLL:
@@ -237,6 +260,38 @@ def fp8q_moe_decode(x, ldx, tokens, hidden, logits, ldl, experts, top_k, renorma
     return _lib.fp8q_moe_decode(x, ldx, tokens, hidden, logits, ldl, experts, top_k, renormalize, inner, w_gu, ldw_gu,
                                 w_gu_stride, s_gu, lds_gu, s_gu_stride, w_down, ldw_down, w_down_stride, s_down,
                                 lds_down, s_down_stride, y, y_dtype, ldy, workspace, workspace_bytes, stream)
+
+
+def fp8q_grouped_padded_rows(rows, G) -> int:
+    return _lib.fp8q_grouped_padded_rows(rows, G)
+
+
+def fp8q_grouped_quantize_act(x, x_dtype, rows, cols, ldx, group_offsets, G, qt, ldqt, st, ldst, scale_mode,
+                              stream=None) -> int:
+    return _lib.fp8q_grouped_quantize_act(x, x_dtype, rows, cols, ldx, group_offsets, G, qt, ldqt, st, ldst,
+                                          scale_mode, stream)
+
+
+def fp8q_grouped_requant_transpose(q, rows, cols, ldq, s, lds, group_offsets, G, qt, ldqt, st, ldst, scale_mode,
+                                   stream=None) -> int:
+    return _lib.fp8q_grouped_requant_transpose(q, rows, cols, ldq, s, lds, group_offsets, G, qt, ldqt, st, ldst,
+                                               scale_mode, stream)
+
+
+def fp8q_grouped_wgrad_workspace(rows, G, N, K) -> int:
+    return _lib.fp8q_grouped_wgrad_workspace(rows, G, N, K)
+
+
+def fp8q_grouped_wgrad(a, lda, sa, ldsa, b, ldb, sb, ldsb, group_offsets, G, rows, N, K, dw, dw_dtype, lddw,
+                       dw_group_stride, accumulate, flags, workspace, workspace_bytes, stream=None) -> int:
+    return _lib.fp8q_grouped_wgrad(a, lda, sa, ldsa, b, ldb, sb, ldsb, group_offsets, G, rows, N, K, dw, dw_dtype,
+                                   lddw, dw_group_stride, accumulate, flags, workspace, workspace_bytes, stream)
+
+
+def fp8q_adamw(tensors, count, g_dtype, bits, config, scale_mode, stream=None) -> int:
+    """tensors: an array of fp8q_adamw_tensor (or its address); config: a fp8q_adamw_config."""
+    return _lib.fp8q_adamw(tensors, count, g_dtype, bits, None if config is None else ctypes.addressof(config),
+                           scale_mode, stream)
 
 
 NORM_MAX_COLS = 16384
@@ -804,3 +859,279 @@ def moe_decode(x: torch.Tensor, logits: torch.Tensor, w_gu: torch.Tensor, s_gu: 
                                 s_down.stride(0), y.data_ptr(), _dtype_code(y), _ld(y), base, need, _stream()),
            "fp8q_moe_decode")
     return y
+
+
+# ------------------------------------------------------------------ experts' weight gradients, AdamW
+
+def _on_current_device(what: str, *ts: torch.Tensor) -> None:
+    """Every tensor on torch's current HIP device, whose current stream the call goes to."""
+    _on_device(what, *ts)
+    if ts and ts[0].device.index != torch.cuda.current_device():
+        raise ValueError(f"{what}: tensors on {ts[0].device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _check_offsets(what: str, offsets: torch.Tensor) -> int:
+    """int32 [G+1], dense; gives G."""
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 2 or not offsets.is_contiguous():
+        raise ValueError(f"{what}: offsets must be a contiguous int32 vector of the groups and one more, got "
+                         f"{tuple(offsets.shape)} {offsets.dtype}")
+    return offsets.numel() - 1
+
+
+class GroupedOperand(NamedTuple):
+    """An operand of grouped_wgrad(): codes [channels][padded tokens], every group in whole 128-token chunks, scales
+    [chunks][channels], and the rows of all groups together that it was made from."""
+    q: torch.Tensor
+    s: torch.Tensor
+    rows: int
+
+
+def _grouped_operand(rows: int, cols: int, G: int, device) -> GroupedOperand:
+    padded = _lib.fp8q_grouped_padded_rows(rows, G)
+    return GroupedOperand(torch.empty((cols, padded), dtype=torch.uint8, device=device),
+                          _scales(padded // 128, cols, device), rows)
+
+
+def grouped_quantize_act(x: torch.Tensor, offsets: torch.Tensor, scale_mode: int = FP8Q_SCALE_FP32) -> GroupedOperand:
+    """Rows x[offsets[g] .. offsets[g+1]) of each group in 128x1 tiles of their own, transposed; see
+    fp8q_grouped_quantize_act.  Codes and scales past the last group's chunks hold what the memory held."""
+    G = _check_offsets("grouped_quantize_act", offsets)
+    rows, cols = x.shape
+    _on_current_device("grouped_quantize_act", x, offsets)
+    o = _grouped_operand(rows, cols, G, x.device)
+    _check(_lib.fp8q_grouped_quantize_act(x.data_ptr(), _dtype_code(x), rows, cols, _ld(x), offsets.data_ptr(), G,
+                                          o.q.data_ptr(), o.q.shape[1], o.s.data_ptr(), cols, scale_mode, _stream()),
+           "fp8q_grouped_quantize_act")
+    return o
+
+
+def grouped_requant_transpose(q: torch.Tensor, s: torch.Tensor, offsets: torch.Tensor,
+                              scale_mode: int = FP8Q_SCALE_FP32) -> GroupedOperand:
+    """Cached 1x128 codes q[rows][cols] + scales s[ceil(cols/128)][rows], rows grouped, as grouped_quantize_act()
+    gives them; see fp8q_grouped_requant_transpose."""
+    _check_codes("grouped_requant_transpose codes", q)
+    G = _check_offsets("grouped_requant_transpose", offsets)
+    rows, cols = q.shape
+    _check_scales("grouped_requant_transpose scales (layout [ceil(cols/128)][rows])", s, _cdiv(cols, 128), rows)
+    _on_current_device("grouped_requant_transpose", q, s, offsets)
+    o = _grouped_operand(rows, cols, G, q.device)
+    _check(_lib.fp8q_grouped_requant_transpose(q.data_ptr(), rows, cols, _ld(q), s.data_ptr(),
+                                               s.stride(0) if s.shape[0] > 1 else max(rows, 1), offsets.data_ptr(), G,
+                                               o.q.data_ptr(), o.q.shape[1], o.s.data_ptr(), cols, scale_mode,
+                                               _stream()),
+           "fp8q_grouped_requant_transpose")
+    return o
+
+
+def grouped_wgrad(dy: GroupedOperand, x: GroupedOperand, offsets: torch.Tensor,
+                  out_dtype: torch.dtype = torch.float32, dw: Optional[torch.Tensor] = None, accumulate: bool = False,
+                  flags: int = 0) -> torch.Tensor:
+    """Weight gradients dW [G][N][K] of all groups from dy (N channels) and x (K channels); with `accumulate` added
+    to the given fp32 dw.  See fp8q_grouped_wgrad."""
+    G = _check_offsets("grouped_wgrad", offsets)
+    (qa, sa, rows), (qb, sb, rows_x) = dy, x
+    if rows != rows_x:
+        raise ValueError(f"grouped_wgrad: operands of {rows} and {rows_x} rows")
+    N, K = qa.shape[0], qb.shape[0]
+    padded = _lib.fp8q_grouped_padded_rows(rows, G)
+    for name, q, s in (("dy", qa, sa), ("x", qb, sb)):
+        _check_codes(f"grouped_wgrad {name}", q)
+        if q.shape[1] < padded:
+            raise ValueError(f"grouped_wgrad: {name} has {q.shape[1]} tokens, {G} groups of {rows} rows take up to {padded}")
+        _check_scales(f"grouped_wgrad {name} (layout [chunks][channels])", s, padded // 128, q.shape[0])
+    if accumulate and dw is None:
+        raise ValueError("grouped_wgrad: accumulate needs the gradient to add to")
+    if dw is None:
+        dw = torch.empty((G, N, K), dtype=out_dtype, device=qa.device)
+    elif dw.shape != (G, N, K) or (K > 1 and dw.stride(2) != 1):
+        raise ValueError(f"grouped_wgrad: dw is {tuple(dw.shape)}, expected [{G}][{N}][{K}] with unit inner stride")
+    _on_current_device("grouped_wgrad", qa, sa, qb, sb, offsets, dw)
+    lddw = dw.stride(1) if N > 1 else max(K, 1)  # axes of one element may carry any stride
+    need = _lib.fp8q_grouped_wgrad_workspace(rows, G, N, K)
+    ws, base = _workspace(need, qa.device)
+    _check(_lib.fp8q_grouped_wgrad(qa.data_ptr(), _ld(qa) if N > 1 else max(qa.shape[1], 16), sa.data_ptr(),
+                                   sa.stride(0) if sa.shape[0] > 1 else max(N, 1), qb.data_ptr(),
+                                   _ld(qb) if K > 1 else max(qb.shape[1], 16), sb.data_ptr(),
+                                   sb.stride(0) if sb.shape[0] > 1 else max(K, 1), offsets.data_ptr(), G, rows, N, K,
+                                   dw.data_ptr(), _dtype_code(dw), lddw, dw.stride(0) if G > 1 else N * lddw,
+                                   1 if accumulate else 0, flags, base, need, _stream()),
+           "fp8q_grouped_wgrad")
+    return dw
+
+
+class AdamwState(NamedTuple):
+    """Moments of one tensor of n elements: m and v fp32 [n], or codes [n] of m and sqrt(v) with scales sm and sv
+    [ceil(n/128)]."""
+    m: torch.Tensor
+    v: torch.Tensor
+    sm: Optional[torch.Tensor]
+    sv: Optional[torch.Tensor]
+
+
+def adamw_state(p: torch.Tensor, bits: int = 32) -> AdamwState:
+    """The moments of p before its first step."""
+    if bits not in (8, 32):
+        raise ValueError(f"adamw_state: moments of {bits} bits; there are 8 and 32")
+    n = p.numel()
+    if bits == 32:
+        return AdamwState(*(torch.zeros(n, dtype=torch.float32, device=p.device) for _ in range(2)), None, None)
+    return AdamwState(*(torch.zeros(n, dtype=torch.uint8, device=p.device) for _ in range(2)),
+                      *(torch.zeros(_cdiv(n, 128), dtype=torch.float32, device=p.device) for _ in range(2)))
+
+
+class WeightCodes(NamedTuple):
+    """FP8 codes of weights [N][K] or [G][N][K] and of their transposes: q and s as quantize_weight() gives them for
+    each matrix, qt [..][K][N] (row stride a multiple of 16) and st as transpose_weight() does, or None."""
+    q: torch.Tensor
+    s: torch.Tensor
+    qt: Optional[torch.Tensor]
+    st: Optional[torch.Tensor]
+
+
+def weight_codes(w: torch.Tensor, transposed: bool = True, scale_mode: int = FP8Q_SCALE_FP32) -> WeightCodes:
+    """The codes of weights w ([N][K] or [G][N][K], K a multiple of 128) that adamw() keeps up to date."""
+    if w.dim() not in (2, 3) or w.shape[-1] % 128 != 0 or not w.is_contiguous():
+        raise ValueError(f"weight_codes: weights {tuple(w.shape)}, expected dense [N][K] or [G][N][K] with K a multiple of 128")
+    _on_current_device("weight_codes", w)
+    lead, (N, K), dev = w.shape[:-2], w.shape[-2:], w.device
+    nb, kb, n16 = _cdiv(N, 128), K // 128, _pad16(N)
+    o = WeightCodes(torch.empty((*lead, N, K), dtype=torch.uint8, device=dev),
+                    torch.empty((*lead, nb, kb), dtype=torch.float32, device=dev),
+                    torch.empty((*lead, K, n16), dtype=torch.uint8, device=dev)[..., :N] if transposed else None,
+                    torch.empty((*lead, kb, nb), dtype=torch.float32, device=dev) if transposed else None)
+    for g in range(w.shape[0]) if w.dim() == 3 else [...]:
+        _check(fp8q_quantize_weight_ex(w[g].data_ptr(), _dtype_code(w), N, K, max(K, 8), o.q[g].data_ptr(), max(K, 16),
+                                       o.s[g].data_ptr(), max(kb, 1), scale_mode, _stream()), "fp8q_quantize_weight_ex")
+        if transposed:
+            _check(fp8q_transpose_weight(o.q[g].data_ptr(), N, K, max(K, 16), o.s[g].data_ptr(), max(kb, 1),
+                                         o.qt[g].data_ptr(), max(n16, 16), o.st[g].data_ptr(), max(nb, 1), _stream()),
+                   "fp8q_transpose_weight")
+    return o
+
+
+class AdamwTensors:
+    """What adamw() works on: made by adamw_tensors(), kept from step to step.  It holds the tensors."""
+
+    def __init__(self, held: tuple, array, g_dtype: int, bits: int, device: torch.device):
+        self.held, self.array, self.g_dtype, self.bits, self.device = held, array, g_dtype, bits, device
+
+
+def _dense_span(what: str, name: str, t: torch.Tensor, shape: Optional[tuple], dtype: Optional[torch.dtype]) -> None:
+    if (shape is not None and tuple(t.shape) != tuple(shape)) or (dtype is not None and t.dtype != dtype) or \
+            not t.is_contiguous():
+        raise ValueError(f"{what}: {name} is {tuple(t.shape)} {t.dtype} with strides {t.stride()}, expected dense "
+                         f"{'' if shape is None else tuple(shape)} {'' if dtype is None else dtype}")
+
+
+def adamw_tensors(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], states: Sequence[AdamwState],
+                  codes: Optional[Sequence[Optional[WeightCodes]]] = None) -> AdamwTensors:
+    """Checks the tensors of an optimizer step once: dense fp32 params, grads of the same shapes (all fp32 or all
+    bf16), moments of adamw_state() (all of 32 or all of 8 bits), and for weights the codes of weight_codes() or None.
+    adamw() then updates params, moments and codes in place, from what grads hold at that time."""
+    what = "adamw_tensors"
+    codes = [None] * len(params) if codes is None else list(codes)
+    if not len(params) == len(grads) == len(states) == len(codes):
+        raise ValueError(f"{what}: {len(params)} params, {len(grads)} grads, {len(states)} states, {len(codes)} codes")
+    if not params:
+        raise ValueError(f"{what}: no tensors")
+    bits = 8 if states[0].m.dtype == torch.uint8 else 32
+    array = (fp8q_adamw_tensor * len(params))()
+    written, read = [], []
+    for i, (p, g, state, c) in enumerate(zip(params, grads, states, codes)):
+        at, n = f"{what}: tensor {i}", p.numel()
+        _dense_span(at, "the parameter", p, None, torch.float32)
+        _dense_span(at, "the gradient", g, p.shape, grads[0].dtype)
+        kind = torch.uint8 if bits == 8 else torch.float32
+        _dense_span(at, "m", state.m, (n,), kind)
+        _dense_span(at, "v", state.v, (n,), kind)
+        out = [p, state.m, state.v]
+        if bits == 8:
+            for name, t in (("sm", state.sm), ("sv", state.sv)):
+                if t is None:
+                    raise ValueError(f"{at}: 8-bit moments need scales")
+                _dense_span(at, name, t, (_cdiv(n, 128),), torch.float32)
+                out.append(t)
+        elif state.sm is not None or state.sv is not None:
+            raise ValueError(f"{at}: fp32 moments have no scales")
+        d = array[i]
+        d.n, d.p, d.g, d.m, d.v, d.sm, d.sv = (n, p.data_ptr(), g.data_ptr(), state.m.data_ptr(), state.v.data_ptr(),
+                                               _ptr(state.sm), _ptr(state.sv))
+        if c is not None and n:
+            if p.dim() not in (2, 3) or p.shape[-1] % 128 != 0:
+                raise ValueError(f"{at}: codes are kept of [N][K] or [G][N][K] with K a multiple of 128, not {tuple(p.shape)}")
+            lead, (N, K) = p.shape[:-2], p.shape[-2:]
+            nb, kb, n16 = _cdiv(N, 128), K // 128, _pad16(N)
+            _dense_span(at, "q", c.q, p.shape, torch.uint8)
+            _dense_span(at, "s", c.s, (*lead, nb, kb), torch.float32)
+            out += [c.q, c.s]
+            if (c.qt is None) != (c.st is None):
+                raise ValueError(f"{at}: qt and st go together")
+            if c.qt is not None:
+                _dense_span(at, "st", c.st, (*lead, kb, nb), torch.float32)
+                if tuple(c.qt.shape) != (*lead, K, N) or c.qt.dtype != torch.uint8 or \
+                        (N > 1 and c.qt.stride(-1) != 1) or c.qt.stride(-2) != n16 or \
+                        (lead and lead[0] > 1 and c.qt.stride(0) != K * n16):
+                    raise ValueError(f"{at}: qt is {tuple(c.qt.shape)} {c.qt.dtype} with strides {c.qt.stride()}, expected "
+                                     f"that of weight_codes()")
+                out += [c.qt, c.st]
+            d.N, d.K, d.q, d.s, d.qt, d.st = N, K, c.q.data_ptr(), c.s.data_ptr(), _ptr(c.qt), _ptr(c.st)
+        _on_current_device(at, g, *out)
+        read.append(g)
+        written += out
+    _no_overlap(what, written, read)
+    return AdamwTensors((tuple(params), tuple(grads), tuple(states), tuple(codes)), array, _dtype_code(grads[0]), bits,
+                        params[0].device)
+
+
+def _no_overlap(what: str, written: list, read: list) -> None:
+    """No byte that is written belongs to two of the tensors (gradients may share)."""
+    spans = []
+    for t, w in [(t, True) for t in written] + [(t, False) for t in read]:
+        if t.numel():
+            last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+            spans.append((t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size(), w))
+    spans.sort()
+    end, end_w = 0, 0  # ends of what was met so far, and of what is written of it
+    for lo, hi, w in spans:
+        if lo < end_w or (w and lo < end):
+            raise ValueError(f"{what}: tensors overlap (each may be in the list once)")
+        end = max(end, hi)
+        end_w = max(end_w, hi) if w else end_w
+
+
+def adamw(tensors: AdamwTensors, step: Union[int, torch.Tensor], lr: Union[float, torch.Tensor], beta1: float = 0.9,
+          beta2: float = 0.95, eps: float = 1e-8, weight_decay: float = 0.1,
+          grad_scale: Optional[torch.Tensor] = None, seed: int = 0, scale_mode: int = FP8Q_SCALE_FP32) -> None:
+    """One AdamW step over all the tensors, in place; step counts from 1.  step (int64), lr and grad_scale (fp32) may
+    be tensors of one element on the device, read when the step runs: a captured step is then replayed with other
+    values.  grad_scale multiplies the gradients; seed chooses the random numbers that round 8-bit moments.  See
+    fp8q_adamw."""
+    c = fp8q_adamw_config(0.0, beta1, beta2, eps, weight_decay, 0, None, None, None, seed & 0xFFFFFFFF)
+    given = []
+    if isinstance(step, torch.Tensor):
+        _device_scalar("step", step, torch.int64)
+        c.step_dev = step.data_ptr()
+        given.append(step)
+    else:
+        c.step = step
+    if isinstance(lr, torch.Tensor):
+        _device_scalar("lr", lr, torch.float32)
+        c.lr_dev = lr.data_ptr()
+        given.append(lr)
+    else:
+        c.lr = lr
+    if grad_scale is not None:
+        _device_scalar("grad_scale", grad_scale, torch.float32)
+        c.grad_scale = grad_scale.data_ptr()
+        given.append(grad_scale)
+    if given:
+        _on_device("adamw", *given)
+    if tensors.device.index != torch.cuda.current_device() or any(t.device != tensors.device for t in given):
+        raise ValueError(f"adamw: tensors on {tensors.device}, the current device is cuda:{torch.cuda.current_device()}")
+    _check(_lib.fp8q_adamw(tensors.array, len(tensors.array), tensors.g_dtype, tensors.bits, ctypes.addressof(c),
+                           scale_mode, _stream()), "fp8q_adamw")
+
+
+def _device_scalar(name: str, t: torch.Tensor, dtype: torch.dtype) -> None:
+    if t.numel() != 1 or t.dtype != dtype:
+        raise ValueError(f"adamw: {name} must be one {dtype} on the device, got {tuple(t.shape)} {t.dtype}")

@@ -143,7 +143,7 @@ const char* fp8q_strerror(int status) {
     }
 }
 
-int fp8q_version(void) { return 300; }
+int fp8q_version(void) { return 400; }
 
 int fp8q_quantize_act(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, int tile,
                       uint8_t* q, int64_t ldq, float* s, int64_t lds, void* stream) {
@@ -383,6 +383,66 @@ int fp8q_moe_decode(const void* x, int64_t ldx, int64_t tokens, int64_t hidden, 
     a.s_down = s_down; a.lds_down = lds_down; a.s_down_stride = s_down_stride;
     a.y = y; a.y_dtype = y_dtype; a.ldy = ldy; a.workspace = workspace;
     return status_of(fp8q::launch_moe_decode(a, static_cast<hipStream_t>(stream)));
+}
+
+int64_t fp8q_grouped_padded_rows(int64_t rows, int G) {
+    return rows < 0 || G < 0 || rows > INT32_MAX ? 0 : fp8q::check::padded_rows(rows, G);
+}
+
+int fp8q_grouped_quantize_act(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx,
+                              const int32_t* group_offsets, int G, uint8_t* qt, int64_t ldqt, float* st, int64_t ldst,
+                              int scale_mode, void* stream) {
+    const int rc = fp8q::check::grouped_quantize_act(x, x_dtype, rows, cols, ldx, group_offsets, G, qt, ldqt, st, ldst,
+                                                     scale_mode);
+    if (rc != kLaunch) return rc;
+    return status_of(fp8q::launch_grouped_quantize_128x1(x, x_dtype == FP8Q_BF16 ? 1 : 0, rows, cols, ldx, nullptr, 0,
+                                                         group_offsets, G, qt, ldqt, st, ldst,
+                                                         scale_mode == FP8Q_SCALE_POW2,
+                                                         static_cast<hipStream_t>(stream)));
+}
+
+int fp8q_grouped_requant_transpose(const uint8_t* q, int64_t rows, int64_t cols, int64_t ldq, const float* s,
+                                   int64_t lds, const int32_t* group_offsets, int G, uint8_t* qt, int64_t ldqt,
+                                   float* st, int64_t ldst, int scale_mode, void* stream) {
+    const int rc = fp8q::check::grouped_requant(q, rows, cols, ldq, s, lds, group_offsets, G, qt, ldqt, st, ldst,
+                                                scale_mode);
+    if (rc != kLaunch) return rc;
+    return status_of(fp8q::launch_grouped_quantize_128x1(q, 2, rows, cols, ldq, s, lds, group_offsets, G, qt, ldqt, st,
+                                                         ldst, scale_mode == FP8Q_SCALE_POW2,
+                                                         static_cast<hipStream_t>(stream)));
+}
+
+int64_t fp8q_grouped_wgrad_workspace(int64_t rows, int G, int64_t N, int64_t K) {
+    if (fp8q::check::wgrad_sizes(rows, G, N, K) != kLaunch || rows == 0 || N == 0 || K == 0) return 0;
+    return fp8q::grouped_wgrad_bytes(rows, G, N, K);
+}
+
+int fp8q_grouped_wgrad(const uint8_t* a, int64_t lda, const float* sa, int64_t ldsa, const uint8_t* b, int64_t ldb,
+                       const float* sb, int64_t ldsb, const int32_t* group_offsets, int G, int64_t rows, int64_t N,
+                       int64_t K, void* dw, int dw_dtype, int64_t lddw, int64_t dw_group_stride, int accumulate,
+                       unsigned flags, void* workspace, int64_t workspace_bytes, void* stream) {
+    const int rc = fp8q::check::grouped_wgrad(a, lda, sa, ldsa, b, ldb, sb, ldsb, group_offsets, G, rows, N, K, dw,
+                                              dw_dtype, lddw, dw_group_stride, accumulate, flags,
+                                              fp8q_grouped_wgrad_workspace(rows, G, N, K), workspace,
+                                              workspace_bytes);
+    if (rc != kLaunch) return rc;
+    fp8q::GemmArgs g{};
+    g.a = a; g.lda = lda; g.sa = sa; g.ldsa = ldsa;
+    g.b = b; g.ldb = ldb; g.sb = sb; g.ldsb = ldsb;
+    g.offsets = group_offsets; g.groups = G;
+    g.M = N; g.N = K; g.K = rows; g.c = dw; g.ldc = lddw;
+    g.bscale = FP8Q_BSCALE_ROW; g.c_dtype = dw_dtype; g.accumulate = accumulate ? 1 : 0;
+    g.mma = datapath_of(flags);
+    g.workspace = workspace; g.workspace_bytes = workspace_bytes;
+    return status_of(fp8q::launch_grouped_wgrad(g, dw_group_stride, static_cast<hipStream_t>(stream)));
+}
+
+int fp8q_adamw(const fp8q_adamw_tensor* tensors, int count, int g_dtype, int bits, const fp8q_adamw_config* config,
+               int scale_mode, void* stream) {
+    const int rc = fp8q::check::adamw(tensors, count, g_dtype, bits, config, scale_mode);
+    if (rc != kLaunch) return rc;
+    return status_of(fp8q::launch_adamw(tensors, count, g_dtype, bits, *config, scale_mode == FP8Q_SCALE_POW2,
+                                        static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

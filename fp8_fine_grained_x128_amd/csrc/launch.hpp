@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "../../include/fp8q.h"
+
 namespace fp8q {
 
 constexpr int kDtypeF32 = 0;   // FP8Q_F32
@@ -26,6 +28,12 @@ hipError_t launch_quantize_128x128(const void* w, int dtype, int64_t N, int64_t 
 hipError_t launch_quantize_128x1(const void* x, int kind, int64_t rows, int64_t cols, int64_t ldx,
                                  const float* s_in, int64_t lds_in, uint8_t* qt, int64_t ldqt,
                                  float* st_out, int64_t ldst, int pow2, hipStream_t st);
+
+// The same per group of rows (groups.hpp).
+hipError_t launch_grouped_quantize_128x1(const void* x, int kind, int64_t rows, int64_t cols, int64_t ldx,
+                                         const float* s_in, int64_t lds_in, const int32_t* offsets, int groups,
+                                         uint8_t* qt, int64_t ldqt, float* st_out, int64_t ldst, int pow2,
+                                         hipStream_t st);
 
 hipError_t launch_transpose_weight(const uint8_t* q, int64_t N, int64_t K, int64_t ldq, const float* s,
                                    int64_t lds, uint8_t* qt, int64_t ldqt, float* st, int64_t ldst,
@@ -77,6 +85,14 @@ struct SplitPlan {
 };
 SplitPlan plan_splitk(int64_t M, int64_t N, int64_t K);
 hipError_t launch_grouped_gemm(const GemmArgs& g, hipStream_t st);
+
+// Weight gradients per group: A [M][padded rows], B [N][padded rows], K = rows
+// of all groups, C [groups][M][N]; bytes of the workspace they take.
+int64_t grouped_wgrad_bytes(int64_t rows, int groups, int64_t M, int64_t N);
+hipError_t launch_grouped_wgrad(const GemmArgs& g, int64_t c_group_stride, hipStream_t st);
+
+hipError_t launch_adamw(const fp8q_adamw_tensor* tensors, int count, int g_dtype, int bits,
+                        const fp8q_adamw_config& c, int pow2, hipStream_t st);
 
 // ---- feed-forward operators around the GEMMs
 

@@ -22,6 +22,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "groups.hpp"
 #include "launch.hpp"
 #include "tile_io.hpp"
 
@@ -221,11 +222,16 @@ enum SrcKind { SRC_F32 = 0, SRC_BF16 = 1, SRC_FP8 = 2 };
 
 __device__ __forceinline__ int swz_unit(int ch, int unit) { return unit ^ ((ch >> 3) & 7); }
 
-template <int KIND, bool POW2>
+// GROUPED (groups.hpp): tile row blockIdx.y is a 128-token chunk of one group,
+// whose rows begin anywhere; its codes fill a whole chunk, zeros past the
+// group's last row (0 / s: the quantizer's code of a zero is a zero).  Every
+// wave finds the chunk's rows by itself, from 16 or fewer offsets a lane.
+template <int KIND, bool POW2, bool GROUPED>
 __global__ __launch_bounds__(512) void quantize_128x1_kernel(
     const void* __restrict__ src, int64_t rows, int64_t cols, int64_t ldx,
     const float* __restrict__ s_in, int64_t lds_in,
-    uint8_t* __restrict__ qt, int64_t ldqt, float* __restrict__ st, int64_t ldst) {
+    uint8_t* __restrict__ qt, int64_t ldqt, float* __restrict__ st, int64_t ldst,
+    const int32_t* __restrict__ offsets, int groups) {
     constexpr int kThreads = 512;
     constexpr int kWaves = kThreads / 64;
     constexpr int kCh = 8;                              // channels per thread
@@ -239,7 +245,15 @@ __global__ __launch_bounds__(512) void quantize_128x1_kernel(
     const int t = threadIdx.x;
     const int lane = t & 63, wave = t >> 6;
     const int cg = t % kChGroups, rg = t / kChGroups;
-    const int64_t r0 = (int64_t)blockIdx.y * 128, c0 = (int64_t)blockIdx.x * 128;
+    const int64_t c0 = (int64_t)blockIdx.x * 128;
+    int64_t r0 = (int64_t)blockIdx.y * 128;
+    if constexpr (GROUPED) {
+        const GroupChunk ck = find_chunk(offsets, groups, (int)rows, (int)blockIdx.y);
+        if (!ck.live) return;
+        r0 = ck.row0;
+        rows = ck.row_end;
+    }
+    const int64_t out0 = (int64_t)blockIdx.y * 128;  // first token of the output tile
     const int64_t cbase = c0 + kCh * cg;
     const bool full = r0 + 128 <= rows && c0 + 128 <= cols;
 
@@ -359,7 +373,7 @@ __global__ __launch_bounds__(512) void quantize_128x1_kernel(
         for (int wv = 0; wv < kWaves; ++wv) mm = max(mm, s_part[wv][t]);
         const TileScale ts = make_scale_mode<POW2>(mm);
         s_sr[t] = make_float2(ts.s, ts.r);
-        if (c0 + t < cols) st[(r0 >> 7) * ldst + c0 + t] = ts.s;
+        if (c0 + t < cols) st[(int64_t)blockIdx.y * ldst + c0 + t] = ts.s;
     }
     __syncthreads();
     // quantize and write codes transposed into the LDS tile (values decoded
@@ -403,13 +417,17 @@ __global__ __launch_bounds__(512) void quantize_128x1_kernel(
         const uint4 val = *reinterpret_cast<const uint4*>(s_tile + ch * 128 + 16 * unit);
         const int lunit = swz_unit(ch, unit);  // logical token unit held here
         const int64_t c = c0 + ch;
-        const int64_t tok = r0 + 16 * lunit;
+        const int64_t tok = out0 + 16 * lunit;
         uint8_t* dst = qt + c * ldqt + tok;
         if (full) {
             *reinterpret_cast<uint4*>(dst) = val;
             continue;
         }
         if (c >= cols) continue;
+        if constexpr (GROUPED) {  // whole chunks
+            *reinterpret_cast<uint4*>(dst) = val;
+            continue;
+        }
         if (tok + 16 <= rows) {
             *reinterpret_cast<uint4*>(dst) = val;
         } else {
@@ -464,19 +482,21 @@ void launch_128x128(const void* w, int dtype, int64_t N, int64_t K, int64_t ldw,
                            static_cast<const float*>(w), N, K, ldw, q, ldq, s, lds);
 }
 
-template <bool POW2>
+template <bool POW2, bool GROUPED>
 void launch_128x1(const void* x, int kind, int64_t rows, int64_t cols, int64_t ldx, const float* s_in,
-                  int64_t lds_in, uint8_t* qt, int64_t ldqt, float* st_out, int64_t ldst, hipStream_t st) {
-    dim3 grid((unsigned)((cols + 127) / 128), (unsigned)((rows + 127) / 128));
+                  int64_t lds_in, uint8_t* qt, int64_t ldqt, float* st_out, int64_t ldst, const int32_t* offsets,
+                  int groups, hipStream_t st) {
+    const int64_t chunks = GROUPED ? group_chunks(rows, groups) : (rows + 127) / 128;
+    dim3 grid((unsigned)((cols + 127) / 128), (unsigned)chunks);
     if (kind == SRC_BF16)
-        hipLaunchKernelGGL((quantize_128x1_kernel<SRC_BF16, POW2>), grid, dim3(512), 0, st, x, rows, cols,
-                           ldx, s_in, lds_in, qt, ldqt, st_out, ldst);
+        hipLaunchKernelGGL((quantize_128x1_kernel<SRC_BF16, POW2, GROUPED>), grid, dim3(512), 0, st, x, rows, cols,
+                           ldx, s_in, lds_in, qt, ldqt, st_out, ldst, offsets, groups);
     else if (kind == SRC_F32)
-        hipLaunchKernelGGL((quantize_128x1_kernel<SRC_F32, POW2>), grid, dim3(512), 0, st, x, rows, cols,
-                           ldx, s_in, lds_in, qt, ldqt, st_out, ldst);
+        hipLaunchKernelGGL((quantize_128x1_kernel<SRC_F32, POW2, GROUPED>), grid, dim3(512), 0, st, x, rows, cols,
+                           ldx, s_in, lds_in, qt, ldqt, st_out, ldst, offsets, groups);
     else
-        hipLaunchKernelGGL((quantize_128x1_kernel<SRC_FP8, POW2>), grid, dim3(512), 0, st, x, rows, cols,
-                           ldx, s_in, lds_in, qt, ldqt, st_out, ldst);
+        hipLaunchKernelGGL((quantize_128x1_kernel<SRC_FP8, POW2, GROUPED>), grid, dim3(512), 0, st, x, rows, cols,
+                           ldx, s_in, lds_in, qt, ldqt, st_out, ldst, offsets, groups);
 }
 
 }  // namespace
@@ -508,8 +528,21 @@ hipError_t launch_quantize_128x128(const void* w, int dtype, int64_t N, int64_t 
 hipError_t launch_quantize_128x1(const void* x, int kind, int64_t rows, int64_t cols, int64_t ldx,
                                  const float* s_in, int64_t lds_in, uint8_t* qt, int64_t ldqt,
                                  float* st_out, int64_t ldst, int pow2, hipStream_t st) {
-    if (pow2) launch_128x1<true>(x, kind, rows, cols, ldx, s_in, lds_in, qt, ldqt, st_out, ldst, st);
-    else launch_128x1<false>(x, kind, rows, cols, ldx, s_in, lds_in, qt, ldqt, st_out, ldst, st);
+    if (pow2)
+        launch_128x1<true, false>(x, kind, rows, cols, ldx, s_in, lds_in, qt, ldqt, st_out, ldst, nullptr, 0, st);
+    else
+        launch_128x1<false, false>(x, kind, rows, cols, ldx, s_in, lds_in, qt, ldqt, st_out, ldst, nullptr, 0, st);
+    return hipGetLastError();
+}
+
+hipError_t launch_grouped_quantize_128x1(const void* x, int kind, int64_t rows, int64_t cols, int64_t ldx,
+                                         const float* s_in, int64_t lds_in, const int32_t* offsets, int groups,
+                                         uint8_t* qt, int64_t ldqt, float* st_out, int64_t ldst, int pow2,
+                                         hipStream_t st) {
+    if (pow2)
+        launch_128x1<true, true>(x, kind, rows, cols, ldx, s_in, lds_in, qt, ldqt, st_out, ldst, offsets, groups, st);
+    else
+        launch_128x1<false, true>(x, kind, rows, cols, ldx, s_in, lds_in, qt, ldqt, st_out, ldst, offsets, groups, st);
     return hipGetLastError();
 }
 

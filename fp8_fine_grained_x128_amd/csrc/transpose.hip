@@ -15,32 +15,14 @@
 // row's block index (conflict-free stores); 16 threads then read each output
 // row's 16 slots and write 128 contiguous bytes.  Edge tiles copy byte by
 // byte.  The block scale is moved by thread 0.
-#include "device_common.hpp"
 #include "launch.hpp"
+#include "tile_io.hpp"
 
 namespace fp8q {
 
 // The weight codes are read once (non-temporal loads below); the transposed
 // copy is what the Dgrad GEMM reads next.
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-
-// v_perm_b32: byte i of the result is byte sel[i] of the 8-byte value hi:lo.
-__device__ __forceinline__ uint32_t perm(uint32_t hi, uint32_t lo, uint32_t sel) {
-    return __builtin_amdgcn_perm(hi, lo, sel);
-}
-
-// Transpose of a 4x4 byte matrix held as 4 dwords (dword r = row r, byte c =
-// column c): out[c] = column c.
-__device__ __forceinline__ void transpose4x4(const uint32_t a[4], uint32_t out[4]) {
-    const uint32_t x0 = perm(a[1], a[0], 0x06020400u);  // a0.0 a1.0 a0.2 a1.2
-    const uint32_t x1 = perm(a[1], a[0], 0x07030501u);  // a0.1 a1.1 a0.3 a1.3
-    const uint32_t x2 = perm(a[3], a[2], 0x06020400u);
-    const uint32_t x3 = perm(a[3], a[2], 0x07030501u);
-    out[0] = perm(x2, x0, 0x05040100u);
-    out[1] = perm(x3, x1, 0x05040100u);
-    out[2] = perm(x2, x0, 0x07060302u);
-    out[3] = perm(x3, x1, 0x07060302u);
-}
 
 __global__ __launch_bounds__(256) void transpose_weight_kernel(
     const uint8_t* __restrict__ q, int64_t N, int64_t K, int64_t ldq, const float* __restrict__ s, int64_t lds,

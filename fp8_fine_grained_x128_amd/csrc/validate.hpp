@@ -360,5 +360,122 @@ inline int moe_decode(const void* x, int64_t ldx, int64_t tokens, int64_t hidden
     return kLaunch;
 }
 
+// ---- weight gradients of groups of rows, AdamW
+
+// Columns of the padded layout (groups.hpp): chunks of all groups at most.
+inline int64_t padded_rows(int64_t rows, int64_t G) { return (rows + 127 * (G < rows ? G : rows)) / 128 * 128; }
+
+inline int groups(int64_t rows, int64_t cols, const void* group_offsets, int G, const void* qt, int64_t ldqt,
+                  const void* st, int64_t ldst, int scale_mode) {
+    if (!valid_scale_mode(scale_mode)) return FP8Q_EINVAL;
+    if (G < 1 || G > kMaxGroups || rows < 0 || cols < 0 || !ld_ok(ldqt) || !ld_ok(ldst)) return FP8Q_ESHAPE;
+    if (rows > INT32_MAX) return FP8Q_EUNSUPPORTED;
+    if (ldqt < padded_rows(rows, G) || ldst < cols) return FP8Q_ESHAPE;
+    if (rows == 0 || cols == 0) return FP8Q_OK;
+    if (!group_offsets || !qt || !st) return FP8Q_EINVAL;
+    if (!aligned(group_offsets, 4) || !aligned(qt, 16) || ldqt % 16 != 0 || !aligned(st, 4)) return FP8Q_EALIGN;
+    if (padded_rows(rows, G) / 128 > kMaxGridY) return FP8Q_EUNSUPPORTED;
+    return kLaunch;
+}
+
+inline int grouped_quantize_act(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx,
+                                const void* group_offsets, int G, const void* qt, int64_t ldqt, const void* st,
+                                int64_t ldst, int scale_mode) {
+    if (!valid_dtype(x_dtype)) return FP8Q_EINVAL;
+    if (!ld_ok(ldx) || ldx < cols) return FP8Q_ESHAPE;
+    const int rc = groups(rows, cols, group_offsets, G, qt, ldqt, st, ldst, scale_mode);
+    if (rc != kLaunch) return rc;
+    if (!x) return FP8Q_EINVAL;
+    return row_aligned(x, ldx, x_dtype) ? kLaunch : FP8Q_EALIGN;
+}
+
+inline int grouped_requant(const void* q, int64_t rows, int64_t cols, int64_t ldq, const void* s, int64_t lds,
+                           const void* group_offsets, int G, const void* qt, int64_t ldqt, const void* st,
+                           int64_t ldst, int scale_mode) {
+    if (!ld_ok(ldq) || !ld_ok(lds) || ldq < cols || lds < rows) return FP8Q_ESHAPE;
+    const int rc = groups(rows, cols, group_offsets, G, qt, ldqt, st, ldst, scale_mode);
+    if (rc != kLaunch) return rc;
+    if (!q || !s) return FP8Q_EINVAL;
+    return aligned(q, 16) && ldq % 16 == 0 && aligned(s, 4) ? kLaunch : FP8Q_EALIGN;
+}
+
+// Sizes of the weight gradients: FP8Q_ESHAPE or FP8Q_EUNSUPPORTED where there
+// are none.
+inline int wgrad_sizes(int64_t rows, int G, int64_t N, int64_t K) {
+    if (G < 1 || G > kMaxGroups || rows < 0 || N < 0 || K < 0) return FP8Q_ESHAPE;
+    if (N > kMaxLd || K > kMaxLd || rows > INT32_MAX || padded_rows(rows, G) > kMaxOperandLd) return FP8Q_EUNSUPPORTED;
+    return kLaunch;
+}
+
+// `need`: the bytes that the split of this shape takes.  rows == 0 launches:
+// the gradients are set to zero.
+inline int grouped_wgrad(const void* a, int64_t lda, const void* sa, int64_t ldsa, const void* b, int64_t ldb,
+                         const void* sb, int64_t ldsb, const void* group_offsets, int G, int64_t rows, int64_t N,
+                         int64_t K, const void* dw, int dw_dtype, int64_t lddw, int64_t dw_group_stride,
+                         int accumulate, unsigned flags, int64_t need, const void* workspace,
+                         int64_t workspace_bytes) {
+    if (!valid_dtype(dw_dtype) || (flags & ~kKnownGemmFlags) != 0u) return FP8Q_EINVAL;
+    if (accumulate && dw_dtype != FP8Q_F32) return FP8Q_EUNSUPPORTED;
+    if (!ld_ok(lda) || !ld_ok(ldb) || !ld_ok(ldsa) || !ld_ok(ldsb) || !ld_ok(lddw) || dw_group_stride < 0 ||
+        dw_group_stride > kMaxGroupStride || workspace_bytes < 0)
+        return FP8Q_ESHAPE;
+    const int rc = wgrad_sizes(rows, G, N, K);
+    if (rc != kLaunch) return rc;
+    if (lda < padded_rows(rows, G) || ldb < padded_rows(rows, G) || ldsa < N || ldsb < K || lddw < K)
+        return FP8Q_ESHAPE;
+    if (lda > kMaxOperandLd || ldb > kMaxOperandLd) return FP8Q_EUNSUPPORTED;
+    if (N == 0 || K == 0) return FP8Q_OK;
+    // N, lddw <= 2^32: the product may pass 2^63 only where a factor is over 2^31
+    if (N > (int64_t(1) << 31) || lddw > (int64_t(1) << 31)) return FP8Q_EUNSUPPORTED;
+    if (G > 1 && dw_group_stride < (N - 1) * lddw + K) return FP8Q_ESHAPE;
+    if (!dw) return FP8Q_EINVAL;
+    if (!aligned(dw, (uintptr_t)elem_bytes(dw_dtype))) return FP8Q_EALIGN;
+    if (rows == 0) return accumulate ? FP8Q_OK : kLaunch;
+    if (!a || !sa || !b || !sb || !group_offsets) return FP8Q_EINVAL;
+    if (!aligned(a, 16) || lda % 16 != 0 || !aligned(b, 16) || ldb % 16 != 0 || !aligned(sa, 4) || !aligned(sb, 4) ||
+        !aligned(group_offsets, 4))
+        return FP8Q_EALIGN;
+    return splitk_workspace(need, workspace, workspace_bytes);
+}
+
+constexpr int64_t kMaxAdamwElements = int64_t(1) << 33;
+constexpr int64_t kMaxAdamwBlocks = int64_t(1) << 22;
+
+inline int adamw_tensor(const fp8q_adamw_tensor& t, int bits) {
+    if (t.n < 0) return FP8Q_ESHAPE;
+    if (t.n == 0) return FP8Q_OK;
+    if (!t.p || !t.g || !t.m || !t.v || (bits == 8 && (!t.sm || !t.sv))) return FP8Q_EINVAL;
+    if (!t.q != !t.s || !t.qt != !t.st || (t.qt && !t.q)) return FP8Q_EINVAL;
+    if (!aligned(t.p, 16) || !aligned(t.g, 16) || !aligned(t.m, 16) || !aligned(t.v, 16) ||
+        (bits == 8 && (!aligned(t.sm, 4) || !aligned(t.sv, 4))))
+        return FP8Q_EALIGN;
+    if (t.n > kMaxAdamwElements) return FP8Q_EUNSUPPORTED;
+    if (!t.q) return kLaunch;
+    if (t.N < 1 || t.K < 1 || t.K % 128 != 0 || t.N > t.n || t.K > t.n || t.n % t.N != 0 || t.n / t.N % t.K != 0)
+        return FP8Q_ESHAPE;
+    if (!aligned(t.q, 16) || !aligned(t.s, 4) || !aligned(t.qt, 16) || !aligned(t.st, 4)) return FP8Q_EALIGN;
+    if (t.n / (t.N * t.K) * cdiv(t.N, 128) * (t.K / 128) > kMaxAdamwBlocks) return FP8Q_EUNSUPPORTED;
+    return kLaunch;
+}
+
+// The first tensor that is refused gives the status; nothing is launched then.
+inline int adamw(const fp8q_adamw_tensor* tensors, int count, int g_dtype, int bits, const fp8q_adamw_config* c,
+                 int scale_mode) {
+    if (!valid_dtype(g_dtype) || (bits != 8 && bits != 32) || !valid_scale_mode(scale_mode) || !c) return FP8Q_EINVAL;
+    if (count < 0) return FP8Q_ESHAPE;
+    if (!(c->beta1 >= 0.0 && c->beta1 < 1.0 && c->beta2 >= 0.0 && c->beta2 < 1.0 && c->eps >= 0.0)) return FP8Q_EINVAL;
+    if (!(c->weight_decay >= 0.0) || (!c->lr_dev && !(c->lr >= 0.0)) || (!c->step_dev && c->step < 1)) return FP8Q_EINVAL;
+    if (count == 0) return FP8Q_OK;
+    if (!tensors) return FP8Q_EINVAL;
+    if (!aligned(c->lr_dev, 4) || !aligned(c->step_dev, 8) || !aligned(c->grad_scale, 4)) return FP8Q_EALIGN;
+    int all = FP8Q_OK;
+    for (int i = 0; i < count; ++i) {
+        const int rc = adamw_tensor(tensors[i], bits);
+        if (rc == kLaunch) all = kLaunch;
+        else if (rc != FP8Q_OK) return rc;
+    }
+    return all;
+}
+
 }  // namespace check
 }  // namespace fp8q

@@ -31,9 +31,9 @@
  * Conventions for every entry point:
  *   - all data pointers are DEVICE pointers owned by the caller; the library
  *     never allocates, frees or keeps a pointer after the call returns (the
- *     calls that need scratch memory, split-K, the norm's backward pass and
- *     the mixture-of-experts layer, take it from the caller as a workspace
- *     argument);
+ *     calls that need scratch memory, split-K, the norm's backward pass, the
+ *     mixture-of-experts layer and the experts' weight gradients, take it from
+ *     the caller as a workspace argument);
  *   - `stream` is a hipStream_t (NULL = the null stream); work is enqueued
  *     asynchronously on it and the call returns without synchronizing;
  *   - arguments are validated on the host before anything is enqueued; on
@@ -44,7 +44,8 @@
  *     leading dimensions of code/input arrays multiples of 16 bytes; scale
  *     arrays need 4-byte alignment only;
  *   - empty problems (a zero dimension) are valid and launch nothing
- *     (fp8q_layernorm_backward of no rows clears the sums it was asked for);
+ *     (fp8q_layernorm_backward of no rows clears the sums it was asked for,
+ *     fp8q_grouped_wgrad of no rows the gradients);
  *   - calls hold no global mutable state and may be made from several host
  *     threads; calls on one stream execute in order;
  *   - a call enqueues kernel launches only (no memset, copy or host
@@ -489,6 +490,139 @@ int fp8q_moe_decode(const void *x, int64_t ldx, int64_t tokens, int64_t hidden, 
                     int64_t w_down_stride, const float *s_down, int64_t lds_down, int64_t s_down_stride,
                     void *y, int y_dtype, int64_t ldy, void *workspace, int64_t workspace_bytes,
                     void *stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The experts' weight gradients, and the AdamW step that takes them.
+ *
+ * Rows grouped by expert (fp8q_grouped_gemm) are contracted per expert in the
+ * Wgrad GEMM: dW_g[N][K] = dY_g^T X_g, in 128-token chunks with one scale per
+ * channel (page 4, sunipension.com wr_id=314414, passages on Figure 7(a) and
+ * Figure 6).  A chunk may not hold tokens of two experts, so both operands are
+ * written transposed in a padded layout: group g, with n_g rows, takes
+ * ceil(n_g / 128) chunks of its own from chunk P_g on,
+ *   P_0 = 0,  P_{g+1} = P_g + ceil(n_g / 128),
+ * its row i stands at column 128 P_g + i, and the columns up to 128 P_{g+1}
+ * are zero codes.  Where every offset is a multiple of 128 this is the layout
+ * of FP8Q_TILE_128x1.  group_offsets are those of fp8q_grouped_gemm (DEVICE
+ * int32[G+1], read on the device, taken as off'[0] = clamp(off[0], 0, rows),
+ * off'[g+1] = clamp(off[g+1], off'[g], rows)); G <= 1024.
+ * ---------------------------------------------------------------------------
+ */
+
+/* Columns of the padded layout that suffice for any G groups of `rows` rows
+   together: a multiple of 128; 0 for negative arguments. */
+int64_t fp8q_grouped_padded_rows(int64_t rows, int G);
+
+/*
+ * fp8q_quantize_act with FP8Q_TILE_128x1, and fp8q_requant_transpose, per
+ * group: x[rows][cols] (or codes q with 1x128 scales s) into the padded layout
+ * qt[cols][..] (stride ldqt >= fp8q_grouped_padded_rows(rows, G)) with scales
+ * st[chunk][cols] (stride ldst >= cols; as many rows as chunks).  Same codes and
+ * scales as the whole-matrix calls give for each group's rows alone.  Columns
+ * and scales past the last group's chunks are not written, rows outside
+ * [off'[0], off'[G]) not read.
+ */
+int fp8q_grouped_quantize_act(const void *x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx,
+                              const int32_t *group_offsets, int G, uint8_t *qt, int64_t ldqt, float *st,
+                              int64_t ldst, int scale_mode, void *stream);
+
+int fp8q_grouped_requant_transpose(const uint8_t *q, int64_t rows, int64_t cols, int64_t ldq, const float *s,
+                                   int64_t lds, const int32_t *group_offsets, int G, uint8_t *qt,
+                                   int64_t ldqt, float *st, int64_t ldst, int scale_mode, void *stream);
+
+/*
+ * Weight gradients of all groups:
+ *   dW_g[n][k] (=|+=) sum over g's chunks c of
+ *       s_a(c, n) * s_b(c, k) * sum_{i in c} dec(A[n][i]) * dec(B[k][i])
+ * a: codes [N][..] (dY^T, stride lda >= fp8q_grouped_padded_rows(rows, G)) with
+ * scales s_a[chunk][N] (ldsa >= N); b: codes [K][..] (X^T) with s_b[chunk][K];
+ * rows, group_offsets, G: those of the two calls above.  dw[G][N][K] (row
+ * stride lddw, group stride dw_group_stride, elements), dw_dtype FP8Q_BF16 or
+ * FP8Q_F32; accumulate != 0 (fp32 only) adds to dw.  The gradient of a group
+ * without rows is zero (rows == 0 too: nothing is read then).  Any N and K;
+ * `flags` and the error bounds are those of fp8q_gemm_ex.
+ * Where the tiles of the gradients do not fill the GPU the contraction is split
+ * as in fp8q_gemm_splitk: workspace of at least
+ * fp8q_grouped_wgrad_workspace(rows, G, N, K) bytes (0: none needed), under the
+ * rules there.  Repeated calls give the same bits.
+ */
+int64_t fp8q_grouped_wgrad_workspace(int64_t rows, int G, int64_t N, int64_t K);
+
+int fp8q_grouped_wgrad(const uint8_t *a, int64_t lda, const float *sa, int64_t ldsa, const uint8_t *b,
+                       int64_t ldb, const float *sb, int64_t ldsb, const int32_t *group_offsets, int G,
+                       int64_t rows, int64_t N, int64_t K, void *dw, int dw_dtype, int64_t lddw,
+                       int64_t dw_group_stride, int accumulate, unsigned flags, void *workspace,
+                       int64_t workspace_bytes, void *stream);
+
+/*
+ * One AdamW step over many tensors, in place.  For every element, in fp32:
+ *   x  = g * grad_scale
+ *   m' = beta1 m + (1 - beta1) x,   v' = beta2 v + (1 - beta2) x^2
+ *   p' = p (1 - lr weight_decay)
+ *        - lr / (1 - beta1^step) * m' / (sqrt(v' / (1 - beta2^step)) + eps)
+ * Master weights p are fp32; gradients g are FP8Q_F32 or FP8Q_BF16 (g_dtype, of
+ * all tensors).  The pages keep master weights and gradients in fp32 and the
+ * moments in fewer bits (page 1, why-be.why-be.co.kr wr_id=65900; page 3,
+ * why-be.why-be.co.kr wr_id=55081).  Moments (bits, of all tensors):
+ *   32: m[n] and v[n], fp32; sm, sv unused;
+ *   8:  codes m[n] of m and v[n] of sqrt(v), with one fp32 scale per 128
+ *       consecutive elements, sm[ceil(n/128)] and sv[..]: s = fl32(amax *
+ *       fl32(1/448)).  A value y = fl32(|x| / s) between two neighbours of the
+ *       E4M3 grid, `unit` apart, becomes
+ *       unit * floor(fl32(y / unit + (r + 1/2) / 2^16)), at most 448: up with
+ *       the probability of its way there (s == 0 gives zeros).  sqrt(v) > 0
+ *       becomes 2^-9 at least.  The step of p takes the moments before they
+ *       are rounded.  Every product and sum of m' and v' and the square root
+ *       round to fp32 (x^2 before its factor), so codes and scales are
+ *       bit-reproducible.
+ *       r, of 16 bits, is the low half (m) or the high half (v) of
+ *         mix(i ^ mix(mix(seed + 0x9e3779b9 * t) + step))   modulo 2^32,
+ *       i the element's index (low 32 bits), t the tensor's in the list, and
+ *         mix(x): x ^= x >> 16; x *= 0x7feb352d; x ^= x >> 15;
+ *                 x *= 0x846ca68b; x ^= x >> 16.
+ *       Zeroed codes and scales are the state before the first step.
+ * Codes of the new weights (q == NULL: none): p holds n / (N K) matrices
+ * [N][K], K a multiple of 128; q[..][N][K] and s[..][ceil(N/128)][K/128] are
+ * what fp8q_quantize_weight gives for each (`scale_mode`), qt[..][K][N16] (N16
+ * = N rounded up to a multiple of 16; columns past N are not written) and
+ * st[..][K/128][ceil(N/128)] what fp8q_transpose_weight gives for that (qt and
+ * st NULL: none).  All arrays are dense.
+ *
+ * `tensors` and `config` are HOST arrays, read before the call returns; a
+ * launch takes 60 tensors without codes, or 34 with.  Arrays of different tensors may not
+ * overlap.  p, g, m, v, q and qt are 16-byte aligned, sm, sv, s and st 4-byte.
+ * n == 0 is an empty tensor; n <= 2^33, and at most 2^22 blocks of 128x128 of a
+ * tensor with codes (else FP8Q_EUNSUPPORTED).
+ * lr_dev, step_dev, grad_scale: DEVICE scalars read when the step runs (NULL:
+ * lr, step, 1), so that a captured step can be replayed with others.
+ * A gradient that is NaN or infinite shows in its element, and in its tile's
+ * scales of 8-bit moments.
+ */
+typedef struct {
+    int64_t n;
+    float *p;
+    const void *g;
+    void *m, *v;
+    float *sm, *sv;
+    int64_t N, K;
+    uint8_t *q;
+    float *s;
+    uint8_t *qt;
+    float *st;
+} fp8q_adamw_tensor;
+
+typedef struct {
+    double lr, beta1, beta2, eps, weight_decay;
+    int64_t step; /* from 1 on */
+    const float *lr_dev;
+    const int64_t *step_dev;
+    const float *grad_scale;
+    uint32_t seed;
+} fp8q_adamw_config;
+
+int fp8q_adamw(const fp8q_adamw_tensor *tensors, int count, int g_dtype, int bits,
+               const fp8q_adamw_config *config, int scale_mode, void *stream);
 
 /* Static, human-readable name of a status code (never NULL). */
 const char *fp8q_strerror(int status);
