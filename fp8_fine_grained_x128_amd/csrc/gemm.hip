@@ -236,17 +236,6 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_strip_kernel(GemmParams 
 constexpr int kMaxGroups = 1024;
 constexpr int kTileClasses = 4;  // 256-, 192-, 128- and 64-row tiles
 
-// Largest g < G with start[g] <= t (start is non-decreasing, start[G] > t).
-__device__ __forceinline__ int find_group(const int32_t* start, int G, int64_t t) {
-    int lo = 0, hi = G;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (start[mid] <= t) lo = mid; else hi = mid;
-    }
-    while (lo + 1 < G && start[lo + 1] <= t) ++lo;  // skip groups with no tiles here
-    return __builtin_amdgcn_readfirstlane(lo);
-}
-
 // Height class of an expert's last row tile: 0 (256 rows), 1 (192), 2 (128)
 // or 3 (64) for `last` = 1..256 rows in it.
 __device__ __forceinline__ int last_tile_class(int64_t last) {

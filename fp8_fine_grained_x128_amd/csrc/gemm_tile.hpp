@@ -785,4 +785,15 @@ __device__ __forceinline__ int64_t uniform64(int64_t v) {
     return (int64_t)(((uint64_t)hi << 32) | lo);
 }
 
+// Largest g < G with start[g] <= t (start is non-decreasing, start[G] > t).
+__device__ __forceinline__ int find_group(const int32_t* start, int G, int64_t t) {
+    int lo = 0, hi = G;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid] <= t) lo = mid; else hi = mid;
+    }
+    while (lo + 1 < G && start[lo + 1] <= t) ++lo;  // skip groups with no tiles here
+    return __builtin_amdgcn_readfirstlane(lo);
+}
+
 }  // namespace fp8q

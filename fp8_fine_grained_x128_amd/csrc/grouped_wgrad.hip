@@ -1,74 +1,388 @@
 // grouped_wgrad.hip -- the weight gradients of all experts:
-//   dW_g[n][k] (=|+=) sum over the 128-token chunks t of group g
-//                     s_a(t, n) * s_b(t, k) * sum_{token in t} dec(A[n][token]) * dec(B[k][token])
-// A = dY^T and B = X^T in the layout of groups.hpp (every group takes whole
-// chunks of its own), one scale per row and chunk, so a tile of a group's
-// gradient is the row-scaled product of gemm_tile.hpp over that group's chunks.
+//   dW_g[n][k] (=|+=) sum over the 128-token chunks c of group g
+//                     s_dy(c, n) * s_x(c, k) * sum_{i in c} dec(dY^T[n][i]) * dec(X^T[k][i])
+// Both operands lie transposed in the layout of groups.hpp (every group takes
+// whole chunks of its own), one scale per channel and chunk, so a tile of a
+// group's gradient is the row-scaled product of gemm_tile.hpp over that
+// group's chunks.
 #include "gemm_tile.hpp"
 #include "groups.hpp"
+#include "tile_io.hpp"
 
 namespace fp8q {
 
+namespace {
+
 constexpr int kMaxWgradGroups = 1024;
 
-template <int BM, int BN, int WM, int WN, int OUT, bool ACC, int MMA>
-__global__ __launch_bounds__(64 * WM * WN, 1) void grouped_wgrad_kernel(GemmParams p, int64_t c_group_stride) {
-    using Cfg = GemmCfg<BM, BN, WM, WN, 1>;
-    // one LDS object (see grouped_gemm_kernel): the tile stages, then the first chunk of every group
-    __shared__ __align__(1024) uint8_t lds[2 * Cfg::kStageBytes + 4 * (kMaxWgradGroups + 1)];
-    int32_t* first = reinterpret_cast<int32_t*>(lds + 2 * Cfg::kStageBytes);
-    const int G = p.groups;
-    if (p.K == 0) {  // no rows, perhaps no offsets either
-        for (int g = threadIdx.x; g <= G; g += 64 * WM * WN) first[g] = 0;
-    } else if (threadIdx.x < 64) {
-        const int lane = threadIdx.x;
-        int mine = 0;
-        for_groups_of_lane(p.offsets, G, (int)p.K, lane, [&](int, int lo, int hi) { mine += (hi - lo + 127) >> 7; });
-        int at = wave_scan_sum(mine) - mine;
-        for_groups_of_lane(p.offsets, G, (int)p.K, lane, [&](int g, int lo, int hi) {
-            first[g] = at;
-            at += (hi - lo + 127) >> 7;
-            first[g + 1] = at;
-        });
-    }
-    __syncthreads();
-    const int64_t tiles = p.tiles_m * p.tiles_n;
-    const int64_t total = tiles * G;
-    const int64_t nwg = gridDim.x;
-    const int64_t slot = nwg % 8 == 0 ? (int64_t)(blockIdx.x % 8) * (nwg / 8) + blockIdx.x / 8 : blockIdx.x;
-    for (int64_t w = slot; w < total; w += nwg) {
-        const int g = __builtin_amdgcn_readfirstlane((int)(w / tiles));
-        const int64_t in_g = w % tiles;
-        TileCoord tc;
-        tc.group = g;
-        tc.m0 = uniform64(in_g / p.tiles_n * BM);
-        tc.n0 = uniform64(in_g % p.tiles_n * BN);
-        tc.m_end = p.M;
-        const int64_t kb0 = __builtin_amdgcn_readfirstlane(first[g]), kb1 = __builtin_amdgcn_readfirstlane(first[g + 1]);
-        GemmParams q = p;
-        q.c = static_cast<uint8_t*>(p.c) + g * c_group_stride * (OUT == kDtypeF32 ? 4 : 2);
-        if (kb0 < kb1) {
-            gemm_tile<BM, BN, WM, WN, 1, OUT, ACC, MMA, -2, true>(q, tc, p.b, p.sb, lds, kb0, kb1);
-            __syncthreads();
-        } else if (!ACC) {  // no tokens: a zero gradient
-            const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-            const v4f zero[Cfg::MT][Cfg::NT] = {};
-            store_tile<Cfg, OUT, false>(zero, q.c, p.ldc, tc, p.N, wave / WN, wave % WN, lane);
+// 4-byte buffer copy to LDS: lane i's dword (or 0 past the record count) lands at lds + 4 * i.
+__device__ __forceinline__ void buffer_copy4_to_lds(__amdgpu_buffer_rsrc_t r, uint32_t voffset, void* lds) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)lds, 4, voffset, 0, 0, 0);
+#else
+    (void)r;
+    (void)voffset;
+    (void)lds;
+#endif
+}
+
+// A is X^T (rows k), B is dY^T (rows n): an accumulator's four elements of a
+// lane are then four consecutive k of one row of dW.
+struct WgradParams {
+    const uint8_t* a;
+    const uint8_t* b;
+    const float* sa;
+    const float* sb;
+    int lda, ldb;
+    int64_t ldsa, ldsb;
+    const int32_t* offsets;
+    int groups;
+    int rows;
+    int M, N;  // channels of X, channels of dY
+    void* c;
+    int64_t ldc, c_group_stride;
+    int tiles_m, tiles_n;
+    int vec;    // c and its strides allow stores of four elements
+    int slice;  // chunks of a slice: a group of more is split, its slices' tiles go to ws
+    float* ws;  // [slice][N][ldws]
+    int64_t ldws;
+};
+
+// Slices of a group of `chunks`: one that is stored to dW at once, or several.
+__device__ __forceinline__ int split_slices(int chunks, int slice) {
+    return chunks > slice ? (chunks + slice - 1) / slice : 0;
+}
+
+template <int BM, int BN>
+struct Job {
+    int kb, kb1;  // chunks
+    int m0, n0;
+    void* c;      // nullptr: no more jobs
+    int64_t ldc;
+    bool partial;  // fp32 slice in ws
+};
+
+// Four consecutive values of a row, the first at p; `count` of them exist.
+template <int OUT, bool ACC>
+__device__ __forceinline__ void store4(void* row, int64_t k, int count, const v4f& v, bool vec) {
+    if constexpr (OUT == kDtypeF32) {
+        float* p = static_cast<float*>(row) + k;
+        if (vec && count >= 4) {
+            v4f w = v;
+            if constexpr (ACC) w += *reinterpret_cast<const v4f*>(p);
+            *reinterpret_cast<v4f*>(p) = w;
+        } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (r < count) p[r] = ACC ? p[r] + v[r] : v[r];
+        }
+    } else {
+        uint16_t* p = static_cast<uint16_t*>(row) + k;
+        uint16_t h[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) h[r] = f32_to_bf16(v[r]);
+        if (vec && count >= 4) {
+            *reinterpret_cast<uint2*>(p) = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
+        } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (r < count) p[r] = h[r];
         }
     }
 }
 
-namespace {
+template <class Cfg, int OUT, bool ACC>
+__device__ __forceinline__ void store_transposed(const v4f (&acc)[Cfg::MT][Cfg::NT], void* c, int64_t ldc, int m0,
+                                                 int n0, int M, int N, int wm, int wn, int lane, bool vec) {
+    const int g = lane >> 4, r16 = lane & 15;
+    constexpr int kEl = OUT == kDtypeF32 ? 4 : 2;
+#pragma unroll
+    for (int j = 0; j < Cfg::NT; ++j) {
+        const int n = n0 + wn * Cfg::TN + 16 * j + r16;
+        if (n >= N) continue;
+        uint8_t* row = static_cast<uint8_t*>(c) + n * ldc * kEl;
+#pragma unroll
+        for (int i = 0; i < Cfg::MT; ++i) {
+            const int k = m0 + wm * Cfg::TM + 16 * i + 4 * g;
+            store4<OUT, ACC>(row, k, M - k > 4 ? 4 : M - k, acc[i][j], vec);
+        }
+    }
+}
+
+// A tile that lies inside dW's columns, through a buffer descriptor: its
+// record count ends at dW's last row (rows past it are dropped by the range
+// check), an element's place is one 32-bit offset, and the 16 columns of a
+// subtile are constants of the instruction.
+#ifndef WG_AUX
+#define WG_AUX 0
+#endif
+template <class Cfg, int OUT, bool ACC>
+__device__ __forceinline__ void store_tile_buffer(const v4f (&acc)[Cfg::MT][Cfg::NT], __amdgpu_buffer_rsrc_t rc,
+                                                  uint32_t row_bytes, int wm, int wn, int lane) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    constexpr uint32_t kEl = OUT == kDtypeF32 ? 4 : 2;
+    const int g = lane >> 4, r16 = lane & 15;
+    uint32_t off = (wn * Cfg::TN + r16) * row_bytes + (wm * Cfg::TM + 4 * g) * kEl;
+#pragma unroll
+    for (int j = 0; j < Cfg::NT; ++j) {
+        if constexpr (ACC) {
+            v4f old[Cfg::MT];
+#pragma unroll
+            for (int i = 0; i < Cfg::MT; ++i)
+                old[i] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rc, off + 16 * i * kEl, 0, 0));
+#pragma unroll
+            for (int i = 0; i < Cfg::MT; ++i)
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, old[i] + acc[i][j]), rc,
+                                                       off + 16 * i * kEl, 0, WG_AUX);
+        } else if constexpr (OUT == kDtypeF32) {
+#pragma unroll
+            for (int i = 0; i < Cfg::MT; ++i)
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[i][j]), rc, off + 16 * i * kEl, 0,
+                                                       WG_AUX);
+        } else {
+            typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+            for (int i = 0; i < Cfg::MT; ++i) {
+                const u32x2 h = {pack_bf16(acc[i][j][0], acc[i][j][1]), pack_bf16(acc[i][j][2], acc[i][j][3])};
+                __builtin_amdgcn_raw_buffer_store_b64(h, rc, off + 16 * i * kEl, 0, WG_AUX);
+            }
+        }
+        off += 16 * row_bytes;
+    }
+#endif
+}
+
+// This lane's number, formed where it stands: what is derived from it is then
+// not held (and spilled) across the loops around.
+__device__ __forceinline__ int lane_now() {
+#if defined(__HIP_DEVICE_COMPILE__)
+    int v = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+    asm volatile("" : "+v"(v));
+    return v;
+#else
+    return 0;
+#endif
+}
+
+// Where a job's operands come from: descriptors of its rows of codes (as in
+// gemm_tile.hpp: rows past the matrix read zeros) and of the scales of one
+// 64-channel run a wave, which move by a row of scales from chunk to chunk.
+struct Source {
+    __amdgpu_buffer_rsrc_t ra, rb;
+    const float* s;  // this wave's run in chunk 0
+    uint32_t s_bytes;
+};
+
+// The asynchronous copies of chunk kb into a stage, in gemm_tile.hpp's layout:
+// part `it` of a wave is 8 rows of codes, and with part 0 goes its run of scales.
+template <class Cfg, int BM>
+struct Copies {
+    uint32_t off_a, off_b;
+    __device__ __forceinline__ Copies(const WgradParams& p, int wave) {
+        const int lane = lane_now(), lrow = lane >> 3, unit = (lane & 7) ^ swz(lrow);
+        off_a = (uint32_t)((8 * wave + lrow) * p.lda + 16 * unit);
+        off_b = (uint32_t)((8 * wave + lrow) * p.ldb + 16 * unit);
+    }
+    __device__ __forceinline__ void issue(uint8_t* stage, const Source& src, const WgradParams& p, int kb, int wave,
+                                          int it) const {
+        constexpr int kRows = 8 * Cfg::kWaves;  // rows of one part of all waves
+        const bool is_a = kRows * it < BM;
+        const uint32_t step = (uint32_t)(is_a ? kRows * it * p.lda : (kRows * it - BM) * p.ldb);
+        uint32_t voff;
+        asm volatile("v_add_u32 %0, %1, %2" : "=v"(voff) : "s"(step), "v"(is_a ? off_a : off_b));
+        buffer_copy16_to_lds(is_a ? src.ra : src.rb, voff, (uint32_t)kb * 128u, stage + 1024 * (wave + Cfg::kWaves * it));
+        if (it == 0 && wave < Cfg::kScaleCopies) {
+            const __amdgpu_buffer_rsrc_t rs =
+                make_rsrc(src.s + (int64_t)kb * (wave < BM / 64 ? p.ldsa : p.ldsb), src.s_bytes);
+            buffer_copy4_to_lds(rs, 4u * lane_now(), stage + Cfg::kTileBytes + 256 * wave);
+        }
+    }
+};
+
+// One chunk's products from stage `cur` while the next one's operands are
+// copied into stage `nxt`.  (The stages are told apart by the parameters'
+// __restrict__: without it the compiler lets every fragment read wait for all
+// copies under way, 1.4 times the time of the whole kernel.)
+template <class Cfg, int BM, int MMA>
+__device__ __forceinline__ void chunk_step(const uint8_t* __restrict__ cur, uint8_t* __restrict__ nxt, const Source& src,
+                                           const WgradParams& p, int kb_next, v4f (&acc)[Cfg::MT][Cfg::NT], int wave,
+                                           int wm, int wn, int lane) {
+    const Copies<Cfg, BM> copies(p, wave);
+    auto issue = [&](int part) __attribute__((always_inline)) { copies.issue(nxt, src, p, kb_next, wave, part); };
+    compute_chunk<Cfg, BM, 1, MMA>(cur, reinterpret_cast<const float*>(cur + Cfg::kTileBytes), acc, wm, wn, lane, 0,
+                                   issue);
+}
+
+template <int BM, int BN, int WM, int WN, int OUT, bool ACC, int MMA>
+__global__ __launch_bounds__(64 * WM * WN, 2) void grouped_wgrad_kernel(WgradParams p) {
+    using Cfg = GemmCfg<BM, BN, WM, WN, 1>;
+    // One LDS object (see grouped_gemm_kernel): the tile stages, then the first
+    // chunk of every group and the first job of every group.
+    __shared__ __align__(1024) uint8_t lds[2 * Cfg::kStageBytes + 12 * (kMaxWgradGroups + 1)];
+    int32_t* first = reinterpret_cast<int32_t*>(lds + 2 * Cfg::kStageBytes);
+    int32_t* slices = first + kMaxWgradGroups + 1;  // slices before the group's, in ws
+    int32_t* parts = slices + kMaxWgradGroups + 1;  // tile rounds (one a slice) before the group's
+    const int G = p.groups;
+    const int lane = threadIdx.x & 63;
+    if (p.rows == 0) {  // perhaps no offsets either
+        for (int g = threadIdx.x; g <= G; g += 64 * WM * WN) first[g] = slices[g] = 0, parts[g] = g;
+    } else if (threadIdx.x < 64) {
+        int n_chunks = 0, n_slices = 0, n_parts = 0;
+        for_groups_of_lane(p.offsets, G, p.rows, lane, [&](int, int lo, int hi) {
+            const int chunks = (hi - lo + 127) >> 7, sl = split_slices(chunks, p.slice);
+            n_chunks += chunks, n_slices += sl, n_parts += sl ? sl : 1;
+        });
+        int c0 = wave_scan_sum(n_chunks) - n_chunks, s0 = wave_scan_sum(n_slices) - n_slices;
+        int p0 = wave_scan_sum(n_parts) - n_parts;
+        for_groups_of_lane(p.offsets, G, p.rows, lane, [&](int g, int lo, int hi) {
+            const int chunks = (hi - lo + 127) >> 7, sl = split_slices(chunks, p.slice);
+            first[g] = c0, slices[g] = s0, parts[g] = p0;
+            c0 += chunks, s0 += sl, p0 += sl ? sl : 1;
+            first[g + 1] = c0, slices[g + 1] = s0, parts[g + 1] = p0;
+        });
+    }
+    __syncthreads();
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    // The tiles of a round (one slice of a group) go to consecutive work-groups,
+    // round by round; this one takes every gridDim.x-th.
+    const uint32_t tiles = (uint32_t)p.tiles_m * p.tiles_n, nwg = gridDim.x;
+    uint32_t in = nwg % 8 == 0 ? blockIdx.x % 8 * (nwg / 8) + blockIdx.x / 8 : blockIdx.x;
+    int part = 0, g = 0;
+    const int n_parts = __builtin_amdgcn_readfirstlane(parts[G]);
+    constexpr int kEl = OUT == kDtypeF32 ? 4 : 2;
+
+    // The next job; gradients of groups without rows are written on the way.
+    auto next_job = [&]() __attribute__((always_inline)) {
+        Job<BM, BN> job;
+        job.c = nullptr;
+        for (;; in += nwg) {
+            while (in >= tiles) in -= tiles, ++part;
+            if (part >= n_parts) return job;
+            while (__builtin_amdgcn_readfirstlane(parts[g + 1]) <= part) ++g;
+            const int c0 = __builtin_amdgcn_readfirstlane(first[g]), c1 = __builtin_amdgcn_readfirstlane(first[g + 1]);
+            // eight tiles of k by all of n, then the next eight: concurrent tiles share their operands in L2
+            const uint32_t band = 8 * p.tiles_n, b0 = in / band * 8, in_band = in % band;
+            const uint32_t height = p.tiles_m - b0 < 8 ? p.tiles_m - b0 : 8;
+            job.m0 = (int)(b0 + in_band % height) * BM;
+            job.n0 = (int)(in_band / height) * BN;
+            uint8_t* c = static_cast<uint8_t*>(p.c) + g * p.c_group_stride * kEl;
+            job.partial = c1 - c0 > p.slice;
+            if (job.partial) {
+                const int sl = part - __builtin_amdgcn_readfirstlane(parts[g]);
+                job.kb = c0 + sl * p.slice;
+                job.kb1 = job.kb + p.slice < c1 ? job.kb + p.slice : c1;
+                job.ldc = p.ldws;
+                job.c = p.ws + (int64_t)(__builtin_amdgcn_readfirstlane(slices[g]) + sl) * p.N * p.ldws;
+                return job;
+            }
+            if (c0 < c1) {
+                job.kb = c0, job.kb1 = c1, job.ldc = p.ldc;
+                job.c = c;
+                return job;
+            }
+            if constexpr (!ACC) {
+                const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (int e = 64 * wave + lane_now(); e < BN * BM / 4; e += 64 * WM * WN) {
+                    const int n = job.n0 + e / (BM / 4), k = job.m0 + e % (BM / 4) * 4;
+                    if (n < p.N && k < p.M)
+                        store4<OUT, false>(c + n * p.ldc * kEl, k, p.M - k > 4 ? 4 : p.M - k, zero, p.vec);
+                }
+            }
+        }
+    };
+
+    auto source_of = [&](const Job<BM, BN>& job) __attribute__((always_inline)) {
+        Source s;
+        s.ra = make_rsrc(p.a + (int64_t)job.m0 * p.lda, (int64_t)(p.M - job.m0) * p.lda);
+        s.rb = make_rsrc(p.b + (int64_t)job.n0 * p.ldb, (int64_t)(p.N - job.n0) * p.ldb);
+        const int of_a = job.m0 + 64 * wave, of_b = job.n0 + 64 * (wave - BM / 64);
+        const int left = wave < BM / 64 ? p.M - of_a : p.N - of_b;
+        s.s = wave < BM / 64 ? p.sa + of_a : p.sb + of_b;
+        s.s_bytes = left <= 0 ? 0u : left >= 64 ? 256u : 4u * left;
+        return s;
+    };
+
+    Job<BM, BN> job = next_job();
+    if (!job.c) return;
+    Source src = source_of(job);
+    int stage = 0;
+    bool behind = false;  // Cfg::MT * Cfg::NT stores were issued after the last copies
+    {
+        const Copies<Cfg, BM> copies(p, wave);
+#pragma unroll
+        for (int it = 0; it < Cfg::kLoadsPerWave; ++it) copies.issue(lds, src, p, job.kb, wave, it);
+    }
+    for (;;) {
+        v4f acc[Cfg::MT][Cfg::NT];
+#pragma unroll
+        for (int i = 0; i < Cfg::MT; ++i)
+#pragma unroll
+            for (int j = 0; j < Cfg::NT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        Job<BM, BN> next = job;
+        for (int kb = job.kb; kb < job.kb1; ++kb) {
+            // memory operations complete in order: a job's first chunk was
+            // copied before the last job's stores, which go on under it
+            if (behind) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(Cfg::MT * Cfg::NT) : "memory");
+            else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            behind = false;
+            __syncthreads();
+            // under this chunk's products the next one of this job is copied,
+            // or the first one of the next job (after the last of all, this
+            // one again, into the stage that is not read any more)
+            int kb_next = kb + 1;
+            if (kb_next == job.kb1) {
+                in += nwg;
+                next = next_job();
+                kb_next = kb;
+                if (next.c) {
+                    src = source_of(next);
+                    kb_next = next.kb;
+                }
+            }
+            chunk_step<Cfg, BM, MMA>(lds + stage * Cfg::kStageBytes, lds + (stage ^ 1) * Cfg::kStageBytes, src, p, kb_next,
+                                     acc, wave, wm, wn, lane_now());
+            stage ^= 1;
+        }
+        const int ln = lane_now();
+        if (p.vec && job.m0 + BM <= p.M) {
+            const uint32_t row_bytes = (uint32_t)job.ldc * (job.partial ? 4 : kEl);
+            const int64_t rows = p.N - job.n0 < BN ? p.N - job.n0 : BN;
+            const __amdgpu_buffer_rsrc_t rc =
+                make_rsrc(static_cast<uint8_t*>(job.c) + job.n0 * (int64_t)row_bytes + (int64_t)job.m0 * (job.partial ? 4 : kEl),
+                          (rows - 1) * row_bytes + BM * (job.partial ? 4 : kEl));
+            if (job.partial)
+                store_tile_buffer<Cfg, kDtypeF32, false>(acc, rc, row_bytes, wm, wn, ln);
+            else
+                store_tile_buffer<Cfg, OUT, ACC>(acc, rc, row_bytes, wm, wn, ln);
+            behind = true;
+        } else if (job.partial) {
+            store_transposed<Cfg, kDtypeF32, false>(acc, job.c, job.ldc, job.m0, job.n0, p.M, p.N, wm, wn, ln, true);
+        } else {
+            store_transposed<Cfg, OUT, ACC>(acc, job.c, job.ldc, job.m0, job.n0, p.M, p.N, wm, wn, ln, p.vec);
+        }
+        if (!next.c) break;
+        job = next;
+    }
+}
+
+#ifdef WG_SMALL
+#define WG_CFG 128, 128, 2, 2
+constexpr int kTile = 128, kWg = 2, kThr = 256;
+#else
+#define WG_CFG 256, 256, 2, 4
+constexpr int kTile = 256, kWg = 1, kThr = 512;
+#endif
 
 template <int MMA>
-void launch_wgrad_mma(const GemmArgs& g, const GemmParams& p, int64_t grid, int64_t c_group_stride, hipStream_t st) {
-    const dim3 gr((unsigned)grid), bl(512);
+void launch_wgrad_mma(const GemmArgs& g, const WgradParams& p, int64_t grid, hipStream_t st) {
+    const dim3 gr((unsigned)grid), bl(kThr);
     if (g.c_dtype == kDtypeBF16)
-        hipLaunchKernelGGL((grouped_wgrad_kernel<256, 256, 2, 4, kDtypeBF16, false, MMA>), gr, bl, 0, st, p, c_group_stride);
+        hipLaunchKernelGGL((grouped_wgrad_kernel<WG_CFG, kDtypeBF16, false, MMA>), gr, bl, 0, st, p);
     else if (g.accumulate)
-        hipLaunchKernelGGL((grouped_wgrad_kernel<256, 256, 2, 4, kDtypeF32, true, MMA>), gr, bl, 0, st, p, c_group_stride);
+        hipLaunchKernelGGL((grouped_wgrad_kernel<WG_CFG, kDtypeF32, true, MMA>), gr, bl, 0, st, p);
     else
-        hipLaunchKernelGGL((grouped_wgrad_kernel<256, 256, 2, 4, kDtypeF32, false, MMA>), gr, bl, 0, st, p, c_group_stride);
+        hipLaunchKernelGGL((grouped_wgrad_kernel<WG_CFG, kDtypeF32, false, MMA>), gr, bl, 0, st, p);
 }
 
 }  // namespace
@@ -76,23 +390,24 @@ void launch_wgrad_mma(const GemmArgs& g, const GemmParams& p, int64_t grid, int6
 int64_t grouped_wgrad_bytes(int64_t, int, int64_t, int64_t) { return 0; }
 
 hipError_t launch_grouped_wgrad(const GemmArgs& g, int64_t c_group_stride, hipStream_t st) {
-    GemmParams p{};
-    p.a = g.a; p.lda = g.lda; p.sa = g.sa; p.ldsa = g.ldsa;
-    p.b = g.b; p.ldb = g.ldb; p.sb = g.sb; p.ldsb = g.ldsb;
-    p.offsets = g.offsets; p.groups = g.groups;
-    p.M = g.M; p.N = g.N; p.K = g.K; p.c = g.c; p.ldc = g.ldc;
-    p.tiles_m = (g.M + 255) / 256;
-    p.tiles_n = (g.N + 255) / 256;
+    WgradParams p{};
+    p.a = g.b; p.lda = (int)g.ldb; p.sa = g.sb; p.ldsa = g.ldsb;
+    p.b = g.a; p.ldb = (int)g.lda; p.sb = g.sa; p.ldsb = g.ldsa;
+    p.offsets = g.offsets; p.groups = g.groups; p.rows = (int)g.K;
+    p.M = (int)g.N; p.N = (int)g.M; p.c = g.c; p.ldc = g.ldc; p.c_group_stride = c_group_stride;
+    p.tiles_m = (p.M + kTile - 1) / kTile;
+    p.tiles_n = (p.N + kTile - 1) / kTile;
     const int64_t el = g.c_dtype == kDtypeF32 ? 4 : 2;
-    p.vec_store = (reinterpret_cast<uintptr_t>(g.c) % 16 == 0) && ((g.ldc * el) % 16 == 0) &&
-                  ((c_group_stride * el) % 16 == 0);
-    const int64_t work = p.tiles_m * p.tiles_n * g.groups, cus = compute_units();
+    p.vec = reinterpret_cast<uintptr_t>(g.c) % 16 == 0 && g.ldc * el % 16 == 0 && c_group_stride * el % 16 == 0 &&
+            g.ldc * el < (int64_t(1) << 24);  // 256 rows within 32-bit offsets
+    p.slice = INT32_MAX;
+    const int64_t work = (int64_t)p.tiles_m * p.tiles_n * g.groups, cus = kWg * compute_units();
     const int64_t grid = work < cus ? work : cus;
     switch (g.mma) {
-        case kMmaFp8: launch_wgrad_mma<kMmaFp8>(g, p, grid, c_group_stride, st); break;
-        case kMmaBf16Fold: launch_wgrad_mma<kMmaBf16Fold>(g, p, grid, c_group_stride, st); break;
-        case kMmaFp8Scaled: launch_wgrad_mma<kMmaFp8Scaled>(g, p, grid, c_group_stride, st); break;
-        default: launch_wgrad_mma<kMmaF16>(g, p, grid, c_group_stride, st); break;
+        case kMmaFp8: launch_wgrad_mma<kMmaFp8>(g, p, grid, st); break;
+        case kMmaBf16Fold: launch_wgrad_mma<kMmaBf16Fold>(g, p, grid, st); break;
+        case kMmaFp8Scaled: launch_wgrad_mma<kMmaFp8Scaled>(g, p, grid, st); break;
+        default: launch_wgrad_mma<kMmaF16>(g, p, grid, st); break;
     }
     return hipGetLastError();
 }

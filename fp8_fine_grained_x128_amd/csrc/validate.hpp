@@ -399,11 +399,17 @@ inline int grouped_requant(const void* q, int64_t rows, int64_t cols, int64_t ld
     return aligned(q, 16) && ldq % 16 == 0 && aligned(s, 4) ? kLaunch : FP8Q_EALIGN;
 }
 
+constexpr int64_t kMaxWgradChannels = int64_t(1) << 30;
+constexpr int64_t kMaxWgradTiles = int64_t(1) << 30;
+
 // Sizes of the weight gradients: FP8Q_ESHAPE or FP8Q_EUNSUPPORTED where there
 // are none.
 inline int wgrad_sizes(int64_t rows, int G, int64_t N, int64_t K) {
     if (G < 1 || G > kMaxGroups || rows < 0 || N < 0 || K < 0) return FP8Q_ESHAPE;
-    if (N > kMaxLd || K > kMaxLd || rows > INT32_MAX || padded_rows(rows, G) > kMaxOperandLd) return FP8Q_EUNSUPPORTED;
+    if (rows > INT32_MAX || padded_rows(rows, G) > kMaxOperandLd) return FP8Q_EUNSUPPORTED;
+    // channels and 128x128 tiles of all groups are counted in 32 bits
+    if (N > kMaxWgradChannels || K > kMaxWgradChannels || cdiv(N, 128) * cdiv(K, 128) > kMaxWgradTiles / G)
+        return FP8Q_EUNSUPPORTED;
     return kLaunch;
 }
 
@@ -425,8 +431,6 @@ inline int grouped_wgrad(const void* a, int64_t lda, const void* sa, int64_t lds
         return FP8Q_ESHAPE;
     if (lda > kMaxOperandLd || ldb > kMaxOperandLd) return FP8Q_EUNSUPPORTED;
     if (N == 0 || K == 0) return FP8Q_OK;
-    // N, lddw <= 2^32: the product may pass 2^63 only where a factor is over 2^31
-    if (N > (int64_t(1) << 31) || lddw > (int64_t(1) << 31)) return FP8Q_EUNSUPPORTED;
     if (G > 1 && dw_group_stride < (N - 1) * lddw + K) return FP8Q_ESHAPE;
     if (!dw) return FP8Q_EINVAL;
     if (!aligned(dw, (uintptr_t)elem_bytes(dw_dtype))) return FP8Q_EALIGN;
