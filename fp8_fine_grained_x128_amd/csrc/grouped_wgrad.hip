@@ -5,6 +5,8 @@
 // whole chunks of its own), one scale per channel and chunk, so a tile of a
 // group's gradient is the row-scaled product of gemm_tile.hpp over that
 // group's chunks.
+#include <type_traits>
+
 #include "gemm_tile.hpp"
 #include "groups.hpp"
 #include "tile_io.hpp"
@@ -91,65 +93,104 @@ __device__ __forceinline__ void store4(void* row, int64_t k, int count, const v4
     }
 }
 
-template <class Cfg, int OUT, bool ACC>
-__device__ __forceinline__ void store_transposed(const v4f (&acc)[Cfg::MT][Cfg::NT], void* c, int64_t ldc, int m0,
-                                                 int n0, int M, int N, int wm, int wn, int lane, bool vec) {
-    const int g = lane >> 4, r16 = lane & 15;
-    constexpr int kEl = OUT == kDtypeF32 ? 4 : 2;
+// A wave's tile that lies inside dW's columns, 16 rows at a time through its
+// LDS region: a store instruction writes two 512-byte (bf16: four 256-byte)
+// pieces of rows, through a buffer descriptor whose record count ends at dW's
+// last row (rows past it are dropped by the range check).  kStores of them.
+// They are marked as streaming: 64 experts of 2048x7168, 1312 -> 1277 us.
+[[maybe_unused]] constexpr int kStreaming = 2;
+template <class Cfg, int OUT>
+struct Rows {
+    static constexpr int kEl = OUT == kDtypeF32 ? 4 : 2;
+    static constexpr int kBytes = Cfg::TM * kEl, kPitch = kBytes + 16, kUnits = kBytes / 16;
+    static constexpr int kAtOnce = 64 / kUnits;  // rows of one store
+    static constexpr int kStores = Cfg::NT * 16 / kAtOnce;
+    static_assert(16 * kPitch * Cfg::kWaves <= Cfg::kStageBytes, "the regions of all waves in one stage");
+};
+// Rows 16j .. 16j+15 of a wave's tile into its LDS region.
+template <class Cfg, int OUT>
+__device__ __forceinline__ void stage_rows(const v4f (&acc)[Cfg::MT][Cfg::NT], int j, uint8_t* region, int lane) {
+    using R = Rows<Cfg, OUT>;
+    uint8_t* to = region + (lane & 15) * R::kPitch + 4 * (lane >> 4) * R::kEl;
+    if (j > 0) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the last rows are read
 #pragma unroll
-    for (int j = 0; j < Cfg::NT; ++j) {
-        const int n = n0 + wn * Cfg::TN + 16 * j + r16;
-        if (n >= N) continue;
-        uint8_t* row = static_cast<uint8_t*>(c) + n * ldc * kEl;
-#pragma unroll
-        for (int i = 0; i < Cfg::MT; ++i) {
-            const int k = m0 + wm * Cfg::TM + 16 * i + 4 * g;
-            store4<OUT, ACC>(row, k, M - k > 4 ? 4 : M - k, acc[i][j], vec);
-        }
+    for (int i = 0; i < Cfg::MT; ++i) {
+        if constexpr (OUT == kDtypeF32)
+            *reinterpret_cast<v4f*>(to + 16 * i * R::kEl) = acc[i][j];
+        else
+            *reinterpret_cast<uint2*>(to + 16 * i * R::kEl) =
+                make_uint2(pack_bf16(acc[i][j][0], acc[i][j][1]), pack_bf16(acc[i][j][2], acc[i][j][3]));
     }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // written
 }
 
-// A tile that lies inside dW's columns, through a buffer descriptor: its
-// record count ends at dW's last row (rows past it are dropped by the range
-// check), an element's place is one 32-bit offset, and the 16 columns of a
-// subtile are constants of the instruction.
-#ifndef WG_AUX
-#define WG_AUX 0
-#endif
 template <class Cfg, int OUT, bool ACC>
-__device__ __forceinline__ void store_tile_buffer(const v4f (&acc)[Cfg::MT][Cfg::NT], __amdgpu_buffer_rsrc_t rc,
-                                                  uint32_t row_bytes, int wm, int wn, int lane) {
+__device__ __forceinline__ void store_rows(const v4f (&acc)[Cfg::MT][Cfg::NT], __amdgpu_buffer_rsrc_t rc,
+                                           uint32_t row_bytes, int wm, int wn, int lane, uint8_t* region) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    constexpr uint32_t kEl = OUT == kDtypeF32 ? 4 : 2;
-    const int g = lane >> 4, r16 = lane & 15;
-    uint32_t off = (wn * Cfg::TN + r16) * row_bytes + (wm * Cfg::TM + 4 * g) * kEl;
+    using R = Rows<Cfg, OUT>;
+    const uint8_t* from = region + lane / R::kUnits * R::kPitch + lane % R::kUnits * 16;
+    uint32_t off = (wn * Cfg::TN + lane / R::kUnits) * row_bytes + wm * R::kBytes + lane % R::kUnits * 16;
 #pragma unroll
     for (int j = 0; j < Cfg::NT; ++j) {
+        stage_rows<Cfg, OUT>(acc, j, region, lane);
+        constexpr int kN = 16 / R::kAtOnce;
+        u32x4 v[kN];
+        v4f old[ACC ? kN : 1];
         if constexpr (ACC) {
-            v4f old[Cfg::MT];
 #pragma unroll
-            for (int i = 0; i < Cfg::MT; ++i)
-                old[i] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rc, off + 16 * i * kEl, 0, 0));
+            for (int u = 0; u < kN; ++u)
+                old[u] = __builtin_bit_cast(
+                    v4f, __builtin_amdgcn_raw_buffer_load_b128(rc, off + u * R::kAtOnce * row_bytes, 0, 0));
+        }
 #pragma unroll
-            for (int i = 0; i < Cfg::MT; ++i)
-                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, old[i] + acc[i][j]), rc,
-                                                       off + 16 * i * kEl, 0, WG_AUX);
-        } else if constexpr (OUT == kDtypeF32) {
+        for (int u = 0; u < kN; ++u) v[u] = *reinterpret_cast<const u32x4*>(from + u * R::kAtOnce * R::kPitch);
 #pragma unroll
-            for (int i = 0; i < Cfg::MT; ++i)
-                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[i][j]), rc, off + 16 * i * kEl, 0,
-                                                       WG_AUX);
-        } else {
-            typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-#pragma unroll
-            for (int i = 0; i < Cfg::MT; ++i) {
-                const u32x2 h = {pack_bf16(acc[i][j][0], acc[i][j][1]), pack_bf16(acc[i][j][2], acc[i][j][3])};
-                __builtin_amdgcn_raw_buffer_store_b64(h, rc, off + 16 * i * kEl, 0, WG_AUX);
-            }
+        for (int u = 0; u < kN; ++u) {
+            if constexpr (ACC) v[u] = __builtin_bit_cast(u32x4, old[u] + __builtin_bit_cast(v4f, v[u]));
+            __builtin_amdgcn_raw_buffer_store_b128(v[u], rc, off + u * R::kAtOnce * row_bytes, 0, kStreaming);
         }
         off += 16 * row_bytes;
     }
 #endif
+}
+
+// The same for a tile at dW's last columns, or rows that do not lie on 16
+// bytes: 64 consecutive elements of a row by one instruction.  (Elements
+// stored from the accumulators, 16 rows by one instruction: 16 experts of
+// 333x1111 in bf16 27 us.)
+template <class Cfg, int OUT, bool ACC>
+__device__ __forceinline__ void store_elements(const v4f (&acc)[Cfg::MT][Cfg::NT], void* c, int64_t ldc, int m0, int n0,
+                                               int M, int N, int wm, int wn, int lane, uint8_t* region) {
+    using R = Rows<Cfg, OUT>;
+    using T = typename std::conditional<OUT == kDtypeF32, float, uint16_t>::type;
+    constexpr int kRows = 4;  // rows under way at once
+    const int k0 = m0 + wm * Cfg::TM + lane;
+#pragma unroll
+    for (int j = 0; j < Cfg::NT; ++j) {
+        stage_rows<Cfg, OUT>(acc, j, region, lane);
+        const int nj = n0 + wn * Cfg::TN + 16 * j;
+#pragma unroll 1
+        for (int r0 = 0; r0 < 16 && nj + r0 < N; r0 += kRows) {
+            T* const row = static_cast<T*>(c) + (int64_t)(nj + r0) * ldc + k0;
+            const uint8_t* from = region + r0 * R::kPitch + lane * R::kEl;
+            const int rows = N - nj - r0;
+#pragma unroll
+            for (int h = 0; h < Cfg::TM / 64; ++h) {
+                if (k0 + 64 * h >= M) continue;
+                T v[kRows];
+                T old[kRows];
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    v[r] = *reinterpret_cast<const T*>(from + r * R::kPitch + 64 * h * R::kEl);
+                    old[r] = ACC && r < rows ? row[r * ldc + 64 * h] : T(0);
+                }
+#pragma unroll
+                for (int r = 0; r < kRows; ++r)
+                    if (r < rows) row[r * ldc + 64 * h] = ACC ? T(old[r] + v[r]) : v[r];
+            }
+        }
+    }
 }
 
 // This lane's number, formed where it stands: what is derived from it is then
@@ -307,107 +348,188 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grouped_wgrad_kernel(WgradPar
     if (!job.c) return;
     Source src = source_of(job);
     int stage = 0;
-    bool behind = false;  // Cfg::MT * Cfg::NT stores were issued after the last copies
+    bool behind = false;  // at least Rows::kStores stores were issued after the last copies
     {
         const Copies<Cfg, BM> copies(p, wave);
 #pragma unroll
         for (int it = 0; it < Cfg::kLoadsPerWave; ++it) copies.issue(lds, src, p, job.kb, wave, it);
     }
+    // Waits for the copies of the chunk that comes next.  Memory operations
+    // complete in order: a job's first chunk was copied before the last job's
+    // stores, which go on under it.
+    auto arrive = [&]() __attribute__((always_inline)) {
+        if (behind) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(Rows<Cfg, OUT>::kStores) : "memory");
+        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        behind = false;
+        lds_barrier();  // (__syncthreads would wait for the stores)
+    };
+    constexpr int kRegion = Cfg::kStageBytes / Cfg::kWaves & ~15;
     for (;;) {
         v4f acc[Cfg::MT][Cfg::NT];
 #pragma unroll
         for (int i = 0; i < Cfg::MT; ++i)
 #pragma unroll
             for (int j = 0; j < Cfg::NT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-        Job<BM, BN> next = job;
-        for (int kb = job.kb; kb < job.kb1; ++kb) {
-            // memory operations complete in order: a job's first chunk was
-            // copied before the last job's stores, which go on under it
-            if (behind) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(Cfg::MT * Cfg::NT) : "memory");
-            else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            behind = false;
-            __syncthreads();
-            // under this chunk's products the next one of this job is copied,
-            // or the first one of the next job (after the last of all, this
-            // one again, into the stage that is not read any more)
-            int kb_next = kb + 1;
-            if (kb_next == job.kb1) {
-                in += nwg;
-                next = next_job();
-                kb_next = kb;
-                if (next.c) {
-                    src = source_of(next);
-                    kb_next = next.kb;
-                }
-            }
+        in += nwg;
+        const Job<BM, BN> next = next_job();
+        // under a chunk's products the next one of this job is copied, or the
+        // first one of the next job (after the last of all, this one again,
+        // into the stage that is not read any more)
+        auto next_chunk = [&](int kb) __attribute__((always_inline)) {
+            if (kb + 1 < job.kb1) return kb + 1;
+            if (!next.c) return kb;
+            src = source_of(next);
+            return next.kb;
+        };
+        const bool inside = (job.partial || p.vec) && job.m0 + BM <= p.M;
+        const uint32_t el = job.partial ? 4 : kEl, row_bytes = (uint32_t)job.ldc * el;
+        const int rows = p.N - job.n0 < BN ? p.N - job.n0 : BN;
+        const __amdgpu_buffer_rsrc_t rc =
+            make_rsrc(static_cast<uint8_t*>(job.c) + job.n0 * (int64_t)row_bytes + (int64_t)job.m0 * el,
+                      (int64_t)(rows - 1) * row_bytes + BM * el);
+        int kb = job.kb;
+        for (; kb < job.kb1; ++kb) {
+            arrive();
+            const int kb_next = next_chunk(kb);
             chunk_step<Cfg, BM, MMA>(lds + stage * Cfg::kStageBytes, lds + (stage ^ 1) * Cfg::kStageBytes, src, p, kb_next,
                                      acc, wave, wm, wn, lane_now());
             stage ^= 1;
         }
         const int ln = lane_now();
-        if (p.vec && job.m0 + BM <= p.M) {
-            const uint32_t row_bytes = (uint32_t)job.ldc * (job.partial ? 4 : kEl);
-            const int64_t rows = p.N - job.n0 < BN ? p.N - job.n0 : BN;
-            const __amdgpu_buffer_rsrc_t rc =
-                make_rsrc(static_cast<uint8_t*>(job.c) + job.n0 * (int64_t)row_bytes + (int64_t)job.m0 * (job.partial ? 4 : kEl),
-                          (rows - 1) * row_bytes + BM * (job.partial ? 4 : kEl));
-            if (job.partial)
-                store_tile_buffer<Cfg, kDtypeF32, false>(acc, rc, row_bytes, wm, wn, ln);
-            else
-                store_tile_buffer<Cfg, OUT, ACC>(acc, rc, row_bytes, wm, wn, ln);
+        __builtin_amdgcn_s_barrier();  // every wave is done with the stage just read
+        uint8_t* region = lds + (stage ^ 1) * Cfg::kStageBytes + wave * kRegion;
+        if (inside) {
+            if (job.partial) store_rows<Cfg, kDtypeF32, false>(acc, rc, row_bytes, wm, wn, ln, region);
+            else store_rows<Cfg, OUT, ACC>(acc, rc, row_bytes, wm, wn, ln, region);
             behind = true;
         } else if (job.partial) {
-            store_transposed<Cfg, kDtypeF32, false>(acc, job.c, job.ldc, job.m0, job.n0, p.M, p.N, wm, wn, ln, true);
+            store_elements<Cfg, kDtypeF32, false>(acc, job.c, job.ldc, job.m0, job.n0, p.M, p.N, wm, wn, ln, region);
         } else {
-            store_transposed<Cfg, OUT, ACC>(acc, job.c, job.ldc, job.m0, job.n0, p.M, p.N, wm, wn, ln, p.vec);
+            store_elements<Cfg, OUT, ACC>(acc, job.c, job.ldc, job.m0, job.n0, p.M, p.N, wm, wn, ln, region);
         }
         if (!next.c) break;
         job = next;
     }
 }
 
-#ifdef WG_SMALL
-#define WG_CFG 128, 128, 2, 2
-constexpr int kTile = 128, kWg = 2, kThr = 256;
-#else
-#define WG_CFG 256, 256, 2, 4
-constexpr int kTile = 256, kWg = 1, kThr = 512;
+// dW of the groups that were split: the sum of their slices, in order.  Each
+// thread owns four consecutive k of a row.
+template <int OUT, bool ACC>
+__global__ __launch_bounds__(256) void wgrad_join_kernel(WgradParams p) {
+    const int g = blockIdx.y, lane = threadIdx.x & 63;
+    int mine = 0, before = 0, count = 0;
+    for_groups_of_lane(p.offsets, p.groups, p.rows, lane, [&](int h, int lo, int hi) {
+        const int sl = split_slices((hi - lo + 127) >> 7, p.slice);
+        if (h < g) before += sl;
+        if (h == g) count = sl;
+        mine += sl;
+    });
+    const int per = (p.groups + 63) / 64;
+    before += wave_scan_sum(mine) - mine;  // of the lanes below
+    count = __builtin_amdgcn_readlane(count, g / per);
+    before = __builtin_amdgcn_readlane(before, g / per);
+    if (count == 0) return;
+    const int64_t quads = (p.M + 3) / 4, total = p.N * quads, stride = p.N * p.ldws;
+    constexpr int kEl = OUT == kDtypeF32 ? 4 : 2;
+    const float* first = p.ws + before * stride;
+    uint8_t* c = static_cast<uint8_t*>(p.c) + g * p.c_group_stride * kEl;
+    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
+        const int64_t n = e / quads;
+        const int k = 4 * (int)(e - n * quads);
+        const float* q = first + n * p.ldws + k;
+        v4f sum = *reinterpret_cast<const v4f*>(q);
+        for (int sl = 1; sl < count; ++sl) sum += *reinterpret_cast<const v4f*>(q + sl * stride);
+        store4<OUT, ACC>(c + n * p.ldc * kEl, k, p.M - k > 4 ? 4 : p.M - k, sum, p.vec);
+    }
+}
+
+// 256x256 tiles, one work-group of 8 waves a compute unit, or 128x128 tiles,
+// two work-groups of 4 waves; and the chunks of a slice (INT32_MAX: no split).
+struct WgradPlan {
+    bool large;
+    int slice;
+    int64_t ldws, bytes;
+};
+
+#ifndef MIN_SLICE
+#define MIN_SLICE 4
 #endif
+constexpr int kMinSlice = MIN_SLICE;
+
+WgradPlan plan_wgrad(int64_t rows, int64_t G, int64_t N, int64_t K) {
+    const int64_t cus = compute_units(), groups = G < rows ? G : rows;
+    const int64_t large = ((N + 255) / 256) * ((K + 255) / 256) * groups;
+    WgradPlan plan{true, INT32_MAX, 0, 0};
+    // share of the rounds of large tiles that is gradient, in percent
+    const int64_t rounds = (large + cus - 1) / cus;
+    if (rounds == 0 || 100 * groups * N * K >= 75 * rounds * cus * 65536) return plan;
+    plan.large = false;
+    const int64_t tiles = ((N + 127) / 128) * ((K + 127) / 128), slots = 2 * cus;
+    const int64_t chunks = rows / 128 + (groups + 1) / 2;  // about as many
+    int64_t slice = (chunks * tiles + slots - 1) / slots;
+    slice = slice < kMinSlice ? kMinSlice : slice;
+    const int64_t all = group_chunks(rows, G), most = (rows + 127) / 128;
+    plan.ldws = (K + 3) / 4 * 4;
+    if (most <= slice || plan.ldws * 4 >= (int64_t(1) << 24)) return plan;
+    plan.slice = (int)slice;
+    const int64_t split = all / (slice + 1);  // groups of more chunks than a slice
+    plan.bytes = (all + split * (slice - 1)) / slice * N * plan.ldws * 4;
+    return plan;
+}
+
+template <int OUT, bool ACC, int MMA>
+void launch_wgrad_typed(const WgradParams& p, const WgradPlan& plan, int64_t grid, hipStream_t st) {
+    const dim3 gr((unsigned)grid);
+    if (plan.large)
+        hipLaunchKernelGGL((grouped_wgrad_kernel<256, 256, 2, 4, OUT, ACC, MMA>), gr, dim3(512), 0, st, p);
+    else
+        hipLaunchKernelGGL((grouped_wgrad_kernel<128, 128, 2, 2, OUT, ACC, MMA>), gr, dim3(256), 0, st, p);
+    if (plan.slice == INT32_MAX) return;
+    const int64_t quads = (int64_t)p.N * ((p.M + 3) / 4);
+    const int64_t blocks = (quads + 255) / 256;
+    hipLaunchKernelGGL((wgrad_join_kernel<OUT, ACC>), dim3((unsigned)(blocks < 1024 ? blocks : 1024), p.groups), dim3(256),
+                       0, st, p);
+}
 
 template <int MMA>
-void launch_wgrad_mma(const GemmArgs& g, const WgradParams& p, int64_t grid, hipStream_t st) {
-    const dim3 gr((unsigned)grid), bl(kThr);
-    if (g.c_dtype == kDtypeBF16)
-        hipLaunchKernelGGL((grouped_wgrad_kernel<WG_CFG, kDtypeBF16, false, MMA>), gr, bl, 0, st, p);
-    else if (g.accumulate)
-        hipLaunchKernelGGL((grouped_wgrad_kernel<WG_CFG, kDtypeF32, true, MMA>), gr, bl, 0, st, p);
-    else
-        hipLaunchKernelGGL((grouped_wgrad_kernel<WG_CFG, kDtypeF32, false, MMA>), gr, bl, 0, st, p);
+void launch_wgrad_mma(const GemmArgs& g, const WgradParams& p, const WgradPlan& plan, int64_t grid, hipStream_t st) {
+    if (g.c_dtype == kDtypeBF16) launch_wgrad_typed<kDtypeBF16, false, MMA>(p, plan, grid, st);
+    else if (g.accumulate) launch_wgrad_typed<kDtypeF32, true, MMA>(p, plan, grid, st);
+    else launch_wgrad_typed<kDtypeF32, false, MMA>(p, plan, grid, st);
 }
 
 }  // namespace
 
-int64_t grouped_wgrad_bytes(int64_t, int, int64_t, int64_t) { return 0; }
+int64_t grouped_wgrad_bytes(int64_t rows, int groups, int64_t M, int64_t N) {
+    return plan_wgrad(rows, groups, M, N).bytes;
+}
 
 hipError_t launch_grouped_wgrad(const GemmArgs& g, int64_t c_group_stride, hipStream_t st) {
+    const WgradPlan plan = plan_wgrad(g.K, g.groups, g.M, g.N);
     WgradParams p{};
     p.a = g.b; p.lda = (int)g.ldb; p.sa = g.sb; p.ldsa = g.ldsb;
     p.b = g.a; p.ldb = (int)g.lda; p.sb = g.sa; p.ldsb = g.ldsa;
     p.offsets = g.offsets; p.groups = g.groups; p.rows = (int)g.K;
     p.M = (int)g.N; p.N = (int)g.M; p.c = g.c; p.ldc = g.ldc; p.c_group_stride = c_group_stride;
-    p.tiles_m = (p.M + kTile - 1) / kTile;
-    p.tiles_n = (p.N + kTile - 1) / kTile;
+    const int tile = plan.large ? 256 : 128;
+    p.tiles_m = (p.M + tile - 1) / tile;
+    p.tiles_n = (p.N + tile - 1) / tile;
     const int64_t el = g.c_dtype == kDtypeF32 ? 4 : 2;
     p.vec = reinterpret_cast<uintptr_t>(g.c) % 16 == 0 && g.ldc * el % 16 == 0 && c_group_stride * el % 16 == 0 &&
             g.ldc * el < (int64_t(1) << 24);  // 256 rows within 32-bit offsets
-    p.slice = INT32_MAX;
-    const int64_t work = (int64_t)p.tiles_m * p.tiles_n * g.groups, cus = kWg * compute_units();
-    const int64_t grid = work < cus ? work : cus;
+    p.slice = plan.slice;
+    p.ws = static_cast<float*>(g.workspace);
+    p.ldws = plan.ldws;
+    // work-groups: as many as there are jobs, or as fit at once
+    const int64_t split = plan.slice == INT32_MAX ? 0 : group_chunks(g.K, g.groups) / plan.slice;
+    const int64_t jobs = (int64_t)p.tiles_m * p.tiles_n * (g.groups + split);
+    const int64_t slots = (plan.large ? 1 : 2) * (int64_t)compute_units();
+    const int64_t grid = jobs < slots ? jobs : slots;
     switch (g.mma) {
-        case kMmaFp8: launch_wgrad_mma<kMmaFp8>(g, p, grid, st); break;
-        case kMmaBf16Fold: launch_wgrad_mma<kMmaBf16Fold>(g, p, grid, st); break;
-        case kMmaFp8Scaled: launch_wgrad_mma<kMmaFp8Scaled>(g, p, grid, st); break;
-        default: launch_wgrad_mma<kMmaF16>(g, p, grid, st); break;
+        case kMmaFp8: launch_wgrad_mma<kMmaFp8>(g, p, plan, grid, st); break;
+        case kMmaBf16Fold: launch_wgrad_mma<kMmaBf16Fold>(g, p, plan, grid, st); break;
+        case kMmaFp8Scaled: launch_wgrad_mma<kMmaFp8Scaled>(g, p, plan, grid, st); break;
+        default: launch_wgrad_mma<kMmaF16>(g, p, plan, grid, st); break;
     }
     return hipGetLastError();
 }
