@@ -78,17 +78,36 @@ __device__ __forceinline__ Step step_of(const StepArgs& a) {
 }
 
 // y >= 0 (up to 448 and its rounding error) on the E4M3 grid, `unit` = 2^k the
-// grid's step at y: unit * floor(fl32(y / unit + u)), at most 448.
-__device__ __forceinline__ float round_up_by(float y, float u) {
+// grid's step at y: unit * floor(fl32(y / unit + u)), at most 448, with u =
+// (r + 1/2) / 2^16 of a 16-bit number r.
+__device__ __forceinline__ float round_up_by(float y, uint32_t r) {
     const int k = max(__builtin_amdgcn_frexp_expf(y), -5) - 4;  // y in [2^(k+3), 2^(k+4)), or below 2^-6 with k = -9
-    const float t = __builtin_amdgcn_ldexpf(y, -k) + u;
+    const float t = __builtin_amdgcn_ldexpf(y, -k) + __builtin_fmaf((float)r, 0x1p-16f, 0x1p-17f);
     return fminf(__builtin_amdgcn_ldexpf(__builtin_floorf(t), k), kE4M3Max);
 }
 
-// (r + 1/2) / 2^16 of a 16-bit number, exact.
-__device__ __forceinline__ float fraction_16(uint32_t r) { return __builtin_fmaf((float)r, 0x1p-16f, 0x1p-17f); }
+// The same for y = 0 or y >= 2^-6, four instructions instead of eleven: there
+// y / unit lies in [8, 16) with 20 bits behind the point, the last 20 of y's, so
+// adding u to them carries into the four bits that stay.  (Where the sum
+// reaches 16 it may be rounded up to 17 units of y; the grid's step is two there
+// and the code is that of 16 either way.)
+__device__ __forceinline__ float round_normal_up_by(float y, uint32_t r20) {
+    return fminf(__uint_as_float((__float_as_uint(y) + r20) & 0xfff00000u), kE4M3Max);
+}
 
-// A tensor as the kernels see it: 64 bytes, and 112 with codes.
+// Square root rounded to nearest of v in [2^-90, 2^90]: the reciprocal root
+// (within an ulp), one step for the root and for half its reciprocal, and the
+// root's remainder.  11 issue slots; sqrtf, which takes any v, has 19.
+__device__ __forceinline__ float sqrt_in_range(float v) {
+    const float y = __builtin_amdgcn_rsqf(v);
+    float s = v * y, h = 0.5f * y;
+    const float e = __builtin_fmaf(-h, s, 0.5f);
+    h = __builtin_fmaf(h, e, h);
+    s = __builtin_fmaf(s, e, s);
+    return __builtin_fmaf(__builtin_fmaf(-s, s, v), h, s);
+}
+
+// A tensor as the kernels see it: 64 bytes, and 120 with codes.
 struct FlatTensor {
     float* p;
     const void* g;
@@ -106,6 +125,7 @@ struct CodedTensor : FlatTensor {
     uint8_t* qt;  // nullptr: no transposed codes
     float* st;
     int64_t N, K;  // n / (N K) matrices
+    uint32_t units;
 };
 
 // Scale of a tile of moments: fl32(amax * fl32(1 / 448)).
@@ -140,7 +160,7 @@ struct Eight {
     __device__ __forceinline__ void load(const FlatTensor& t, int64_t e, int64_t valid) {
         if (valid >= 8) {
             p.template load_full<false>(t.p + e);
-            g.template load_full<true>(static_cast<const GT*>(t.g) + e);
+            g.template load_full<sizeof(GT) == 2>(static_cast<const GT*>(t.g) + e);
             if constexpr (BITS == 32) {
                 mo.m.template load_full<false>(static_cast<const float*>(t.m) + e);
                 mo.v.template load_full<false>(static_cast<const float*>(t.v) + e);
@@ -207,31 +227,32 @@ struct Eight {
                 v[i] *= v[i];
             }
         }
-        float r[8], d[8];
+        float r[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float x = gr[i] * s.grad;
             m[i] = m[i] * s.beta1 + x * s.rest1;
             v[i] = v[i] * s.beta2 + x * x * s.rest2;
-            r[i] = sqrtf(v[i]);
-            d[i] = r[i] * s.root + s.eps;
         }
-        // m / d: the hardware's reciprocal with one correction by the remainder
-        // (within an ulp) where every denominator of the wave is far from the
-        // ends of the range, else the full division (10 instructions, not 4).
-        float least = d[0], most = d[0];
+        // Where every second moment of the wave is far from the ends of the
+        // range the root takes fewer instructions, and the hardware's
+        // reciprocal (within an ulp) serves for the quotient.
+        float least = v[0], most = v[0];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) least = fminf(least, d[i]), most = fmaxf(most, d[i]);
-        if (wave_all(least >= 0x1p-100f && most <= 0x1p100f)) {
+        for (int i = 1; i < 8; ++i) least = fminf(least, v[i]), most = fmaxf(most, v[i]);
+        if (wave_all(least >= 0x1p-90f && most <= 0x1p90f) && s.eps <= 0x1p90f) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float rc = __builtin_amdgcn_rcpf(d[i]);
-                const float q = m[i] * rc;
-                out[i] = __builtin_fmaf(-s.rate, __builtin_fmaf(__builtin_fmaf(-q, d[i], m[i]), rc, q), out[i] * s.keep);
+                r[i] = sqrt_in_range(v[i]);
+                const float d = r[i] * s.root + s.eps;
+                out[i] = __builtin_fmaf(-s.rate, m[i] * __builtin_amdgcn_rcpf(d), out[i] * s.keep);
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) out[i] = __builtin_fmaf(-s.rate, m[i] / d[i], out[i] * s.keep);
+            for (int i = 0; i < 8; ++i) {
+                r[i] = sqrtf(v[i]);
+                out[i] = __builtin_fmaf(-s.rate, m[i] / (r[i] * s.root + s.eps), out[i] * s.keep);
+            }
         }
         store_values8(t.p, e, e + valid, out);
         if constexpr (BITS == 32) {
@@ -254,12 +275,25 @@ struct Eight {
                     cv[i] = quotient(r[i], tv);
                 }
             }
+            // any value with 0 < y < 2^-6?  (a zero becomes the largest number here)
+            uint32_t low = 0xffffffffu;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                low = min(low, min(__float_as_uint(cm[i]) - 1u, __float_as_uint(cv[i]) - 1u));
+            // (2^-6 in bits, less one; and no quotient of a positive root that is zero)
+            const bool normal = wave_all(low >= 0x3c7fffffu && tv.s <= 0x1p60f);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const uint32_t h = mix32((uint32_t)(e + i) ^ key);
-                cm[i] = __builtin_copysignf(round_up_by(cm[i], fraction_16(h & 0xffffu)), m[i]);
-                const float c = round_up_by(cv[i], fraction_16(h >> 16));
-                cv[i] = r[i] > 0.0f ? fmaxf(c, 0x1p-9f) : c;
+                if (normal) {
+                    cm[i] = round_normal_up_by(cm[i], (h << 4 & 0xffff0u) | 8u);
+                    cv[i] = round_normal_up_by(cv[i], (h >> 12 & 0xffff0u) | 8u);
+                } else {
+                    cm[i] = round_up_by(cm[i], h & 0xffffu);
+                    cv[i] = round_up_by(cv[i], h >> 16);
+                    cv[i] = r[i] > 0.0f ? fmaxf(cv[i], 0x1p-9f) : cv[i];
+                }
+                cm[i] = __builtin_copysignf(cm[i], m[i]);
             }
             uint32_t a = cvt2_in_range<false>(cm[0], cm[1], 0), b = cvt2_in_range<false>(cm[4], cm[5], 0);
             a = cvt2_in_range<true>(cm[2], cm[3], a);
@@ -286,7 +320,7 @@ struct Batch {
     int pow2;
 };
 using FlatBatch = Batch<FlatTensor, 60>;
-using CodedBatch = Batch<CodedTensor, 34>;
+using CodedBatch = Batch<CodedTensor, 33>;
 static_assert(sizeof(FlatBatch) <= 4096 && sizeof(CodedBatch) <= 4096, "kernel arguments");
 
 // Work unit u of the launch belongs to the last tensor whose first unit is <= u.
@@ -318,6 +352,16 @@ __global__ __launch_bounds__(kFlatThreads) void adamw_flat_kernel(FlatBatch b) {
 
 // A 128x128 block of a weight: the step, then the block's codes from the new
 // values in registers, and their transpose through LDS.
+// Work-groups go to the eight XCDs in turn.  Where rows are wide (from 2048
+// columns) each XCD takes a contiguous run of a tensor's blocks, so that the
+// blocks it works on at a time lie in few bands of rows (16 experts 2048x7168
+// with 8-bit moments 901 -> 854 us); in narrow tensors the blocks at a time
+// are contiguous memory as they are (56 experts 2048x1024: 620 us, 664 so).
+__device__ __forceinline__ uint32_t unit_of(uint32_t id, uint32_t units) {
+    const uint32_t xcd = id & 7, per = units >> 3, more = units & 7;
+    return xcd * per + (xcd < more ? xcd : more) + (id >> 3);
+}
+
 template <typename GT, int BITS>
 __global__ __launch_bounds__(512, 4) void adamw_codes_kernel(CodedBatch b) {
     __shared__ uint32_t s_max[8];
@@ -328,6 +372,7 @@ __global__ __launch_bounds__(512, 4) void adamw_codes_kernel(CodedBatch b) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const uint32_t kb = (uint32_t)(t.K >> 7), nb = (uint32_t)((t.N + 127) >> 7);
     uint32_t u = blockIdx.x - t.first;
+    if (t.K >= 2048) u = unit_of(u, t.units);
     const uint32_t bj = u % kb;
     u /= kb;
     const uint32_t bi = u % nb, mat = u / nb;
@@ -450,7 +495,8 @@ void launch_typed(const fp8q_adamw_tensor* tensors, int count, const StepArgs& s
             continue;
         }
         t.q = a.q; t.s = a.s; t.qt = a.qt; t.st = a.st; t.N = a.N; t.K = a.K;
-        coded.add(t, a.n / (a.N * a.K) * ((a.N + 127) / 128) * (a.K / 128));
+        t.units = (uint32_t)(a.n / (a.N * a.K) * ((a.N + 127) / 128) * (a.K / 128));
+        coded.add(t, t.units);
     }
     coded.send();
     flat.send();

@@ -78,22 +78,34 @@ struct GroupChunk {
 // The rows of chunk c, the same in every lane of the wave.
 __device__ __forceinline__ GroupChunk find_chunk(const int32_t* __restrict__ off, int G, int M, int c) {
     const int lane = threadIdx.x & 63;
-    int mine = 0;
-    for_groups_of_lane(off, G, M, lane, [&](int, int lo, int hi) { mine += (hi - lo + 127) >> 7; });
-    const int end = wave_scan_sum(mine);
-    const int start = end - mine;
-    const uint64_t holds = __ballot(c >= start && c < end);
     GroupChunk r;
-    r.live = holds != 0;
-    int at = start, row0 = 0, row_end = 0;
-    for_groups_of_lane(off, G, M, lane, [&](int, int lo, int hi) {
+    int row0 = 0, row_end = 0, start, end;
+    if (G <= 64) {  // a group a lane
+        int lo = clamp_offset(off[lane < G ? lane : G], M);
+        const int hi = wave_scan_max(max(lo, clamp_offset(off[lane < G ? lane + 1 : G], M)));
+        lo = max(lo, from_lane_below(hi));
         const int n = (hi - lo + 127) >> 7;
-        if (c >= at && c < at + n) {
-            row0 = lo + 128 * (c - at);
-            row_end = hi;
-        }
-        at += n;
-    });
+        end = wave_scan_sum(n);
+        start = end - n;
+        row0 = lo + 128 * (c - start);
+        row_end = hi;
+    } else {
+        int mine = 0;
+        for_groups_of_lane(off, G, M, lane, [&](int, int lo, int hi) { mine += (hi - lo + 127) >> 7; });
+        end = wave_scan_sum(mine);
+        start = end - mine;
+        int at = start;
+        for_groups_of_lane(off, G, M, lane, [&](int, int lo, int hi) {
+            const int n = (hi - lo + 127) >> 7;
+            if (c >= at && c < at + n) {
+                row0 = lo + 128 * (c - at);
+                row_end = hi;
+            }
+            at += n;
+        });
+    }
+    const uint64_t holds = __ballot(c >= start && c < end);
+    r.live = holds != 0;
     const int src = r.live ? __builtin_ctzll(holds) : 0;
     r.row0 = __builtin_amdgcn_readlane(row0, src);
     r.row_end = __builtin_amdgcn_readlane(row_end, src);

@@ -277,6 +277,29 @@ __global__ __launch_bounds__(512) void quantize_128x1_kernel(
                 raw[i].load_full(static_cast<const T*>(src) + r * ldx + cbase);
             }
         }
+    } else if (GROUPED && c0 + 128 <= cols) {
+        // a group's last chunk: rows past it are read as its last row, so that
+        // the loads still go out back to back, and then are zeros
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int64_t r = min(r0 + kRows * rg + i, rows - 1);
+            if constexpr (KIND == SRC_FP8) {
+                codes[i] = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(src) + r * ldx + cbase);
+                rs[i] = s_in[(c0 >> 7) * lds_in + r];
+            } else {
+                raw[i].load_full(static_cast<const T*>(src) + r * ldx + cbase);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            if (r0 + kRows * rg + i < rows) continue;
+            if constexpr (KIND == SRC_FP8) {
+                codes[i] = make_uint2(0, 0);
+                rs[i] = 0.0f;
+            } else {
+                raw[i].zero();
+            }
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {

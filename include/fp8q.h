@@ -590,7 +590,7 @@ int fp8q_grouped_wgrad(const uint8_t *a, int64_t lda, const float *sa, int64_t l
  * st NULL: none).  All arrays are dense.
  *
  * `tensors` and `config` are HOST arrays, read before the call returns; a
- * launch takes 60 tensors without codes, or 34 with.  Arrays of different tensors may not
+ * launch takes 60 tensors without codes, or 33 with.  Arrays of different tensors may not
  * overlap.  p, g, m, v, q and qt are 16-byte aligned, sm, sv, s and st 4-byte.
  * n == 0 is an empty tensor; n <= 2^33, and at most 2^22 blocks of 128x128 of a
  * tensor with codes (else FP8Q_EUNSUPPORTED).
