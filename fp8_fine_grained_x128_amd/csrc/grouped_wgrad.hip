@@ -130,27 +130,31 @@ __device__ __forceinline__ void store_rows(const v4f (&acc)[Cfg::MT][Cfg::NT], _
 #if defined(__HIP_DEVICE_COMPILE__)
     using R = Rows<Cfg, OUT>;
     const uint8_t* from = region + lane / R::kUnits * R::kPitch + lane % R::kUnits * 16;
-    uint32_t off = (wn * Cfg::TN + lane / R::kUnits) * row_bytes + wm * R::kBytes + lane % R::kUnits * 16;
-#pragma unroll
-    for (int j = 0; j < Cfg::NT; ++j) {
-        stage_rows<Cfg, OUT>(acc, j, region, lane);
-        constexpr int kN = 16 / R::kAtOnce;
-        u32x4 v[kN];
-        v4f old[ACC ? kN : 1];
+    const uint32_t off = (wn * Cfg::TN + lane / R::kUnits) * row_bytes + wm * R::kBytes + lane % R::kUnits * 16;
+    constexpr int kN = 16 / R::kAtOnce;
+    // the values to add to are read one pass ahead
+    v4f old[2][ACC ? kN : 1];
+    auto read_old = [&](int j) __attribute__((always_inline)) {
         if constexpr (ACC) {
 #pragma unroll
             for (int u = 0; u < kN; ++u)
-                old[u] = __builtin_bit_cast(
-                    v4f, __builtin_amdgcn_raw_buffer_load_b128(rc, off + u * R::kAtOnce * row_bytes, 0, 0));
+                old[j & 1][u] = __builtin_bit_cast(
+                    v4f, __builtin_amdgcn_raw_buffer_load_b128(rc, off + (16 * j + u * R::kAtOnce) * row_bytes, 0, 0));
         }
+    };
+    read_old(0);
+#pragma unroll
+    for (int j = 0; j < Cfg::NT; ++j) {
+        if (j + 1 < Cfg::NT) read_old(j + 1);
+        stage_rows<Cfg, OUT>(acc, j, region, lane);
+        u32x4 v[kN];
 #pragma unroll
         for (int u = 0; u < kN; ++u) v[u] = *reinterpret_cast<const u32x4*>(from + u * R::kAtOnce * R::kPitch);
 #pragma unroll
         for (int u = 0; u < kN; ++u) {
-            if constexpr (ACC) v[u] = __builtin_bit_cast(u32x4, old[u] + __builtin_bit_cast(v4f, v[u]));
-            __builtin_amdgcn_raw_buffer_store_b128(v[u], rc, off + u * R::kAtOnce * row_bytes, 0, kStreaming);
+            if constexpr (ACC) v[u] = __builtin_bit_cast(u32x4, old[j & 1][u] + __builtin_bit_cast(v4f, v[u]));
+            __builtin_amdgcn_raw_buffer_store_b128(v[u], rc, off + (16 * j + u * R::kAtOnce) * row_bytes, 0, kStreaming);
         }
-        off += 16 * row_bytes;
     }
 #endif
 }
