@@ -865,9 +865,12 @@ def moe_decode(x: torch.Tensor, logits: torch.Tensor, w_gu: torch.Tensor, s_gu: 
 
 def _on_current_device(what: str, *ts: torch.Tensor) -> None:
     """Every tensor on torch's current HIP device, whose current stream the call goes to."""
-    _on_device(what, *ts)
-    if ts and ts[0].device.index != torch.cuda.current_device():
-        raise ValueError(f"{what}: tensors on {ts[0].device}, the current device is cuda:{torch.cuda.current_device()}")
+    now = torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+    for t in ts:
+        if not t.is_cuda:
+            raise ValueError(f"{what}: tensors must be on a HIP device")
+        if t.get_device() != now:
+            raise ValueError(f"{what}: a tensor on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
 
 
 def _check_offsets(what: str, offsets: torch.Tensor) -> int:
@@ -935,26 +938,33 @@ def grouped_wgrad(dy: GroupedOperand, x: GroupedOperand, offsets: torch.Tensor,
     N, K = qa.shape[0], qb.shape[0]
     padded = _lib.fp8q_grouped_padded_rows(rows, G)
     for name, q, s in (("dy", qa, sa), ("x", qb, sb)):
-        _check_codes(f"grouped_wgrad {name}", q)
+        if q.dtype != torch.uint8:
+            _check_codes(f"grouped_wgrad {name}", q)
         if q.shape[1] < padded:
             raise ValueError(f"grouped_wgrad: {name} has {q.shape[1]} tokens, {G} groups of {rows} rows take up to {padded}")
         _check_scales(f"grouped_wgrad {name} (layout [chunks][channels])", s, padded // 128, q.shape[0])
     if accumulate and dw is None:
         raise ValueError("grouped_wgrad: accumulate needs the gradient to add to")
+    dev = qa.device
     if dw is None:
-        dw = torch.empty((G, N, K), dtype=out_dtype, device=qa.device)
-    elif dw.shape != (G, N, K) or (K > 1 and dw.stride(2) != 1):
-        raise ValueError(f"grouped_wgrad: dw is {tuple(dw.shape)}, expected [{G}][{N}][{K}] with unit inner stride")
-    _on_current_device("grouped_wgrad", qa, sa, qb, sb, offsets, dw)
-    lddw = dw.stride(1) if N > 1 else max(K, 1)  # axes of one element may carry any stride
+        dw = torch.empty((G, N, K), dtype=out_dtype, device=dev)
+        _on_current_device("grouped_wgrad", qa, sa, qb, sb, offsets)
+    else:
+        if dw.shape != (G, N, K) or (K > 1 and dw.stride(2) != 1):
+            raise ValueError(f"grouped_wgrad: dw is {tuple(dw.shape)}, expected [{G}][{N}][{K}] with unit inner stride")
+        _on_current_device("grouped_wgrad", qa, sa, qb, sb, offsets, dw)
+    sg, lddw, _ = dw.stride()
+    if N <= 1 or G <= 1:  # axes of one element may carry any stride
+        lddw = lddw if N > 1 else max(K, 1)
+        sg = sg if G > 1 else N * lddw
     need = _lib.fp8q_grouped_wgrad_workspace(rows, G, N, K)
-    ws, base = _workspace(need, qa.device)
+    ws, base = _workspace(need, dev)
     _check(_lib.fp8q_grouped_wgrad(qa.data_ptr(), _ld(qa) if N > 1 else max(qa.shape[1], 16), sa.data_ptr(),
                                    sa.stride(0) if sa.shape[0] > 1 else max(N, 1), qb.data_ptr(),
                                    _ld(qb) if K > 1 else max(qb.shape[1], 16), sb.data_ptr(),
                                    sb.stride(0) if sb.shape[0] > 1 else max(K, 1), offsets.data_ptr(), G, rows, N, K,
-                                   dw.data_ptr(), _dtype_code(dw), lddw, dw.stride(0) if G > 1 else N * lddw,
-                                   1 if accumulate else 0, flags, base, need, _stream()),
+                                   dw.data_ptr(), _dtype_code(dw), lddw, sg, 1 if accumulate else 0, flags, base, need,
+                                   _stream()),
            "fp8q_grouped_wgrad")
     return dw
 
@@ -1016,11 +1026,13 @@ class AdamwTensors:
         self.held, self.array, self.g_dtype, self.bits, self.device = held, array, g_dtype, bits, device
 
 
-def _dense_span(what: str, name: str, t: torch.Tensor, shape: Optional[tuple], dtype: Optional[torch.dtype]) -> None:
-    if (shape is not None and tuple(t.shape) != tuple(shape)) or (dtype is not None and t.dtype != dtype) or \
-            not t.is_contiguous():
-        raise ValueError(f"{what}: {name} is {tuple(t.shape)} {t.dtype} with strides {t.stride()}, expected dense "
-                         f"{'' if shape is None else tuple(shape)} {'' if dtype is None else dtype}")
+def _dense(t: torch.Tensor, shape: tuple, dtype: torch.dtype) -> bool:
+    return t.shape == shape and t.dtype == dtype and t.is_contiguous()
+
+
+def _not_dense(at: str, name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype) -> ValueError:
+    return ValueError(f"{at}: {name} is {tuple(t.shape)} {t.dtype} with strides {t.stride()}, expected dense "
+                      f"{tuple(shape)} {dtype}")
 
 
 def adamw_tensors(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], states: Sequence[AdamwState],
@@ -1035,64 +1047,63 @@ def adamw_tensors(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
     if not params:
         raise ValueError(f"{what}: no tensors")
     bits = 8 if states[0].m.dtype == torch.uint8 else 32
+    kind, gtype = torch.uint8 if bits == 8 else torch.float32, grads[0].dtype
     array = (fp8q_adamw_tensor * len(params))()
-    written, read = [], []
-    for i, (p, g, state, c) in enumerate(zip(params, grads, states, codes)):
-        at, n = f"{what}: tensor {i}", p.numel()
-        _dense_span(at, "the parameter", p, None, torch.float32)
-        _dense_span(at, "the gradient", g, p.shape, grads[0].dtype)
-        kind = torch.uint8 if bits == 8 else torch.float32
-        _dense_span(at, "m", state.m, (n,), kind)
-        _dense_span(at, "v", state.v, (n,), kind)
-        out = [p, state.m, state.v]
+    spans = []  # (first byte, one past the last, written)
+    for i, (p, g, (m, v, sm, sv), c) in enumerate(zip(params, grads, states, codes)):
+        at, n, shape = f"{what}: tensor {i}", p.numel(), p.shape
+        flat = torch.Size((n,))
+        checks = [("the parameter", p, shape, torch.float32), ("m", m, flat, kind), ("v", v, flat, kind)]
         if bits == 8:
-            for name, t in (("sm", state.sm), ("sv", state.sv)):
-                if t is None:
-                    raise ValueError(f"{at}: 8-bit moments need scales")
-                _dense_span(at, name, t, (_cdiv(n, 128),), torch.float32)
-                out.append(t)
-        elif state.sm is not None or state.sv is not None:
+            if sm is None or sv is None:
+                raise ValueError(f"{at}: 8-bit moments need scales")
+            tiles = torch.Size((_cdiv(n, 128),))
+            checks += [("sm", sm, tiles, torch.float32), ("sv", sv, tiles, torch.float32)]
+        elif sm is not None or sv is not None:
             raise ValueError(f"{at}: fp32 moments have no scales")
         d = array[i]
-        d.n, d.p, d.g, d.m, d.v, d.sm, d.sv = (n, p.data_ptr(), g.data_ptr(), state.m.data_ptr(), state.v.data_ptr(),
-                                               _ptr(state.sm), _ptr(state.sv))
+        d.n, d.p, d.g, d.m, d.v = n, p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr()
+        if bits == 8:
+            d.sm, d.sv = sm.data_ptr(), sv.data_ptr()
         if c is not None and n:
-            if p.dim() not in (2, 3) or p.shape[-1] % 128 != 0:
-                raise ValueError(f"{at}: codes are kept of [N][K] or [G][N][K] with K a multiple of 128, not {tuple(p.shape)}")
-            lead, (N, K) = p.shape[:-2], p.shape[-2:]
+            if p.dim() not in (2, 3) or shape[-1] % 128 != 0:
+                raise ValueError(f"{at}: codes are kept of [N][K] or [G][N][K] with K a multiple of 128, not {tuple(shape)}")
+            lead, (N, K) = shape[:-2], shape[-2:]
             nb, kb, n16 = _cdiv(N, 128), K // 128, _pad16(N)
-            _dense_span(at, "q", c.q, p.shape, torch.uint8)
-            _dense_span(at, "s", c.s, (*lead, nb, kb), torch.float32)
-            out += [c.q, c.s]
+            checks += [("q", c.q, shape, torch.uint8), ("s", c.s, torch.Size((*lead, nb, kb)), torch.float32)]
             if (c.qt is None) != (c.st is None):
                 raise ValueError(f"{at}: qt and st go together")
+            d.N, d.K, d.q, d.s = N, K, c.q.data_ptr(), c.s.data_ptr()
             if c.qt is not None:
-                _dense_span(at, "st", c.st, (*lead, kb, nb), torch.float32)
+                checks.append(("st", c.st, torch.Size((*lead, kb, nb)), torch.float32))
+                strides = c.qt.stride()
                 if tuple(c.qt.shape) != (*lead, K, N) or c.qt.dtype != torch.uint8 or \
-                        (N > 1 and c.qt.stride(-1) != 1) or c.qt.stride(-2) != n16 or \
-                        (lead and lead[0] > 1 and c.qt.stride(0) != K * n16):
-                    raise ValueError(f"{at}: qt is {tuple(c.qt.shape)} {c.qt.dtype} with strides {c.qt.stride()}, expected "
+                        (N > 1 and strides[-1] != 1) or strides[-2] != n16 or \
+                        (lead and lead[0] > 1 and strides[0] != K * n16):
+                    raise ValueError(f"{at}: qt is {tuple(c.qt.shape)} {c.qt.dtype} with strides {strides}, expected "
                                      f"that of weight_codes()")
-                out += [c.qt, c.st]
-            d.N, d.K, d.q, d.s, d.qt, d.st = N, K, c.q.data_ptr(), c.s.data_ptr(), _ptr(c.qt), _ptr(c.st)
-        _on_current_device(at, g, *out)
-        read.append(g)
-        written += out
-    _no_overlap(what, written, read)
+                _on_current_device(at, c.qt)
+                spans.append((c.qt.data_ptr(), c.qt.data_ptr() + n // N * n16 - n16 + N, True))
+                d.qt, d.st = c.qt.data_ptr(), c.st.data_ptr()
+        for name, t, want, dtype in checks:
+            if not _dense(t, want, dtype):
+                raise _not_dense(at, name, t, want, dtype)
+        if not _dense(g, shape, gtype):
+            raise _not_dense(at, "the gradient", g, shape, gtype)
+        _on_device(at, g, *(t for _, t, _, _ in checks))
+        for _, t, _, _ in checks:
+            spans.append((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), True))
+        spans.append((d.g or 0, (d.g or 0) + n * g.element_size(), False))
+    _on_current_device(what, *params)
+    _no_overlap(what, spans)
     return AdamwTensors((tuple(params), tuple(grads), tuple(states), tuple(codes)), array, _dtype_code(grads[0]), bits,
                         params[0].device)
 
 
-def _no_overlap(what: str, written: list, read: list) -> None:
-    """No byte that is written belongs to two of the tensors (gradients may share)."""
-    spans = []
-    for t, w in [(t, True) for t in written] + [(t, False) for t in read]:
-        if t.numel():
-            last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
-            spans.append((t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size(), w))
-    spans.sort()
-    end, end_w = 0, 0  # ends of what was met so far, and of what is written of it
-    for lo, hi, w in spans:
+def _no_overlap(what: str, spans: list) -> None:
+    """spans: (first byte, one past the last, written).  No byte that is written belongs to two of them."""
+    end = end_w = 0  # ends of what was met so far, and of what is written of it
+    for lo, hi, w in sorted(s for s in spans if s[0] < s[1]):
         if lo < end_w or (w and lo < end):
             raise ValueError(f"{what}: tensors overlap (each may be in the list once)")
         end = max(end, hi)
@@ -1127,7 +1138,8 @@ def adamw(tensors: AdamwTensors, step: Union[int, torch.Tensor], lr: Union[float
     if given:
         _on_device("adamw", *given)
     if tensors.device.index != torch.cuda.current_device() or any(t.device != tensors.device for t in given):
-        raise ValueError(f"adamw: tensors on {tensors.device}, the current device is cuda:{torch.cuda.current_device()}")
+        raise ValueError(f"adamw: tensors on {tensors.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
     _check(_lib.fp8q_adamw(tensors.array, len(tensors.array), tensors.g_dtype, tensors.bits, ctypes.addressof(c),
                            scale_mode, _stream()), "fp8q_adamw")
 

@@ -184,11 +184,13 @@ def test_adamw_tensors_refuses():
 
 def test_overlap_check():
     from fp8_fine_grained_x128_amd.binding import _no_overlap
-    a = torch.zeros(64)
-    _no_overlap("x", [a[:32], a[32:]], [torch.zeros(4)])
-    g = torch.zeros(8)
-    _no_overlap("x", [a], [g, g])  # gradients may be shared
-    for w, r in (([a, a], []), ([a[:33], a[32:]], []), ([a], [a]), ([a[8:16]], [a]), ([a, g], [g[2:3]]),
-                 ([a[10:12], a[4:8], a[6:9]], [])):
+
+    def spans(written, read):
+        return [(a, b, True) for a, b in written] + [(a, b, False) for a, b in read]
+
+    _no_overlap("x", spans([(0, 128), (128, 256), (300, 300)], [(256, 300)]))
+    _no_overlap("x", spans([(0, 128)], [(200, 300), (200, 300), (250, 400)]))  # gradients may be shared
+    for w, r in (([(0, 64), (0, 64)], []), ([(0, 132), (128, 256)], []), ([(0, 64)], [(0, 64)]), ([(32, 64)], [(0, 128)]),
+                 ([(0, 128)], [(32, 64)]), ([(40, 48), (16, 32), (24, 36)], []), ([(10, 20)], [(0, 100), (50, 60)])):
         with pytest.raises(ValueError, match="overlap"):
-            _no_overlap("x", w, r)
+            _no_overlap("x", spans(w, r))
