@@ -863,22 +863,26 @@ def moe_decode(x: torch.Tensor, logits: torch.Tensor, w_gu: torch.Tensor, s_gu: 
 
 # ------------------------------------------------------------------ experts' weight gradients, AdamW
 
-def _on_current_device(what: str, *ts: torch.Tensor) -> None:
-    """Every tensor on torch's current HIP device, whose current stream the call goes to."""
-    now = torch.cuda.current_device() if torch.cuda.is_initialized() else -1
-    for t in ts:
-        if not t.is_cuda:
-            raise ValueError(f"{what}: tensors must be on a HIP device")
-        if t.get_device() != now:
-            raise ValueError(f"{what}: a tensor on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+def _stream_for(what: str, first: torch.Tensor, *rest: torch.Tensor) -> int:
+    """torch's current stream, if every tensor is on the current HIP device (a stream of another device would run
+    the call there)."""
+    dev = first.get_device()
+    for t in rest:
+        if t.get_device() != dev:
+            raise ValueError(f"{what}: tensors on different devices ({first.device}, {t.device})")
+    if dev < 0:
+        raise ValueError(f"{what}: tensors must be on a HIP device")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{what}: tensors on {first.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return torch.cuda.current_stream().cuda_stream if _raw_stream is None else _raw_stream(dev)
 
 
-def _check_offsets(what: str, offsets: torch.Tensor) -> int:
-    """int32 [G+1], dense; gives G."""
-    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 2 or not offsets.is_contiguous():
+def _groups_of(what: str, offsets: torch.Tensor) -> int:
+    """Groups of the offsets: int32 [G+1], dense."""
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] < 2 or offsets.stride(0) != 1:
         raise ValueError(f"{what}: offsets must be a contiguous int32 vector of the groups and one more, got "
                          f"{tuple(offsets.shape)} {offsets.dtype}")
-    return offsets.numel() - 1
+    return offsets.shape[0] - 1
 
 
 class GroupedOperand(NamedTuple):
@@ -892,18 +896,18 @@ class GroupedOperand(NamedTuple):
 def _grouped_operand(rows: int, cols: int, G: int, device) -> GroupedOperand:
     padded = _lib.fp8q_grouped_padded_rows(rows, G)
     return GroupedOperand(torch.empty((cols, padded), dtype=torch.uint8, device=device),
-                          _scales(padded // 128, cols, device), rows)
+                          torch.empty((padded // 128, cols), dtype=torch.float32, device=device), rows)
 
 
 def grouped_quantize_act(x: torch.Tensor, offsets: torch.Tensor, scale_mode: int = FP8Q_SCALE_FP32) -> GroupedOperand:
     """Rows x[offsets[g] .. offsets[g+1]) of each group in 128x1 tiles of their own, transposed; see
     fp8q_grouped_quantize_act.  Codes and scales past the last group's chunks hold what the memory held."""
-    G = _check_offsets("grouped_quantize_act", offsets)
+    G = _groups_of("grouped_quantize_act", offsets)
     rows, cols = x.shape
-    _on_current_device("grouped_quantize_act", x, offsets)
+    stream = _stream_for("grouped_quantize_act", x, offsets)
     o = _grouped_operand(rows, cols, G, x.device)
     _check(_lib.fp8q_grouped_quantize_act(x.data_ptr(), _dtype_code(x), rows, cols, _ld(x), offsets.data_ptr(), G,
-                                          o.q.data_ptr(), o.q.shape[1], o.s.data_ptr(), cols, scale_mode, _stream()),
+                                          o.q.data_ptr(), o.q.shape[1], o.s.data_ptr(), cols, scale_mode, stream),
            "fp8q_grouped_quantize_act")
     return o
 
@@ -913,15 +917,14 @@ def grouped_requant_transpose(q: torch.Tensor, s: torch.Tensor, offsets: torch.T
     """Cached 1x128 codes q[rows][cols] + scales s[ceil(cols/128)][rows], rows grouped, as grouped_quantize_act()
     gives them; see fp8q_grouped_requant_transpose."""
     _check_codes("grouped_requant_transpose codes", q)
-    G = _check_offsets("grouped_requant_transpose", offsets)
+    G = _groups_of("grouped_requant_transpose", offsets)
     rows, cols = q.shape
     _check_scales("grouped_requant_transpose scales (layout [ceil(cols/128)][rows])", s, _cdiv(cols, 128), rows)
-    _on_current_device("grouped_requant_transpose", q, s, offsets)
+    stream = _stream_for("grouped_requant_transpose", q, s, offsets)
     o = _grouped_operand(rows, cols, G, q.device)
     _check(_lib.fp8q_grouped_requant_transpose(q.data_ptr(), rows, cols, _ld(q), s.data_ptr(),
                                                s.stride(0) if s.shape[0] > 1 else max(rows, 1), offsets.data_ptr(), G,
-                                               o.q.data_ptr(), o.q.shape[1], o.s.data_ptr(), cols, scale_mode,
-                                               _stream()),
+                                               o.q.data_ptr(), o.q.shape[1], o.s.data_ptr(), cols, scale_mode, stream),
            "fp8q_grouped_requant_transpose")
     return o
 
@@ -931,40 +934,40 @@ def grouped_wgrad(dy: GroupedOperand, x: GroupedOperand, offsets: torch.Tensor,
                   flags: int = 0) -> torch.Tensor:
     """Weight gradients dW [G][N][K] of all groups from dy (N channels) and x (K channels); with `accumulate` added
     to the given fp32 dw.  See fp8q_grouped_wgrad."""
-    G = _check_offsets("grouped_wgrad", offsets)
+    G = _groups_of("grouped_wgrad", offsets)
     (qa, sa, rows), (qb, sb, rows_x) = dy, x
     if rows != rows_x:
         raise ValueError(f"grouped_wgrad: operands of {rows} and {rows_x} rows")
-    N, K = qa.shape[0], qb.shape[0]
+    (N, held), (K, held_x) = qa.shape, qb.shape
     padded = _lib.fp8q_grouped_padded_rows(rows, G)
-    for name, q, s in (("dy", qa, sa), ("x", qb, sb)):
-        if q.dtype != torch.uint8:
-            _check_codes(f"grouped_wgrad {name}", q)
-        if q.shape[1] < padded:
-            raise ValueError(f"grouped_wgrad: {name} has {q.shape[1]} tokens, {G} groups of {rows} rows take up to {padded}")
-        _check_scales(f"grouped_wgrad {name} (layout [chunks][channels])", s, padded // 128, q.shape[0])
-    if accumulate and dw is None:
-        raise ValueError("grouped_wgrad: accumulate needs the gradient to add to")
-    dev = qa.device
+    if held < padded or held_x < padded:
+        raise ValueError(f"grouped_wgrad: operands of {held} and {held_x} tokens, {G} groups of {rows} rows take up to "
+                         f"{padded}")
+    if qa.dtype != torch.uint8 or qb.dtype != torch.uint8:
+        _check_codes("grouped_wgrad dy", qa)
+        _check_codes("grouped_wgrad x", qb)
+    _check_scales("grouped_wgrad dy (layout [chunks][channels])", sa, padded // 128, N)
+    _check_scales("grouped_wgrad x (layout [chunks][channels])", sb, padded // 128, K)
     if dw is None:
-        dw = torch.empty((G, N, K), dtype=out_dtype, device=dev)
-        _on_current_device("grouped_wgrad", qa, sa, qb, sb, offsets)
+        if accumulate:
+            raise ValueError("grouped_wgrad: accumulate needs the gradient to add to")
+        stream = _stream_for("grouped_wgrad", qa, sa, qb, sb, offsets)
+        dw = torch.empty((G, N, K), dtype=out_dtype, device=qa.device)
+        lddw, sg = max(K, 1), N * max(K, 1)
     else:
         if dw.shape != (G, N, K) or (K > 1 and dw.stride(2) != 1):
             raise ValueError(f"grouped_wgrad: dw is {tuple(dw.shape)}, expected [{G}][{N}][{K}] with unit inner stride")
-        _on_current_device("grouped_wgrad", qa, sa, qb, sb, offsets, dw)
-    sg, lddw, _ = dw.stride()
-    if N <= 1 or G <= 1:  # axes of one element may carry any stride
-        lddw = lddw if N > 1 else max(K, 1)
-        sg = sg if G > 1 else N * lddw
+        stream = _stream_for("grouped_wgrad", qa, sa, qb, sb, offsets, dw)
+        lddw = dw.stride(1) if N > 1 else max(K, 1)  # axes of one element may carry any stride
+        sg = dw.stride(0) if G > 1 else N * lddw
     need = _lib.fp8q_grouped_wgrad_workspace(rows, G, N, K)
-    ws, base = _workspace(need, dev)
-    _check(_lib.fp8q_grouped_wgrad(qa.data_ptr(), _ld(qa) if N > 1 else max(qa.shape[1], 16), sa.data_ptr(),
+    ws, base = _workspace(need, qa.device)
+    _check(_lib.fp8q_grouped_wgrad(qa.data_ptr(), _ld(qa) if N > 1 else max(held, 16), sa.data_ptr(),
                                    sa.stride(0) if sa.shape[0] > 1 else max(N, 1), qb.data_ptr(),
-                                   _ld(qb) if K > 1 else max(qb.shape[1], 16), sb.data_ptr(),
+                                   _ld(qb) if K > 1 else max(held_x, 16), sb.data_ptr(),
                                    sb.stride(0) if sb.shape[0] > 1 else max(K, 1), offsets.data_ptr(), G, rows, N, K,
                                    dw.data_ptr(), _dtype_code(dw), lddw, sg, 1 if accumulate else 0, flags, base, need,
-                                   _stream()),
+                                   stream),
            "fp8q_grouped_wgrad")
     return dw
 
@@ -1002,7 +1005,7 @@ def weight_codes(w: torch.Tensor, transposed: bool = True, scale_mode: int = FP8
     """The codes of weights w ([N][K] or [G][N][K], K a multiple of 128) that adamw() keeps up to date."""
     if w.dim() not in (2, 3) or w.shape[-1] % 128 != 0 or not w.is_contiguous():
         raise ValueError(f"weight_codes: weights {tuple(w.shape)}, expected dense [N][K] or [G][N][K] with K a multiple of 128")
-    _on_current_device("weight_codes", w)
+    _stream_for("weight_codes", w)
     lead, (N, K), dev = w.shape[:-2], w.shape[-2:], w.device
     nb, kb, n16 = _cdiv(N, 128), K // 128, _pad16(N)
     o = WeightCodes(torch.empty((*lead, N, K), dtype=torch.uint8, device=dev),
@@ -1082,7 +1085,7 @@ def adamw_tensors(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
                         (lead and lead[0] > 1 and strides[0] != K * n16):
                     raise ValueError(f"{at}: qt is {tuple(c.qt.shape)} {c.qt.dtype} with strides {strides}, expected "
                                      f"that of weight_codes()")
-                _on_current_device(at, c.qt)
+                _on_device(at, p, c.qt)
                 spans.append((c.qt.data_ptr(), c.qt.data_ptr() + n // N * n16 - n16 + N, True))
                 d.qt, d.st = c.qt.data_ptr(), c.st.data_ptr()
         for name, t, want, dtype in checks:
@@ -1094,7 +1097,7 @@ def adamw_tensors(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
         for _, t, _, _ in checks:
             spans.append((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), True))
         spans.append((d.g or 0, (d.g or 0) + n * g.element_size(), False))
-    _on_current_device(what, *params)
+    _stream_for(what, *params)
     _no_overlap(what, spans)
     return AdamwTensors((tuple(params), tuple(grads), tuple(states), tuple(codes)), array, _dtype_code(grads[0]), bits,
                         params[0].device)
@@ -1118,32 +1121,24 @@ def adamw(tensors: AdamwTensors, step: Union[int, torch.Tensor], lr: Union[float
     values.  grad_scale multiplies the gradients; seed chooses the random numbers that round 8-bit moments.  See
     fp8q_adamw."""
     c = fp8q_adamw_config(0.0, beta1, beta2, eps, weight_decay, 0, None, None, None, seed & 0xFFFFFFFF)
-    given = []
     if isinstance(step, torch.Tensor):
-        _device_scalar("step", step, torch.int64)
-        c.step_dev = step.data_ptr()
-        given.append(step)
+        c.step_dev = _device_scalar("step", step, torch.int64, tensors)
     else:
         c.step = step
     if isinstance(lr, torch.Tensor):
-        _device_scalar("lr", lr, torch.float32)
-        c.lr_dev = lr.data_ptr()
-        given.append(lr)
+        c.lr_dev = _device_scalar("lr", lr, torch.float32, tensors)
     else:
         c.lr = lr
     if grad_scale is not None:
-        _device_scalar("grad_scale", grad_scale, torch.float32)
-        c.grad_scale = grad_scale.data_ptr()
-        given.append(grad_scale)
-    if given:
-        _on_device("adamw", *given)
-    if tensors.device.index != torch.cuda.current_device() or any(t.device != tensors.device for t in given):
-        raise ValueError(f"adamw: tensors on {tensors.device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+        c.grad_scale = _device_scalar("grad_scale", grad_scale, torch.float32, tensors)
+    stream = _stream_for("adamw", tensors.held[0][0])
     _check(_lib.fp8q_adamw(tensors.array, len(tensors.array), tensors.g_dtype, tensors.bits, ctypes.addressof(c),
-                           scale_mode, _stream()), "fp8q_adamw")
+                           scale_mode, stream), "fp8q_adamw")
 
 
-def _device_scalar(name: str, t: torch.Tensor, dtype: torch.dtype) -> None:
-    if t.numel() != 1 or t.dtype != dtype:
-        raise ValueError(f"adamw: {name} must be one {dtype} on the device, got {tuple(t.shape)} {t.dtype}")
+def _device_scalar(name: str, t: torch.Tensor, dtype: torch.dtype, tensors: AdamwTensors) -> int:
+    """Address of one number on the device of the tensors."""
+    if t.numel() != 1 or t.dtype != dtype or t.device != tensors.device:
+        raise ValueError(f"adamw: {name} must be one {dtype} on {tensors.device}, got {tuple(t.shape)} {t.dtype} on "
+                         f"{t.device}")
+    return t.data_ptr()

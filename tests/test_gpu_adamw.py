@@ -286,3 +286,18 @@ def test_writes_nothing_around_the_tensors(fp8q):
                 for b in big[2:]:
                     assert b[0] == 3.0 and (b[1 + t:] == 3.0).all()
             assert (p != 3.0).all()
+
+
+def test_refuses_scalars_elsewhere(fp8q):
+    p = torch.zeros(8, device=DEV)
+    plan = fp8q.adamw_tensors([p], [torch.zeros_like(p)], [fp8q.adamw_state(p)])
+    for kw in (dict(step=torch.tensor(3), lr=1e-3), dict(step=1, lr=torch.tensor(1e-3)), dict(step=1, lr=1e-3, grad_scale=torch.ones(1)),
+               dict(step=torch.tensor(3.0, device=DEV), lr=1e-3), dict(step=torch.ones(2, dtype=torch.int64, device=DEV), lr=1e-3)):
+        with pytest.raises(ValueError, match="must be one"):
+            fp8q.adamw(plan, **kw)
+    for kw in (dict(step=0, lr=1e-3), dict(step=1, lr=-1.0), dict(step=1, lr=1e-3, beta1=1.0)):
+        with pytest.raises(fp8q.Fp8qError):
+            fp8q.adamw(plan, **kw)
+    with pytest.raises(ValueError, match="overlap"):
+        fp8q.adamw_tensors([p, p], [torch.zeros_like(p)] * 2, [fp8q.adamw_state(p), fp8q.adamw_state(p)])
+    assert not p.any()
