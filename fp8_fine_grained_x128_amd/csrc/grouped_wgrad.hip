@@ -16,6 +16,7 @@ namespace fp8q {
 namespace {
 
 constexpr int kMaxWgradGroups = 1024;
+constexpr int kSortedGroups = 256;  // up to so many can be taken by size (each is ranked against all)
 
 // 4-byte buffer copy to LDS: lane i's dword (or 0 past the record count) lands at lds + 4 * i.
 __device__ __forceinline__ void buffer_copy4_to_lds(__amdgpu_buffer_rsrc_t r, uint32_t voffset, void* lds) {
@@ -45,7 +46,8 @@ struct WgradParams {
     int64_t ldc, c_group_stride;
     int tiles_m, tiles_n;
     int vec;    // c and its strides allow stores of four elements
-    int slice;  // chunks of a slice: a group of more is split, its slices' tiles go to ws
+    int sorted;  // groups are taken by size
+    int slice;   // chunks of a slice: a group of more is split, its slices' tiles go to ws
     float* ws;  // [slice][N][ldws]
     int64_t ldws;
 };
@@ -55,7 +57,6 @@ __device__ __forceinline__ int split_slices(int chunks, int slice) {
     return chunks > slice ? (chunks + slice - 1) / slice : 0;
 }
 
-template <int BM, int BN>
 struct Job {
     int kb, kb1;  // chunks
     int m0, n0;
@@ -261,50 +262,85 @@ __device__ __forceinline__ void chunk_step(const uint8_t* __restrict__ cur, uint
 template <int BM, int BN, int WM, int WN, int OUT, bool ACC, int MMA>
 __global__ __launch_bounds__(64 * WM * WN, 2) void grouped_wgrad_kernel(WgradParams p) {
     using Cfg = GemmCfg<BM, BN, WM, WN, 1>;
-    // One LDS object (see grouped_gemm_kernel): the tile stages, then the first
-    // chunk of every group and the first job of every group.
-    __shared__ __align__(1024) uint8_t lds[2 * Cfg::kStageBytes + 12 * (kMaxWgradGroups + 1)];
+    // One LDS object (see grouped_gemm_kernel): the tile stages, then tables of
+    // the groups: their first chunks and the slices before them in ws, the
+    // order they are taken in (by size, the largest first, or as they come) and
+    // the parts (one a slice) before each in that order.
+    constexpr int kThreads = 64 * WM * WN;
+    __shared__ __align__(1024) uint8_t lds[2 * Cfg::kStageBytes + 12 * (kMaxWgradGroups + 4) + 2 * kSortedGroups];
     int32_t* first = reinterpret_cast<int32_t*>(lds + 2 * Cfg::kStageBytes);
-    int32_t* slices = first + kMaxWgradGroups + 1;  // slices before the group's, in ws
-    int32_t* parts = slices + kMaxWgradGroups + 1;  // tile rounds (one a slice) before the group's
+    int32_t* slices = first + kMaxWgradGroups + 4;
+    int32_t* parts = slices + kMaxWgradGroups + 4;
+    uint16_t* by_size = reinterpret_cast<uint16_t*>(parts + kMaxWgradGroups + 4);
     const int G = p.groups;
     const int lane = threadIdx.x & 63;
     if (p.rows == 0) {  // perhaps no offsets either
-        for (int g = threadIdx.x; g <= G; g += 64 * WM * WN) first[g] = slices[g] = 0, parts[g] = g;
+        for (int g = threadIdx.x; g <= G; g += kThreads) first[g] = slices[g] = 0;
     } else if (threadIdx.x < 64) {
-        int n_chunks = 0, n_slices = 0, n_parts = 0;
+        int n_chunks = 0, n_slices = 0;
         for_groups_of_lane(p.offsets, G, p.rows, lane, [&](int, int lo, int hi) {
-            const int chunks = (hi - lo + 127) >> 7, sl = split_slices(chunks, p.slice);
-            n_chunks += chunks, n_slices += sl, n_parts += sl ? sl : 1;
+            const int chunks = (hi - lo + 127) >> 7;
+            n_chunks += chunks, n_slices += split_slices(chunks, p.slice);
         });
         int c0 = wave_scan_sum(n_chunks) - n_chunks, s0 = wave_scan_sum(n_slices) - n_slices;
-        int p0 = wave_scan_sum(n_parts) - n_parts;
         for_groups_of_lane(p.offsets, G, p.rows, lane, [&](int g, int lo, int hi) {
-            const int chunks = (hi - lo + 127) >> 7, sl = split_slices(chunks, p.slice);
-            first[g] = c0, slices[g] = s0, parts[g] = p0;
-            c0 += chunks, s0 += sl, p0 += sl ? sl : 1;
-            first[g + 1] = c0, slices[g + 1] = s0, parts[g + 1] = p0;
+            const int chunks = (hi - lo + 127) >> 7;
+            first[g] = c0, slices[g] = s0;
+            c0 += chunks, s0 += split_slices(chunks, p.slice);
+            first[g + 1] = c0, slices[g + 1] = s0;
         });
+    }
+    __syncthreads();
+    // a group's place: how many are larger, or as large and before it
+    for (int g = threadIdx.x; p.sorted && g < G; g += kThreads) {
+        const int mine = first[g + 1] - first[g];
+        int place = 0, at = 0;
+        for (int h = 0; h < G; ++h) {
+            const int end = first[h + 1], size = end - at;
+            place += size > mine || (size == mine && h < g);
+            at = end;
+        }
+        by_size[place] = (uint16_t)g;
+    }
+    auto group_at = [&](int order) __attribute__((always_inline)) { return p.sorted ? by_size[order] : order; };
+    __syncthreads();
+    if (threadIdx.x < 64) {  // parts in that order
+        const int per = (G + 63) / 64;
+        int n_parts = 0;
+        for (int i = lane * per; i < G && i < (lane + 1) * per; ++i) {
+            const int g = group_at(i);
+            n_parts += max(1, slices[g + 1] - slices[g]);
+        }
+        int p0 = wave_scan_sum(n_parts) - n_parts;
+        for (int i = lane * per; i < G && i < (lane + 1) * per; ++i) {
+            const int g = group_at(i);
+            parts[i] = p0;
+            p0 += max(1, slices[g + 1] - slices[g]);
+            parts[i + 1] = p0;
+        }
     }
     __syncthreads();
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
-    // The tiles of a round (one slice of a group) go to consecutive work-groups,
-    // round by round; this one takes every gridDim.x-th.
+    // The jobs are the tiles of the parts, one part after the other, dealt in
+    // rounds to the work-groups; by size every other round in reverse, so that
+    // who has a longer job in a round has a shorter one in the next.
     const uint32_t tiles = (uint32_t)p.tiles_m * p.tiles_n, nwg = gridDim.x;
-    uint32_t in = nwg % 8 == 0 ? blockIdx.x % 8 * (nwg / 8) + blockIdx.x / 8 : blockIdx.x;
-    int part = 0, g = 0;
+    const uint32_t slot = nwg % 8 == 0 ? blockIdx.x % 8 * (nwg / 8) + blockIdx.x / 8 : blockIdx.x;
+    uint32_t in = slot, step = p.sorted ? 2 * (nwg - 1 - slot) + 1 : nwg;  // to the next round; 2 nwg - step from there
+    int part = 0, order = 0;
     const int n_parts = __builtin_amdgcn_readfirstlane(parts[G]);
     constexpr int kEl = OUT == kDtypeF32 ? 4 : 2;
 
     // The next job; gradients of groups without rows are written on the way.
     auto next_job = [&]() __attribute__((always_inline)) {
-        Job<BM, BN> job;
+        Job job;
         job.c = nullptr;
-        for (;; in += nwg) {
+        for (;; in += step, step = 2 * nwg - step) {
             while (in >= tiles) in -= tiles, ++part;
             if (part >= n_parts) return job;
-            while (__builtin_amdgcn_readfirstlane(parts[g + 1]) <= part) ++g;
+            while (__builtin_amdgcn_readfirstlane(parts[order + 1]) <= part) ++order;
+            const int g = __builtin_amdgcn_readfirstlane(group_at(order));
             const int c0 = __builtin_amdgcn_readfirstlane(first[g]), c1 = __builtin_amdgcn_readfirstlane(first[g + 1]);
             // eight tiles of k by all of n, then the next eight: concurrent tiles share their operands in L2
             const uint32_t band = 8 * p.tiles_n, b0 = in / band * 8, in_band = in % band;
@@ -314,7 +350,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grouped_wgrad_kernel(WgradPar
             uint8_t* c = static_cast<uint8_t*>(p.c) + g * p.c_group_stride * kEl;
             job.partial = c1 - c0 > p.slice;
             if (job.partial) {
-                const int sl = part - __builtin_amdgcn_readfirstlane(parts[g]);
+                const int sl = part - __builtin_amdgcn_readfirstlane(parts[order]);
                 job.kb = c0 + sl * p.slice;
                 job.kb1 = job.kb + p.slice < c1 ? job.kb + p.slice : c1;
                 job.ldc = p.ldws;
@@ -337,7 +373,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grouped_wgrad_kernel(WgradPar
         }
     };
 
-    auto source_of = [&](const Job<BM, BN>& job) __attribute__((always_inline)) {
+    auto source_of = [&](const Job& job) __attribute__((always_inline)) {
         Source s;
         s.ra = make_rsrc(p.a + (int64_t)job.m0 * p.lda, (int64_t)(p.M - job.m0) * p.lda);
         s.rb = make_rsrc(p.b + (int64_t)job.n0 * p.ldb, (int64_t)(p.N - job.n0) * p.ldb);
@@ -348,7 +384,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grouped_wgrad_kernel(WgradPar
         return s;
     };
 
-    Job<BM, BN> job = next_job();
+    Job job = next_job();
     if (!job.c) return;
     Source src = source_of(job);
     int stage = 0;
@@ -374,8 +410,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grouped_wgrad_kernel(WgradPar
         for (int i = 0; i < Cfg::MT; ++i)
 #pragma unroll
             for (int j = 0; j < Cfg::NT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-        in += nwg;
-        const Job<BM, BN> next = next_job();
+        in += step, step = 2 * nwg - step;
+        const Job next = next_job();
         // under a chunk's products the next one of this job is copied, or the
         // first one of the next job (after the last of all, this one again,
         // into the stage that is not read any more)
@@ -447,34 +483,52 @@ __global__ __launch_bounds__(256) void wgrad_join_kernel(WgradParams p) {
     }
 }
 
-// 256x256 tiles, one work-group of 8 waves a compute unit, or 128x128 tiles,
-// two work-groups of 4 waves; and the chunks of a slice (INT32_MAX: no split).
+// How a product is cut.  A compute unit holds one work-group of 8 waves with
+// 256x256 tiles, or two of 4 waves with 128x128.  Times are in us, for fp32
+// gradients and groups of Zipf sizes.
+// Tiles: 256x256 halves the operands' way through the LDS, so it wins where a
+// round of work-groups stays within one or two groups, from half as many such
+// tiles a group as there are compute units (large : small for 64 experts of
+// 2048x7168 1256 : 1432, 4 of 7168x4096 1600 : 1944, 8 of 4096x4096 502 : 577,
+// 8 of 4096x2048 279 : 297), unless a quarter of the rounds would be empty.
+// Where a round spans many groups it waits for the largest one, with fewer and
+// longer jobs to even that out (8 of 2048x2048 117 : 103, 32 of 1024x1024 76 :
+// 62, 64 of 2048x2048 407 : 403).
+// Slices: few 128x128 tiles of long groups leave the card waiting for the
+// longest; groups are then split into slices, as long as one job a work-group
+// makes them, of kMinSlice chunks or more.  A slice's tile is written and read
+// again, some 15 us for a card full of them, so a split has to save
+// kSavedChunks against the longest group, taken as twice the average if there
+// are several.  Without : with where it saves 8 chunks, 1 group of 2048x2048
+// 30 : 42; 17 chunks, 4 of 1408x1408 62 : 86; 28 chunks, 4 of 384x512 47 : 25,
+// 2 of 1024x1024 35 : 33, 1 of 512x512 45 : 21; 42 chunks, 2 of 2048x1408 94 :
+// 90; 64 chunks, 2 of 2048x2048 181 : 152; 166 chunks, 1 of 428x2239 249 : 77.
+// Order: work-groups that get few jobs each (under kFewJobs) take the largest
+// groups first (as they come : by size for 64 of 2048x2048, 32 jobs each, 442 :
+// 403; 32 of 1024x2048 152 : 135).  Many jobs even out by themselves, and
+// groups bound by their stores then run beside others bound by their products
+// (64 of 2048x7168 1256 : 1286).
 struct WgradPlan {
     bool large;
-    int slice;
+    int slice;  // chunks; INT32_MAX: no split
     int64_t ldws, bytes;
 };
 
-#ifndef MIN_SLICE
-#define MIN_SLICE 4
-#endif
-constexpr int kMinSlice = MIN_SLICE;
+constexpr int kMinSlice = 4, kSavedChunks = 20, kFewJobs = 48;
 
 WgradPlan plan_wgrad(int64_t rows, int64_t G, int64_t N, int64_t K) {
     const int64_t cus = compute_units(), groups = G < rows ? G : rows;
-    const int64_t large = ((N + 255) / 256) * ((K + 255) / 256) * groups;
+    const int64_t large = ((N + 255) / 256) * ((K + 255) / 256), rounds = (large * groups + cus - 1) / cus;
     WgradPlan plan{true, INT32_MAX, 0, 0};
-    // share of the rounds of large tiles that is gradient, in percent
-    const int64_t rounds = (large + cus - 1) / cus;
-    if (rounds == 0 || 100 * groups * N * K >= 75 * rounds * cus * 65536) return plan;
+    if (rounds == 0 || (2 * large >= cus && 100 * groups * N * K >= 75 * rounds * cus * 65536)) return plan;
     plan.large = false;
     const int64_t tiles = ((N + 127) / 128) * ((K + 127) / 128), slots = 2 * cus;
     const int64_t chunks = rows / 128 + (groups + 1) / 2;  // about as many
     int64_t slice = (chunks * tiles + slots - 1) / slots;
     slice = slice < kMinSlice ? kMinSlice : slice;
-    const int64_t all = group_chunks(rows, G), most = (rows + 127) / 128;
+    const int64_t all = group_chunks(rows, G), longest = groups == 1 ? all : 2 * chunks / groups;
     plan.ldws = (K + 3) / 4 * 4;
-    if (most <= slice || plan.ldws * 4 >= (int64_t(1) << 24)) return plan;
+    if (longest < slice + kSavedChunks || plan.ldws * 4 >= (int64_t(1) << 24)) return plan;
     plan.slice = (int)slice;
     const int64_t split = all / (slice + 1);  // groups of more chunks than a slice
     plan.bytes = (all + split * (slice - 1)) / slice * N * plan.ldws * 4;
@@ -529,6 +583,7 @@ hipError_t launch_grouped_wgrad(const GemmArgs& g, int64_t c_group_stride, hipSt
     const int64_t jobs = (int64_t)p.tiles_m * p.tiles_n * (g.groups + split);
     const int64_t slots = (plan.large ? 1 : 2) * (int64_t)compute_units();
     const int64_t grid = jobs < slots ? jobs : slots;
+    p.sorted = plan.slice == INT32_MAX && g.groups <= kSortedGroups && jobs > slots && jobs < kFewJobs * slots;
     switch (g.mma) {
         case kMmaFp8: launch_wgrad_mma<kMmaFp8>(g, p, plan, grid, st); break;
         case kMmaBf16Fold: launch_wgrad_mma<kMmaBf16Fold>(g, p, plan, grid, st); break;

@@ -185,6 +185,23 @@ def test_wgrad_shapes(fp8q, G, rows, N, K):
     _check_dw(fp8q.grouped_wgrad(dy, x, offs, out_dtype=torch.bfloat16), dw, t, torch.bfloat16)
 
 
+@pytest.mark.parametrize("G,rows,N,K", [(4, 300, 2000, 4076), (4, 300, 2000, 4075), (3, 9000, 333, 130),
+                                        (6, 40000, 640, 520), (300, 900, 140, 130), (20, 2500, 700, 520)])
+def test_wgrad_cuts(fp8q, G, rows, N, K):
+    """Large tiles past both ends of the gradient; groups in slices, several a work-group; more groups than are taken
+    by size; groups by size."""
+    rows, raw = _many(G, rows, G)
+    off = R.clamped(raw, rows)
+    dy, qa, sa = _operand(fp8q, rows, off, N, 21, 1e-3)
+    x, qb, sb = _operand(fp8q, rows, off, K, 22, 0.1)
+    dw, t = R.wgrad(qa, sa, qb, sb, off)
+    offs = _offsets(raw)
+    one = fp8q.grouped_wgrad(dy, x, offs)
+    _check_dw(one, dw, t, torch.float32)
+    assert torch.equal(fp8q.grouped_wgrad(dy, x, offs, dw=one.clone(), accumulate=True), one + one)
+    _check_dw(fp8q.grouped_wgrad(dy, x, offs, out_dtype=torch.bfloat16), dw, t, torch.bfloat16)
+
+
 def test_wgrad_strided_output(fp8q):
     """Row and group strides of odd lengths; what lies between the rows stays."""
     rows, raw = OFFSETS["empty"]
