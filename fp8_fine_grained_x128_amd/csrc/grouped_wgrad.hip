@@ -15,7 +15,6 @@ namespace fp8q {
 
 namespace {
 
-constexpr int kMaxWgradGroups = 1024;
 constexpr int kSortedGroups = 256;  // up to so many can be taken by size (each is ranked against all)
 
 // 4-byte buffer copy to LDS: lane i's dword (or 0 past the record count) lands at lds + 4 * i.
@@ -267,27 +266,29 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grouped_wgrad_kernel(WgradPar
     // order they are taken in (by size, the largest first, or as they come) and
     // the parts (one a slice) before each in that order.
     constexpr int kThreads = 64 * WM * WN;
-    __shared__ __align__(1024) uint8_t lds[2 * Cfg::kStageBytes + 12 * (kMaxWgradGroups + 4) + 2 * kSortedGroups];
+    __shared__ __align__(1024) uint8_t lds[2 * Cfg::kStageBytes + 12 * (kMostGroups + 4) + 2 * kSortedGroups];
     int32_t* first = reinterpret_cast<int32_t*>(lds + 2 * Cfg::kStageBytes);
-    int32_t* slices = first + kMaxWgradGroups + 4;
-    int32_t* parts = slices + kMaxWgradGroups + 4;
-    uint16_t* by_size = reinterpret_cast<uint16_t*>(parts + kMaxWgradGroups + 4);
+    int32_t* slices = first + kMostGroups + 4;
+    int32_t* parts = slices + kMostGroups + 4;
+    uint16_t* by_size = reinterpret_cast<uint16_t*>(parts + kMostGroups + 4);
     const int G = p.groups;
     const int lane = threadIdx.x & 63;
     if (p.rows == 0) {  // perhaps no offsets either
         for (int g = threadIdx.x; g <= G; g += kThreads) first[g] = slices[g] = 0;
     } else if (threadIdx.x < 64) {
-        int n_chunks = 0, n_slices = 0;
-        for_groups_of_lane(p.offsets, G, p.rows, lane, [&](int, int lo, int hi) {
-            const int chunks = (hi - lo + 127) >> 7;
-            n_chunks += chunks, n_slices += split_slices(chunks, p.slice);
-        });
-        int c0 = wave_scan_sum(n_chunks) - n_chunks, s0 = wave_scan_sum(n_slices) - n_slices;
-        for_groups_of_lane(p.offsets, G, p.rows, lane, [&](int g, int lo, int hi) {
-            const int chunks = (hi - lo + 127) >> 7;
-            first[g] = c0, slices[g] = s0;
-            c0 += chunks, s0 += split_slices(chunks, p.slice);
-            first[g + 1] = c0, slices[g + 1] = s0;
+        for_group_count(G, [&](auto per) __attribute__((always_inline)) {
+            constexpr int PER = decltype(per)::value;
+            const LaneGroups<PER> l(p.offsets, G, p.rows, lane);
+            int n_chunks = 0, n_slices = 0;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) n_chunks += l.chunks(j), n_slices += split_slices(l.chunks(j), p.slice);
+            int c0 = wave_scan_sum(n_chunks) - n_chunks, s0 = wave_scan_sum(n_slices) - n_slices;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                if (PER * lane + j <= G) first[PER * lane + j] = c0, slices[PER * lane + j] = s0;
+                c0 += l.chunks(j), s0 += split_slices(l.chunks(j), p.slice);
+            }
+            if (lane == 63) first[G] = c0, slices[G] = s0;  // of all: groups past G are empty
         });
     }
     __syncthreads();
@@ -457,17 +458,22 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grouped_wgrad_kernel(WgradPar
 template <int OUT, bool ACC>
 __global__ __launch_bounds__(256) void wgrad_join_kernel(WgradParams p) {
     const int g = blockIdx.y, lane = threadIdx.x & 63;
-    int mine = 0, before = 0, count = 0;
-    for_groups_of_lane(p.offsets, p.groups, p.rows, lane, [&](int h, int lo, int hi) {
-        const int sl = split_slices((hi - lo + 127) >> 7, p.slice);
-        if (h < g) before += sl;
-        if (h == g) count = sl;
-        mine += sl;
+    int before = 0, count = 0;
+    for_group_count(p.groups, [&](auto per) __attribute__((always_inline)) {
+        constexpr int PER = decltype(per)::value;
+        const LaneGroups<PER> l(p.offsets, p.groups, p.rows, lane);
+        int mine = 0;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int sl = split_slices(l.chunks(j), p.slice);
+            if (PER * lane + j < g) before += sl;
+            if (PER * lane + j == g) count = sl;
+            mine += sl;
+        }
+        before += wave_scan_sum(mine) - mine;  // of the lanes below
+        count = __builtin_amdgcn_readlane(count, g / PER);
+        before = __builtin_amdgcn_readlane(before, g / PER);
     });
-    const int per = (p.groups + 63) / 64;
-    before += wave_scan_sum(mine) - mine;  // of the lanes below
-    count = __builtin_amdgcn_readlane(count, g / per);
-    before = __builtin_amdgcn_readlane(before, g / per);
     if (count == 0) return;
     const int64_t quads = (p.M + 3) / 4, total = p.N * quads, stride = p.N * p.ldws;
     constexpr int kEl = OUT == kDtypeF32 ? 4 : 2;

@@ -11,6 +11,8 @@
 // lead outside the arrays.
 #pragma once
 
+#include <type_traits>
+
 #include "device_common.hpp"
 
 namespace fp8q {
@@ -48,25 +50,36 @@ __device__ __forceinline__ int from_lane_below(int v) { return dpp_or_zero<0x138
 
 __device__ __forceinline__ int clamp_offset(int32_t v, int M) { return v < 0 ? 0 : v > M ? M : v; }
 
-// Walks the groups of this lane, [lane * per, lane * per + per) of G with per =
-// ceil(G / 64): f(g, lo, hi) with the offsets as above.  Needs the whole wave.
+constexpr int kMostGroups = 1024;
+
+// The rows of groups PER * lane .. PER * lane + PER - 1 (64 * PER >= G; those
+// past G are empty): group j of the lane's has rows [edge[j], edge[j + 1]).
+// All offsets are loaded at once (one after the other, as a loop that carries
+// the running maximum loads them, 2048x2048 of 256 groups took 53 us, not 35).
+template <int PER>
+struct LaneGroups {
+    int edge[PER + 1];
+    // Needs the whole wave.
+    __device__ __forceinline__ LaneGroups(const int32_t* __restrict__ off, int G, int M, int lane) {
+        int32_t v[PER + 1];
+#pragma unroll
+        for (int j = 0; j <= PER; ++j) v[j] = off[min(PER * lane + j, G)];
+        int top = clamp_offset(v[0], M);
+#pragma unroll
+        for (int j = 1; j <= PER; ++j) top = max(top, clamp_offset(v[j], M));
+        edge[0] = max(clamp_offset(v[0], M), from_lane_below(wave_scan_max(top)));
+#pragma unroll
+        for (int j = 1; j <= PER; ++j) edge[j] = max(edge[j - 1], clamp_offset(v[j], M));
+    }
+    __device__ __forceinline__ int chunks(int j) const { return (edge[j + 1] - edge[j] + 127) >> 7; }
+};
+
+// f(std::integral_constant<int, PER>) with a PER for G groups.
 template <class F>
-__device__ __forceinline__ void for_groups_of_lane(const int32_t* __restrict__ off, int G, int M, int lane, F&& f) {
-    const int per = (G + 63) / 64;
-    const int g0 = lane * per < G ? lane * per : G, g1 = g0 + per < G ? g0 + per : G;
-    int top = lane == 0 ? clamp_offset(off[0], M) : 0;
-    for (int g = g0; g < g1; ++g) {
-        const int hi = clamp_offset(off[g + 1], M);
-        top = hi > top ? hi : top;
-    }
-    int lo = from_lane_below(wave_scan_max(top));
-    if (lane == 0) lo = clamp_offset(off[0], M);
-    for (int g = g0; g < g1; ++g) {
-        int hi = clamp_offset(off[g + 1], M);
-        hi = hi > lo ? hi : lo;
-        f(g, lo, hi);
-        lo = hi;
-    }
+__device__ __forceinline__ void for_group_count(int G, F&& f) {
+    if (G <= 64) f(std::integral_constant<int, 1>());
+    else if (G <= 256) f(std::integral_constant<int, 4>());
+    else f(std::integral_constant<int, kMostGroups / 64>());
 }
 
 struct GroupChunk {
@@ -76,34 +89,25 @@ struct GroupChunk {
 };
 
 // The rows of chunk c, the same in every lane of the wave.
+template <int PER>
 __device__ __forceinline__ GroupChunk find_chunk(const int32_t* __restrict__ off, int G, int M, int c) {
     const int lane = threadIdx.x & 63;
-    GroupChunk r;
-    int row0 = 0, row_end = 0, start, end;
-    if (G <= 64) {  // a group a lane
-        int lo = clamp_offset(off[lane < G ? lane : G], M);
-        const int hi = wave_scan_max(max(lo, clamp_offset(off[lane < G ? lane + 1 : G], M)));
-        lo = max(lo, from_lane_below(hi));
-        const int n = (hi - lo + 127) >> 7;
-        end = wave_scan_sum(n);
-        start = end - n;
-        row0 = lo + 128 * (c - start);
-        row_end = hi;
-    } else {
-        int mine = 0;
-        for_groups_of_lane(off, G, M, lane, [&](int, int lo, int hi) { mine += (hi - lo + 127) >> 7; });
-        end = wave_scan_sum(mine);
-        start = end - mine;
-        int at = start;
-        for_groups_of_lane(off, G, M, lane, [&](int, int lo, int hi) {
-            const int n = (hi - lo + 127) >> 7;
-            if (c >= at && c < at + n) {
-                row0 = lo + 128 * (c - at);
-                row_end = hi;
-            }
-            at += n;
-        });
+    const LaneGroups<PER> l(off, G, M, lane);
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) n += l.chunks(j);
+    const int end = wave_scan_sum(n), start = end - n;
+    int row0 = 0, row_end = 0, at = start;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int next = at + l.chunks(j);
+        if (c >= at && c < next) {
+            row0 = l.edge[j] + 128 * (c - at);
+            row_end = l.edge[j + 1];
+        }
+        at = next;
     }
+    GroupChunk r;
     const uint64_t holds = __ballot(c >= start && c < end);
     r.live = holds != 0;
     const int src = r.live ? __builtin_ctzll(holds) : 0;
