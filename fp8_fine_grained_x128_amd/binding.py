@@ -962,9 +962,9 @@ def grouped_wgrad(dy: GroupedOperand, x: GroupedOperand, offsets: torch.Tensor,
         sg = dw.stride(0) if G > 1 else N * lddw
     need = _lib.fp8q_grouped_wgrad_workspace(rows, G, N, K)
     ws, base = _workspace(need, qa.device)
-    _check(_lib.fp8q_grouped_wgrad(qa.data_ptr(), _ld(qa) if N > 1 else max(held, 16), sa.data_ptr(),
+    _check(_lib.fp8q_grouped_wgrad(qa.data_ptr(), _ld(qa), sa.data_ptr(),
                                    sa.stride(0) if sa.shape[0] > 1 else max(N, 1), qb.data_ptr(),
-                                   _ld(qb) if K > 1 else max(held_x, 16), sb.data_ptr(),
+                                   _ld(qb), sb.data_ptr(),
                                    sb.stride(0) if sb.shape[0] > 1 else max(K, 1), offsets.data_ptr(), G, rows, N, K,
                                    dw.data_ptr(), _dtype_code(dw), lddw, sg, 1 if accumulate else 0, flags, base, need,
                                    stream),

@@ -232,6 +232,16 @@ def test_wgrad_datapaths(fp8q, flags):
                   tol=1e-5 + (2.0 ** -10 if flags & 1 else 0.0))
 
 
+def test_wgrad_refuses_strided_codes_of_one_channel(fp8q):
+    offs = _offsets([0, 200])
+    one, other = (fp8q.grouped_quantize_act(_x(200, n, torch.bfloat16, 23), offs) for n in (1, 40))
+    apart = fp8q.GroupedOperand(torch.zeros((1, 2 * one.q.shape[1]), dtype=torch.uint8, device=DEV)[:, ::2], one.s, 200)
+    for dy, x in ((apart, other), (other, apart)):
+        with pytest.raises(ValueError, match="unit column stride"):
+            fp8q.grouped_wgrad(dy, x, offs)
+    assert fp8q.grouped_wgrad(one, other, offs).shape == (1, 1, 40)
+
+
 def test_wgrad_of_no_rows(fp8q):
     o = fp8q.grouped_quantize_act(torch.empty((0, 64), device=DEV), _offsets([0, 0, 0]))
     assert o.q.shape == (64, 0) and o.s.shape == (0, 64)
