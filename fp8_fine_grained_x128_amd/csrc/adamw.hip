@@ -14,6 +14,14 @@
 //   - sqrt(v) of a positive v rounds to one step of the smallest codes at least:
 //     with a zero there the next step would divide m by eps alone.
 // The step itself takes the moments before they are rounded.
+//
+// Both kernels are bound by memory: every byte moves once (per element fp32 28,
+// with 8-bit moments and bf16 gradients 14; the codes add one byte each).  16
+// experts of 2048x7168 with 8-bit moments and both codes, 4.26 GB: 855 us, 5.0
+// TB/s, where a large copy reaches 4.7; 29 million weights with fp32 moments
+// and both codes, 881 MB: 193 us, 4.6 TB/s.  With 8-bit moments the rounding's
+// instructions come close to the time of the bytes: the shorter forms that a
+// wave's values allow, below, took 932 us to 901.
 #include <cmath>
 
 #include "../../include/fp8q.h"

@@ -542,10 +542,9 @@ int fp8q_grouped_requant_transpose(const uint8_t *q, int64_t rows, int64_t cols,
  * FP8Q_F32; accumulate != 0 (fp32 only) adds to dw.  The gradient of a group
  * without rows is zero (rows == 0 too: nothing is read then).  Any N and K;
  * `flags` and the error bounds are those of fp8q_gemm_ex.
- * Where the tiles of the gradients do not fill the GPU the contraction is split
- * as in fp8q_gemm_splitk: workspace of at least
- * fp8q_grouped_wgrad_workspace(rows, G, N, K) bytes (0: none needed), under the
- * rules there.  Repeated calls give the same bits.
+ * Long contractions of few tiles are split as in fp8q_gemm_splitk: workspace of
+ * at least fp8q_grouped_wgrad_workspace(rows, G, N, K) bytes (0: none needed),
+ * under the rules there.  Repeated calls give the same bits.
  */
 int64_t fp8q_grouped_wgrad_workspace(int64_t rows, int G, int64_t N, int64_t K);
 
