@@ -491,14 +491,22 @@ __global__ __launch_bounds__(256) void wgrad_join_kernel(WgradParams p) {
     if (count == 0) return;
     const int64_t quads = (p.M + 3) / 4, total = p.N * quads, stride = p.N * p.ldws;
     constexpr int kEl = OUT == kDtypeF32 ? 4 : 2;
+    constexpr int kAtOnce = 8;  // slices loaded at once
     const float* first = p.ws + before * stride;
     uint8_t* c = static_cast<uint8_t*>(p.c) + g * p.c_group_stride * kEl;
     for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
         const int64_t n = e / quads;
         const int k = 4 * (int)(e - n * quads);
         const float* q = first + n * p.ldws + k;
-        v4f sum = *reinterpret_cast<const v4f*>(q);
-        for (int sl = 1; sl < count; ++sl) sum += *reinterpret_cast<const v4f*>(q + sl * stride);
+        v4f sum = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int s0 = 0; s0 < count; s0 += kAtOnce) {
+            v4f v[kAtOnce];
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) v[u] = *reinterpret_cast<const v4f*>(q + min(s0 + u, count - 1) * stride);
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u)
+                if (s0 + u < count) sum += v[u];
+        }
         store4<OUT, ACC>(c + n * p.ldc * kEl, k, p.M - k > 4 ? 4 : p.M - k, sum, p.vec);
     }
 }
