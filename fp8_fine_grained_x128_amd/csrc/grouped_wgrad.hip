@@ -21,6 +21,7 @@
 // with, the same 300 more; stores between the last chunk's products:
 // 1347 : 1199.)  Few large experts are bound by the products (4 of 7168x4096,
 // 32768 rows: 1604, without stores 1662 : 1688 as measured beside it).
+#include <cmath>
 #include <type_traits>
 
 #include "gemm_tile.hpp"
@@ -62,14 +63,16 @@ struct WgradParams {
     int tiles_m, tiles_n;
     int vec;    // c and its strides allow stores of four elements
     int sorted;  // groups are taken by size
-    int slice;   // chunks of a slice: a group of more is split, its slices' tiles go to ws
+    int slice;   // chunks of a slice: groups of 1.5 or more are split, their slices' tiles go to ws
     float* ws;  // [slice][N][ldws]
     int64_t ldws;
 };
 
-// Slices of a group of `chunks`: one that is stored to dW at once, or several.
+// Slices of a group of `chunks`, of about `slice` each; 0: one part, stored to
+// dW at once.
 __device__ __forceinline__ int split_slices(int chunks, int slice) {
-    return chunks > slice ? (chunks + slice - 1) / slice : 0;
+    const int n = (chunks + (slice >> 1)) / slice;
+    return n > 1 ? n : 0;
 }
 
 struct Job {
@@ -279,14 +282,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grouped_wgrad_kernel(WgradPar
     using Cfg = GemmCfg<BM, BN, WM, WN, 1>;
     // One LDS object (see grouped_gemm_kernel): the tile stages, then tables of
     // the groups: their first chunks and the slices before them in ws, the
-    // order they are taken in (by size, the largest first, or as they come) and
-    // the parts (one a slice) before each in that order.
+    // parts (one a slice) before each in the order that they are taken in (the
+    // longest parts first, or as they come), the lengths of their parts and
+    // that order.
     constexpr int kThreads = 64 * WM * WN;
-    __shared__ __align__(1024) uint8_t lds[2 * Cfg::kStageBytes + 12 * (kMostGroups + 4) + 2 * kSortedGroups];
+    __shared__ __align__(1024) uint8_t lds[2 * Cfg::kStageBytes + 12 * (kMostGroups + 4) + 6 * kSortedGroups];
     int32_t* first = reinterpret_cast<int32_t*>(lds + 2 * Cfg::kStageBytes);
     int32_t* slices = first + kMostGroups + 4;
     int32_t* parts = slices + kMostGroups + 4;
-    uint16_t* by_size = reinterpret_cast<uint16_t*>(parts + kMostGroups + 4);
+    int32_t* length = parts + kMostGroups + 4;
+    uint16_t* by_size = reinterpret_cast<uint16_t*>(length + kSortedGroups);
     const int G = p.groups;
     const int lane = threadIdx.x & 63;
     if (p.rows == 0) {  // perhaps no offsets either
@@ -308,16 +313,19 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grouped_wgrad_kernel(WgradPar
         });
     }
     __syncthreads();
-    // a group's place: how many are larger, or as large and before it
-    for (int g = threadIdx.x; p.sorted && g < G; g += kThreads) {
-        const int mine = first[g + 1] - first[g];
-        int place = 0, at = 0;
-        for (int h = 0; h < G; ++h) {
-            const int end = first[h + 1], size = end - at;
-            place += size > mine || (size == mine && h < g);
-            at = end;
+    if (p.sorted) {
+        for (int g = threadIdx.x; g < G; g += kThreads) {
+            const int n = max(1, slices[g + 1] - slices[g]);
+            length[g] = (first[g + 1] - first[g] + n - 1) / n;
         }
-        by_size[place] = (uint16_t)g;
+        __syncthreads();
+        // a group's place: how many are longer, or as long and before it
+        for (int g = threadIdx.x; g < G; g += kThreads) {
+            const int mine = length[g];
+            int place = 0;
+            for (int h = 0; h < G; ++h) place += length[h] > mine || (length[h] == mine && h < g);
+            by_size[place] = (uint16_t)g;
+        }
     }
     auto group_at = [&](int order) __attribute__((always_inline)) { return p.sorted ? by_size[order] : order; };
     __syncthreads();
@@ -365,13 +373,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grouped_wgrad_kernel(WgradPar
             job.m0 = (int)(b0 + in_band % height) * BM;
             job.n0 = (int)(in_band / height) * BN;
             uint8_t* c = static_cast<uint8_t*>(p.c) + g * p.c_group_stride * kEl;
-            job.partial = c1 - c0 > p.slice;
+            const int s0 = __builtin_amdgcn_readfirstlane(slices[g]), n = __builtin_amdgcn_readfirstlane(slices[g + 1]) - s0;
+            job.partial = n > 0;
             if (job.partial) {
                 const int sl = part - __builtin_amdgcn_readfirstlane(parts[order]);
-                job.kb = c0 + sl * p.slice;
-                job.kb1 = job.kb + p.slice < c1 ? job.kb + p.slice : c1;
+                const int each = (c1 - c0) / n, more = (c1 - c0) % n;
+                job.kb = c0 + sl * each + min(sl, more);
+                job.kb1 = job.kb + each + (sl < more);
                 job.ldc = p.ldws;
-                job.c = p.ws + (int64_t)(__builtin_amdgcn_readfirstlane(slices[g]) + sl) * p.N * p.ldws;
+                job.c = p.ws + (int64_t)(s0 + sl) * p.N * p.ldws;
                 return job;
             }
             if (c0 < c1) {
@@ -524,15 +534,22 @@ __global__ __launch_bounds__(256) void wgrad_join_kernel(WgradParams p) {
 // Where a round spans many groups it waits for the largest one, with fewer and
 // longer jobs to even that out (8 of 2048x2048 117 : 103, 32 of 1024x1024 76 :
 // 62, 64 of 2048x2048 407 : 403).
-// Slices: few 128x128 tiles of long groups leave the card waiting for the
-// longest; groups are then split into slices, as long as one job a work-group
-// makes them, of kMinSlice chunks or more.  A slice's tile is written and read
-// again, some 15 us for a card full of them, so a split has to save
-// kSavedChunks against the longest group, taken as twice the average if there
-// are several.  Without : with where it saves 8 chunks, 1 group of 2048x2048
-// 30 : 42; 17 chunks, 4 of 1408x1408 62 : 86; 28 chunks, 4 of 384x512 47 : 25,
-// 2 of 1024x1024 35 : 33, 1 of 512x512 45 : 21; 42 chunks, 2 of 2048x1408 94 :
-// 90; 64 chunks, 2 of 2048x2048 181 : 152; 166 chunks, 1 of 428x2239 249 : 77.
+// Slices: where 128x128 tiles of a long group leave the card waiting for it,
+// groups are split into even slices of about as many chunks as one job a
+// work-group makes them, kMinSlice or more (groups below 1.5 of that are left
+// whole).  How long the longest group is the host does not know: it is taken as
+// sizes that fall as 1 / rank have it, 1 / (1 + ln G) of all.  A split has to
+// save kSavedChunks against it (the join's launch, 5 us) and one chunk's time
+// for every kChunkBytes of slices, which are written and read again.
+// Without : with, Zipf sizes (equal sizes in brackets), for 32 groups of
+// 512x512, 32768 rows 100 : 44 (28 : 34), 8 of 1024x1024, 65536 rows 399 : 202
+// (153 : 148), 9 of 128x640, 8014 rows 37 : 17 (15 : 17), 4 of 384x512, 8192
+// rows 47 : 23 (26 : 23), 3 of 256x4288, 17908 rows 107 : 66 (68 : 66), 1 of
+// 428x2239, 24782 rows 249 : 76; and where the rule leaves them whole, 1 of
+// 2048x2048, 2048 rows 29 : 41, 4 of 512x1536, 2048 rows 18 : 24 (14 : 23), 4 of
+// 768x2304, 4096 rows 42 : 36 (25 : 29), 16 of 640x640, 4096 rows 24 : 23 (13 :
+// 19).  (Slices of equal length with a remainder, in the groups' order: 3 of
+// 256x4288 81, 4 of 1408x1408, 8192 rows 86, now 58.)
 // Order: work-groups that get few jobs each (under kFewJobs) take the largest
 // groups first (as they come : by size for 64 of 2048x2048, 32 jobs each, 442 :
 // 403; 32 of 1024x2048 152 : 135).  Many jobs even out by themselves, and
@@ -544,7 +561,8 @@ struct WgradPlan {
     int64_t ldws, bytes;
 };
 
-constexpr int kMinSlice = 4, kSavedChunks = 20, kFewJobs = 48;
+constexpr int kMinSlice = 4, kSavedChunks = 6, kFewJobs = 48;
+constexpr double kChunkBytes = 5.3e6;
 
 WgradPlan plan_wgrad(int64_t rows, int64_t G, int64_t N, int64_t K) {
     const int64_t cus = compute_units(), groups = G < rows ? G : rows;
@@ -556,12 +574,13 @@ WgradPlan plan_wgrad(int64_t rows, int64_t G, int64_t N, int64_t K) {
     const int64_t chunks = rows / 128 + (groups + 1) / 2;  // about as many
     int64_t slice = (chunks * tiles + slots - 1) / slots;
     slice = slice < kMinSlice ? kMinSlice : slice;
-    const int64_t all = group_chunks(rows, G), longest = groups == 1 ? all : 2 * chunks / groups;
     plan.ldws = (K + 3) / 4 * 4;
-    if (longest < slice + kSavedChunks || plan.ldws * 4 >= (int64_t(1) << 24)) return plan;
+    const double longest = (double)chunks / (1.0 + std::log((double)groups));
+    const double cost = kSavedChunks + longest / slice * N * plan.ldws * 4 / kChunkBytes;
+    if (longest < slice + cost || plan.ldws * 4 >= (int64_t(1) << 24)) return plan;
     plan.slice = (int)slice;
-    const int64_t split = all / (slice + 1);  // groups of more chunks than a slice
-    plan.bytes = (all + split * (slice - 1)) / slice * N * plan.ldws * 4;
+    // a split group of c chunks has at most c / slice + 1/2 slices, and c >= 1.5 slice
+    plan.bytes = 4 * group_chunks(rows, G) / (3 * slice) * N * plan.ldws * 4;
     return plan;
 }
 
@@ -609,11 +628,11 @@ hipError_t launch_grouped_wgrad(const GemmArgs& g, int64_t c_group_stride, hipSt
     p.ws = static_cast<float*>(g.workspace);
     p.ldws = plan.ldws;
     // work-groups: as many as there are jobs, or as fit at once
-    const int64_t split = plan.slice == INT32_MAX ? 0 : group_chunks(g.K, g.groups) / plan.slice;
+    const int64_t split = plan.slice == INT32_MAX ? 0 : 4 * group_chunks(g.K, g.groups) / (3 * plan.slice);
     const int64_t jobs = (int64_t)p.tiles_m * p.tiles_n * (g.groups + split);
     const int64_t slots = (plan.large ? 1 : 2) * (int64_t)compute_units();
     const int64_t grid = jobs < slots ? jobs : slots;
-    p.sorted = plan.slice == INT32_MAX && g.groups <= kSortedGroups && jobs > slots && jobs < kFewJobs * slots;
+    p.sorted = g.groups <= kSortedGroups && jobs > slots && jobs < kFewJobs * slots;
     switch (g.mma) {
         case kMmaFp8: launch_wgrad_mma<kMmaFp8>(g, p, plan, grid, st); break;
         case kMmaBf16Fold: launch_wgrad_mma<kMmaBf16Fold>(g, p, plan, grid, st); break;
