@@ -540,7 +540,8 @@ __global__ __launch_bounds__(256) void wgrad_join_kernel(WgradParams p) {
 // whole).  How long the longest group is the host does not know: it is taken as
 // sizes that fall as 1 / rank have it, 1 / (1 + ln G) of all.  A split has to
 // save kSavedChunks against it (the join's launch, 5 us) and one chunk's time
-// for every kChunkBytes of slices, which are written and read again.
+// for every kChunkBytes of slices, which are written and read again; and the
+// longest group has to be two slices, else hardly any is cut.
 // Without : with, Zipf sizes (equal sizes in brackets), for 32 groups of
 // 512x512, 32768 rows 100 : 44 (28 : 34), 8 of 1024x1024, 65536 rows 399 : 202
 // (153 : 148), 9 of 128x640, 8014 rows 37 : 17 (15 : 17), 4 of 384x512, 8192
@@ -548,8 +549,9 @@ __global__ __launch_bounds__(256) void wgrad_join_kernel(WgradParams p) {
 // 428x2239, 24782 rows 249 : 76; and where the rule leaves them whole, 1 of
 // 2048x2048, 2048 rows 29 : 41, 4 of 512x1536, 2048 rows 18 : 24 (14 : 23), 4 of
 // 768x2304, 4096 rows 42 : 36 (25 : 29), 16 of 640x640, 4096 rows 24 : 23 (13 :
-// 19).  (Slices of equal length with a remainder, in the groups' order: 3 of
-// 256x4288 81, 4 of 1408x1408, 8192 rows 86, now 58.)
+// 19), 32 of 1024x1024, 8192 rows 61 : 68 (37 : 51), 4 of 1408x1408, 8192 rows
+// 59 : 57 (43 : 45).  (Slices of equal length with a remainder, in the groups'
+// order: 3 of 256x4288 81, 4 of 1408x1408 86.)
 // Order: work-groups that get few jobs each (under kFewJobs) take the largest
 // groups first (as they come : by size for 64 of 2048x2048, 32 jobs each, 442 :
 // 403; 32 of 1024x2048 152 : 135).  Many jobs even out by themselves, and
@@ -577,7 +579,7 @@ WgradPlan plan_wgrad(int64_t rows, int64_t G, int64_t N, int64_t K) {
     plan.ldws = (K + 3) / 4 * 4;
     const double longest = (double)chunks / (1.0 + std::log((double)groups));
     const double cost = kSavedChunks + longest / slice * N * plan.ldws * 4 / kChunkBytes;
-    if (longest < slice + cost || plan.ldws * 4 >= (int64_t(1) << 24)) return plan;
+    if (longest < 2.0 * slice || longest < slice + cost || plan.ldws * 4 >= (int64_t(1) << 24)) return plan;
     plan.slice = (int)slice;
     // a split group of c chunks has at most c / slice + 1/2 slices, and c >= 1.5 slice
     plan.bytes = 4 * group_chunks(rows, G) / (3 * slice) * N * plan.ldws * 4;
