@@ -1,6 +1,7 @@
 """The experts' operators together: the example's training step against the same step in fp32, replayed from a graph,
 and calls on several streams at once."""
 import importlib.util
+import itertools
 import os
 
 import numpy as np
@@ -171,6 +172,27 @@ def test_workspace_of_exactly_the_bytes(fp8q):
                                      need, torch.cuda.current_stream().cuda_stream)
         assert st == 0 and torch.equal(dw, want)
         assert (buf[:lead] == 0x77).all() and (buf[lead + need:] == 0x77).all()
+
+
+@pytest.mark.parametrize("sizes", [[768] * 8, [641] * 8, [640] * 8, [641, 1, 1, 1, 4481, 1, 1, 1], [5000] + [1] * 7])
+def test_most_slices_fit_the_workspace(fp8q, sizes):
+    """Groups of one and a half slices, or just more or less, are cut into the most slices for their rows."""
+    rows, G, N, K = sum(sizes), len(sizes), 70, 128
+    need = fp8q.fp8q_grouped_wgrad_workspace(rows, G, N, K)
+    assert need > 0
+    o = torch.tensor([0, *itertools.accumulate(sizes)], dtype=torch.int32, device=DEV)
+    torch.manual_seed(4)
+    a = fp8q.grouped_quantize_act(torch.randn((rows, 72), device=DEV)[:, :N], o)
+    b = fp8q.grouped_quantize_act(torch.randn((rows, K), device=DEV), o)
+    dw = torch.empty((G, N, K), device=DEV)
+    buf = torch.full((need + 512,), 0x77, dtype=torch.uint8, device=DEV)
+    lead = -buf.data_ptr() % 256
+    assert fp8q.fp8q_grouped_wgrad(a.q.data_ptr(), a.q.shape[1], a.s.data_ptr(), N, b.q.data_ptr(), b.q.shape[1],
+                                   b.s.data_ptr(), K, o.data_ptr(), G, rows, N, K, dw.data_ptr(), 0, K, N * K, 0, 0,
+                                   buf.data_ptr() + lead, need, torch.cuda.current_stream().cuda_stream) == 0
+    assert (buf[:lead] == 0x77).all() and (buf[lead + need:] == 0x77).all()
+    want, t = R.wgrad(*(v.cpu().numpy() for v in (a.q, a.s, b.q, b.s)), np.array(o.cpu()))
+    assert (np.abs(dw.cpu().numpy() - want) <= 1e-5 * t).all()
 
 
 def test_two_streams_at_once(fp8q):
