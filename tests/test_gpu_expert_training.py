@@ -191,7 +191,7 @@ def test_most_slices_fit_the_workspace(fp8q, sizes):
                                    b.s.data_ptr(), K, o.data_ptr(), G, rows, N, K, dw.data_ptr(), 0, K, N * K, 0, 0,
                                    buf.data_ptr() + lead, need, torch.cuda.current_stream().cuda_stream) == 0
     assert (buf[:lead] == 0x77).all() and (buf[lead + need:] == 0x77).all()
-    want, t = R.wgrad(*(v.cpu().numpy() for v in (a.q, a.s, b.q, b.s)), np.array(o.cpu()))
+    want, t = R.wgrad(*(v.cpu().numpy() for v in (a.q, a.s, b.q, b.s)), o.cpu().numpy())
     assert (np.abs(dw.cpu().numpy() - want) <= 1e-5 * t).all()
 
 
