@@ -52,7 +52,7 @@ struct WgradParams {
     const uint8_t* b;
     const float* sa;
     const float* sb;
-    int lda, ldb;
+    uint32_t lda, ldb;  // 256 rows stay below 2^32
     int64_t ldsa, ldsb;
     const int32_t* offsets;
     int groups;
@@ -244,14 +244,14 @@ struct Copies {
     uint32_t off_a, off_b;
     __device__ __forceinline__ Copies(const WgradParams& p, int wave) {
         const int lane = lane_now(), lrow = lane >> 3, unit = (lane & 7) ^ swz(lrow);
-        off_a = (uint32_t)((8 * wave + lrow) * p.lda + 16 * unit);
-        off_b = (uint32_t)((8 * wave + lrow) * p.ldb + 16 * unit);
+        off_a = (uint32_t)(8 * wave + lrow) * p.lda + 16 * unit;
+        off_b = (uint32_t)(8 * wave + lrow) * p.ldb + 16 * unit;
     }
     __device__ __forceinline__ void issue(uint8_t* stage, const Source& src, const WgradParams& p, int kb, int wave,
                                           int it) const {
         constexpr int kRows = 8 * Cfg::kWaves;  // rows of one part of all waves
         const bool is_a = kRows * it < BM;
-        const uint32_t step = (uint32_t)(is_a ? kRows * it * p.lda : (kRows * it - BM) * p.ldb);
+        const uint32_t step = is_a ? (uint32_t)(kRows * it) * p.lda : (uint32_t)(kRows * it - BM) * p.ldb;
         uint32_t voff;
         asm volatile("v_add_u32 %0, %1, %2" : "=v"(voff) : "s"(step), "v"(is_a ? off_a : off_b));
         buffer_copy16_to_lds(is_a ? src.ra : src.rb, voff, (uint32_t)kb * 128u, stage + 1024 * (wave + Cfg::kWaves * it));
@@ -616,8 +616,8 @@ int64_t grouped_wgrad_bytes(int64_t rows, int groups, int64_t M, int64_t N) {
 hipError_t launch_grouped_wgrad(const GemmArgs& g, int64_t c_group_stride, hipStream_t st) {
     const WgradPlan plan = plan_wgrad(g.K, g.groups, g.M, g.N);
     WgradParams p{};
-    p.a = g.b; p.lda = (int)g.ldb; p.sa = g.sb; p.ldsa = g.ldsb;
-    p.b = g.a; p.ldb = (int)g.lda; p.sb = g.sa; p.ldsb = g.ldsa;
+    p.a = g.b; p.lda = (uint32_t)g.ldb; p.sa = g.sb; p.ldsa = g.ldsb;
+    p.b = g.a; p.ldb = (uint32_t)g.lda; p.sb = g.sa; p.ldsb = g.ldsa;
     p.offsets = g.offsets; p.groups = g.groups; p.rows = (int)g.K;
     p.M = (int)g.N; p.N = (int)g.M; p.c = g.c; p.ldc = g.ldc; p.c_group_stride = c_group_stride;
     const int tile = plan.large ? 256 : 128;

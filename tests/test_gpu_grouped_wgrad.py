@@ -232,6 +232,25 @@ def test_wgrad_datapaths(fp8q, flags):
                   tol=1e-5 + (2.0 ** -10 if flags & 1 else 0.0))
 
 
+def test_wgrad_of_the_longest_rows(fp8q):
+    """Offsets inside an operand past 32 bits: as many tokens as the product takes, few of them not zero."""
+    rows, N, K, raw = (1 << 24) - 256, 256, 20, [0, 12345, (1 << 24) - 256]
+    cap = fp8q.fp8q_grouped_padded_rows(rows, 2)
+    first = R.first_chunks(np.array(raw))
+    assert cap == 128 * first[-1] == (1 << 24) - 128
+    q = [torch.zeros((n, cap), dtype=torch.uint8, device=DEV) for n in (N, K)]
+    s = [torch.ones((cap // 128, n), dtype=torch.float32, device=DEV) for n in (N, K)]
+    want = torch.zeros((2, N, K))
+    one = 0x38  # 1.0
+    for g, n, k, at, scale in ((0, 0, 0, 5, 2.0), (0, 255, 19, 12344, 3.0), (1, 255, 0, 128 * first[1], 5.0),
+                               (1, 127, 7, 128 * (first[2] - 1), 7.0), (1, 255, 19, 128 * first[2] - 130, 11.0)):
+        q[0][n, at], q[1][k, at] = one, one
+        s[0][at // 128, n] = scale
+        want[g, n, k] += scale
+    dy, x = (fp8q.GroupedOperand(a, b, rows) for a, b in zip(q, s))
+    assert torch.equal(fp8q.grouped_wgrad(dy, x, _offsets(raw)).cpu(), want)
+
+
 def test_wgrad_refuses_strided_codes_of_one_channel(fp8q):
     offs = _offsets([0, 200])
     one, other = (fp8q.grouped_quantize_act(_x(200, n, torch.bfloat16, 23), offs) for n in (1, 40))
