@@ -301,3 +301,37 @@ def test_refuses_scalars_elsewhere(fp8q):
     with pytest.raises(ValueError, match="overlap"):
         fp8q.adamw_tensors([p, p], [torch.zeros_like(p)] * 2, [fp8q.adamw_state(p), fp8q.adamw_state(p)])
     assert not p.any()
+
+
+@pytest.mark.parametrize("coded", [False, True])
+def test_more_elements_than_32_bits_count(fp8q, coded):
+    """Behind 2^32 elements the random numbers start again, so what stands there steps like a tensor of its own."""
+    rows, K = 40, 128
+    small, sg = _tensor((rows, K), torch.bfloat16, 31)
+    st = _state(fp8q, small, 8, 32)
+    before, n = (1 << 32) // K, (1 << 32) + rows * K
+    p = torch.zeros((before + rows, K), device=DEV)
+    g = torch.zeros((before + rows, K), dtype=torch.bfloat16, device=DEV)
+    big = fp8q.AdamwState(*(torch.zeros(n, dtype=torch.uint8, device=DEV) for _ in range(2)),
+                          *(torch.zeros(n // 128, device=DEV) for _ in range(2)))
+    p[before:], g[before:] = small, sg
+    for b, t in zip(big, st):
+        b[-t.numel():] = t
+    codes = [None, None]
+    if coded:
+        n16 = (before + rows + 15) // 16 * 16
+        blocks = -(-(before + rows) // 128)
+        codes = [fp8q.weight_codes(small),
+                 fp8q.WeightCodes(torch.zeros((before + rows, K), dtype=torch.uint8, device=DEV),
+                                  torch.zeros((blocks, 1), device=DEV),
+                                  torch.zeros((K, n16), dtype=torch.uint8, device=DEV)[:, : before + rows],
+                                  torch.zeros((1, blocks), device=DEV))]
+    for one in ((small, sg, st, codes[0]), (p, g, big, codes[1])):
+        fp8q.adamw(fp8q.adamw_tensors(*([v] for v in one)), step=3, seed=5, **H)
+    assert torch.equal(p[before:], small) and not p[before - 1000: before].any()
+    for b, t in zip(big, st):
+        assert torch.equal(b[-t.numel():], t) and not b[-t.numel() - 1000: -t.numel()].any()
+    if coded:
+        a, b = codes
+        assert torch.equal(b.q[before:], a.q) and torch.equal(b.s[-1], a.s[0])
+        assert torch.equal(b.qt[:, before:], a.qt) and torch.equal(b.st[:, -1], a.st[:, 0])

@@ -121,6 +121,24 @@ def test_columns_write_nothing_else(fp8q):
     assert (sn[1:4, :cols] != 7.0).all()  # written; a chunk of one row has a zero scale where its value is zero
 
 
+def test_columns_past_32_bits(fp8q):
+    """Inputs and codes of more than 2^31 elements: the last group's last columns, against its rows alone."""
+    rows, cols, at = 70001, 32768, 69003
+    offs, tail = _offsets([0, at, rows]), slice(cols - 130, cols)
+    x = torch.zeros((rows, cols), dtype=torch.bfloat16, device=DEV)
+    x[at:] = _x(rows - at, cols, torch.bfloat16, 24)
+    first = 128 * -(-at // 128)
+    o = fp8q.grouped_quantize_act(x, offs)
+    q, s = fp8q.quantize_act(x[at:], fp8q.FP8Q_TILE_128x1)
+    assert torch.equal(o.q[tail, first: first + rows - at], q[tail]) and not o.q[tail, at - 500: first].any()
+    assert torch.equal(o.s[first // 128:, tail][: s.shape[0]], s[:, tail])
+    q, s = fp8q.quantize_act(x)
+    o = fp8q.grouped_requant_transpose(q, s, offs)
+    q, s = fp8q.requant_transpose(q[at:], s[:, at:].contiguous())
+    assert torch.equal(o.q[tail, first: first + rows - at], q[tail]) and not o.q[tail, at - 500: first].any()
+    assert torch.equal(o.s[first // 128:, tail][: s.shape[0]], s[:, tail])
+
+
 # ------------------------------------------------------------------ the product
 
 def _operand(fp8q, rows, off, width, seed, scale):
