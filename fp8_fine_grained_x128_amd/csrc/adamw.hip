@@ -398,8 +398,10 @@ __global__ __launch_bounds__(512, 4) void adamw_codes_kernel(CodedBatch b) {
         for (int k = 0; k < kAhead; ++k) x[k].load(t, e0 + (k0 + k) * t.K, row + k0 + k < t.N ? 8 : 0);
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            x[k].step(t, s, key, e0 + (k0 + k) * t.K, row + k0 + k < t.N ? 8 : 0, w[k0 + k]);
-            am = max(am, amax8(w[k0 + k]));
+            const bool exists = row + k0 + k < t.N;
+            x[k].step(t, s, key, e0 + (k0 + k) * t.K, exists ? 8 : 0, w[k0 + k]);
+            // (rows past N step on zeros: 0 / 0 where eps is zero)
+            am = max(am, exists ? amax8(w[k0 + k]) : 0u);
         }
     }
     am = row_max_u32(am);

@@ -1,0 +1,39 @@
+"""AdamW with an eps of zero: the rows that a weight's last band of 128x128 blocks lacks have nothing to say."""
+import pytest
+import torch
+
+from tests.test_gpu_adamw import H, _check_codes, _tensor, _Want
+
+pytestmark = pytest.mark.gpu
+
+
+def _no_zeros(fp8q, shape, gdtype, bits):
+    """Gradients that are nowhere zero, so that no second moment is."""
+    p, g = _tensor(shape, gdtype, 41)
+    g[g == 0] = 3e-4
+    return p, g, fp8q.adamw_state(p, bits)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [0.0, 1e-46])
+@pytest.mark.parametrize("shape", [(1, 128), (16, 384), (77, 256), (130, 128), (3, 77, 256), (128, 128)])
+def test_codes_of_weights(fp8q, bits, eps, shape):
+    for gdtype in (torch.float32, torch.bfloat16):
+        for mode in (fp8q.FP8Q_SCALE_FP32, fp8q.FP8Q_SCALE_POW2):
+            p, g, st = _no_zeros(fp8q, shape, gdtype, bits)
+            c = fp8q.weight_codes(p, scale_mode=mode)
+            want = _Want(p, g, st, 1, 5, 0, eps=eps)
+            fp8q.adamw(fp8q.adamw_tensors([p], [g], [st], [c]), step=1, seed=5, scale_mode=mode, **{**H, "eps": eps})
+            want.check(p, st)
+            _check_codes(fp8q, p, c, mode)
+
+
+def test_flat_tensors(fp8q):
+    """Lengths that end inside a work-group, a tile and a lane's eight elements."""
+    for bits in (32, 8):
+        for n in (1, 7, 130, 2049):
+            p, g, st = _no_zeros(fp8q, (n,), torch.float32, bits)
+            want = _Want(p, g, st, 2, 5, 0, eps=0.0)
+            fp8q.adamw(fp8q.adamw_tensors([p], [g], [st]), step=2, seed=5, **{**H, "eps": 0.0})
+            want.check(p, st)
+            assert torch.isfinite(p).all()
