@@ -521,7 +521,7 @@ hipError_t launch_adamw(const fp8q_adamw_tensor* tensors, int count, int g_dtype
     a.s.rest1 = (float)(1.0 - c.beta1);
     a.s.beta2 = (float)c.beta2;
     a.s.rest2 = (float)(1.0 - c.beta2);
-    a.s.eps = (float)c.eps;
+    a.s.eps = c.eps > 0.0 ? fmaxf((float)c.eps, 0x1p-149f) : 0.0f;  // never from positive to zero: 0 / eps is 0
     a.s.grad = 1.0f;
     a.beta1 = c.beta1; a.beta2 = c.beta2; a.lr = c.lr; a.decay = c.weight_decay;
     a.lr_dev = c.lr_dev; a.step_dev = c.step_dev; a.grad_scale = c.grad_scale;

@@ -593,6 +593,8 @@ int fp8q_grouped_wgrad(const uint8_t *a, int64_t lda, const float *sa, int64_t l
  * overlap.  p, g, m, v, q and qt are 16-byte aligned, sm, sv, s and st 4-byte.
  * n == 0 is an empty tensor; n <= 2^33, and at most 2^22 blocks of 128x128 of a
  * tensor with codes (else FP8Q_EUNSUPPORTED).
+ * eps is rounded to fp32, a positive one to 2^-149 at least.  With eps == 0 an
+ * element whose v' is zero gets m' / 0: NaN, or infinite.
  * lr_dev, step_dev, grad_scale: DEVICE scalars read when the step runs (NULL:
  * lr, step, 1), so that a captured step can be replayed with others.
  * A gradient that is NaN or infinite shows in its element, and in its tile's

@@ -1,8 +1,9 @@
-"""AdamW with an eps of zero: the rows that a weight's last band of 128x128 blocks lacks have nothing to say."""
+"""AdamW with an eps of zero, or near it: the rows that a weight's last band of 128x128 blocks lacks have nothing to
+say, and a positive eps stays positive."""
 import pytest
 import torch
 
-from tests.test_gpu_adamw import H, _check_codes, _tensor, _Want
+from tests.test_gpu_adamw import DEV, H, _check_codes, _tensor, _Want
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +38,18 @@ def test_flat_tensors(fp8q):
             fp8q.adamw(fp8q.adamw_tensors([p], [g], [st]), step=2, seed=5, **{**H, "eps": 0.0})
             want.check(p, st)
             assert torch.isfinite(p).all()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [1e-46, 5e-324, 1e-40, 2.0 ** -149])
+def test_small_eps_is_not_zero(fp8q, bits, eps):
+    """No gradient and no moments: 0 / eps is 0 for every positive eps, so only the decay is left."""
+    p = torch.randn((77, 256), device=DEV)
+    before, st = p.clone(), fp8q.adamw_state(p, bits)
+    c = fp8q.weight_codes(p)
+    vec = torch.randn(300, device=DEV)
+    vec_before, vec_st = vec.clone(), fp8q.adamw_state(vec, bits)
+    plan = fp8q.adamw_tensors([p, vec], [torch.zeros_like(p), torch.zeros_like(vec)], [st, vec_st], [c, None])
+    fp8q.adamw(plan, step=1, lr=0.5, weight_decay=0.5, eps=eps)
+    assert torch.equal(p, before * 0.75) and torch.equal(vec, vec_before * 0.75)
+    _check_codes(fp8q, p, c)
