@@ -29,6 +29,29 @@ def test_codes_of_weights(fp8q, bits, eps, shape):
             _check_codes(fp8q, p, c, mode)
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_zero_over_zero_shows_in_its_element_and_its_block(fp8q, bits):
+    """Where eps, m and v are all zero the formula is 0 / 0: NaN in that element and in the scale of its block, as the
+    quantizer has it; every other element is as if it were not there."""
+    p, g, st = _no_zeros(fp8q, (200, 256), torch.float32, bits)
+    other, so = p.clone(), fp8q.adamw_state(p, bits)
+    c, co = fp8q.weight_codes(p), fp8q.weight_codes(other)
+    go = g.clone()
+    g[130, 5] = 0.0
+    for args in ((p, g, st, c), (other, go, so, co)):
+        fp8q.adamw(fp8q.adamw_tensors(*([a] for a in args)), step=1, seed=5, **{**H, "eps": 0.0})
+    at = torch.zeros_like(p, dtype=torch.bool)
+    at[130, 5] = True
+    assert p[at].isnan().all() and torch.equal(p[~at], other[~at])
+    q, s = fp8q.quantize_weight(p)
+    assert c.s.isnan().tolist() == [[False, False], [True, False]] == s.isnan().tolist()
+    assert torch.equal(c.s.nan_to_num(7.0), s.nan_to_num(7.0))
+    assert torch.equal(c.st.t().nan_to_num(7.0), s.nan_to_num(7.0))
+    live = torch.ones_like(p, dtype=torch.bool)
+    live[128:, :128] = False  # the codes of that block multiply a NaN
+    assert torch.equal(c.q[live], q[live]) and torch.equal(c.q[live], co.q[live])
+
+
 def test_flat_tensors(fp8q):
     """Lengths that end inside a work-group, a tile and a lane's eight elements."""
     for bits in (32, 8):
