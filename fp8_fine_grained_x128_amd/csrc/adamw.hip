@@ -11,6 +11,9 @@
 //   - rounded to the neighbour above with a probability of the way to it: a
 //     moving average changes by less than half a step of a 4-bit significand
 //     almost always, and rounded to nearest it would never move;
+//     (What it does not bias is sqrt(v).  v, the square, gets the rounding's
+//     variance: 2.4 % in the mean at beta2 = 0.95, 5.5 % at 0.999, where a
+//     step's change is a small part of the grid's step and so is its variance.)
 //   - sqrt(v) of a positive v rounds to one step of the smallest codes at least:
 //     with a zero there the next step would divide m by eps alone.
 // The step itself takes the moments before they are rounded.

@@ -580,6 +580,11 @@ int fp8q_grouped_wgrad(const uint8_t *a, int64_t lda, const float *sa, int64_t l
  *       i the element's index (low 32 bits), t the tensor's in the list, and
  *         mix(x): x ^= x >> 16; x *= 0x7feb352d; x ^= x >> 15;
  *                 x *= 0x846ca68b; x ^= x >> 16.
+ *       What is unbiased is the rounding of sqrt(v): its square, the v of the
+ *       next step, has the rounding's variance on top.  Of gradients that are
+ *       normally distributed the mean v comes to stand 1.4 % (beta2 0.9), 2.4 %
+ *       (0.95), 4.8 % (0.99), 5.5 % (0.999) above that of fp32 moments, and the
+ *       updates half of that below.
  *       Zeroed codes and scales are the state before the first step.
  * Codes of the new weights (q == NULL: none): p holds n / (N K) matrices
  * [N][K], K a multiple of 128; q[..][N][K] and s[..][ceil(N/128)][K/128] are
