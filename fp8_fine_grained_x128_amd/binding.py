@@ -1023,10 +1023,15 @@ def weight_codes(w: torch.Tensor, transposed: bool = True, scale_mode: int = FP8
 
 
 class AdamwTensors:
-    """What adamw() works on: made by adamw_tensors(), kept from step to step.  It holds the tensors."""
+    """What adamw() works on: made by adamw_tensors(), kept from step to step.  It holds the tensors and the memory that
+    they had then, which adamw() reads and writes, and refuses parameters that have got other memory since."""
 
     def __init__(self, held: tuple, array, g_dtype: int, bits: int, device: torch.device):
         self.held, self.array, self.g_dtype, self.bits, self.device = held, array, g_dtype, bits, device
+        params, grads, states, codes = held
+        self.params, self.addresses, self.places = list(params), [p.data_ptr() for p in params], list(range(len(params)))
+        self.memory = tuple(t.untyped_storage() for ts in (params, grads, *states, *filter(None, codes)) for t in ts
+                            if t is not None)
 
 
 def _dense(t: torch.Tensor, shape: tuple, dtype: torch.dtype) -> bool:
@@ -1042,7 +1047,8 @@ def adamw_tensors(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
                   codes: Optional[Sequence[Optional[WeightCodes]]] = None) -> AdamwTensors:
     """Checks the tensors of an optimizer step once: dense fp32 params, grads of the same shapes (all fp32 or all
     bf16), moments of adamw_state() (all of 32 or all of 8 bits), and for weights the codes of weight_codes() or None.
-    adamw() then updates params, moments and codes in place, from what grads hold at that time."""
+    adamw() then updates params, moments and codes in place, from what grads hold at that time.  A tensor that gets
+    other memory (p.data = ..., a new gradient tensor) needs a new list; none may be resized while the list is used."""
     what = "adamw_tensors"
     codes = [None] * len(params) if codes is None else list(codes)
     if not len(params) == len(grads) == len(states) == len(codes):
@@ -1120,6 +1126,7 @@ def adamw(tensors: AdamwTensors, step: Union[int, torch.Tensor], lr: Union[float
     be tensors of one element on the device, read when the step runs: a captured step is then replayed with other
     values.  grad_scale multiplies the gradients; seed chooses the random numbers that round 8-bit moments.  See
     fp8q_adamw."""
+    _not_moved(tensors.params, tensors.addresses, tensors.places)
     c = fp8q_adamw_config(0.0, beta1, beta2, eps, weight_decay, 0, None, None, None, seed & 0xFFFFFFFF)
     if isinstance(step, torch.Tensor):
         c.step_dev = _device_scalar("step", step, torch.int64, tensors)
@@ -1134,6 +1141,19 @@ def adamw(tensors: AdamwTensors, step: Union[int, torch.Tensor], lr: Union[float
     stream = _stream_for("adamw", tensors.held[0][0])
     _check(_lib.fp8q_adamw(tensors.array, len(tensors.array), tensors.g_dtype, tensors.bits, ctypes.addressof(c),
                            scale_mode, stream), "fp8q_adamw")
+
+
+# Not a documented function of torch: one call for all tensors, 1.8 us for 60 of them, where asking each takes 2.6.
+_same_addresses = getattr(torch._C, "_tensors_data_ptrs_at_indices_equal", None)
+
+
+def _not_moved(params: list, addresses: list, places: list) -> None:
+    """The parameters stand where they stood when their list was made."""
+    if _same_addresses is not None and _same_addresses(params, addresses, places):
+        return
+    for i, (p, a) in enumerate(zip(params, addresses)):
+        if p.data_ptr() != a:
+            raise ValueError(f"adamw: parameter {i} has other memory than when its list was made; make a new list")
 
 
 def _device_scalar(name: str, t: torch.Tensor, dtype: torch.dtype, tensors: AdamwTensors) -> int:
