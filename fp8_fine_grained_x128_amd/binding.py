@@ -21,6 +21,7 @@ import os
 from typing import NamedTuple, Optional, Sequence, Tuple, Union
 
 import torch
+from torch.autograd.graph import increment_version
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfp8q.so")
@@ -1032,6 +1033,9 @@ class AdamwTensors:
         self.params, self.addresses, self.places = list(params), [p.data_ptr() for p in params], list(range(len(params)))
         self.memory = tuple(t.untyped_storage() for ts in (params, grads, *states, *filter(None, codes)) for t in ts
                             if t is not None)
+        # what a backward pass may have kept: parameters that autograd follows, and codes
+        self.versioned = [p for p in params if p.requires_grad] + [t for c in codes if c is not None for t in c
+                                                                   if t is not None]
 
 
 def _dense(t: torch.Tensor, shape: tuple, dtype: torch.dtype) -> bool:
@@ -1125,7 +1129,7 @@ def adamw(tensors: AdamwTensors, step: Union[int, torch.Tensor], lr: Union[float
     """One AdamW step over all the tensors, in place; step counts from 1.  step (int64), lr and grad_scale (fp32) may
     be tensors of one element on the device, read when the step runs: a captured step is then replayed with other
     values.  grad_scale multiplies the gradients; seed chooses the random numbers that round 8-bit moments.  See
-    fp8q_adamw."""
+    fp8q_adamw.  To autograd the parameters and codes are changed in place: a backward pass that kept them is refused."""
     _not_moved(tensors.params, tensors.addresses, tensors.places)
     c = fp8q_adamw_config(0.0, beta1, beta2, eps, weight_decay, 0, None, None, None, seed & 0xFFFFFFFF)
     if isinstance(step, torch.Tensor):
@@ -1141,6 +1145,8 @@ def adamw(tensors: AdamwTensors, step: Union[int, torch.Tensor], lr: Union[float
     stream = _stream_for("adamw", tensors.held[0][0])
     _check(_lib.fp8q_adamw(tensors.array, len(tensors.array), tensors.g_dtype, tensors.bits, ctypes.addressof(c),
                            scale_mode, stream), "fp8q_adamw")
+    if tensors.versioned:
+        increment_version(tensors.versioned)
 
 
 # Not a documented function of torch: one call for all tensors, 1.8 us for 60 of them, where asking each takes 2.6.

@@ -43,3 +43,40 @@ def test_memory_given_up_is_not_written(fp8q):
     torch.cuda.synchronize()
     assert all((o == 5.0).all() for o in others)
     assert ((p + 1e-2).abs() <= 1e-7).all()
+
+
+def test_backward_through_changed_weights_is_refused(fp8q):
+    """As after any change in place: a graph that kept a parameter, or its codes, does not go on with other values."""
+    w = torch.nn.Parameter(torch.randn((16, 128), device=DEV))
+    c, st = fp8q.weight_codes(w.detach()), fp8q.adamw_state(w)
+    plan = fp8q.adamw_tensors([w], [torch.ones((16, 128), device=DEV)], [st], [c])
+
+    class ByCodes(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x):
+            ctx.save_for_backward(c.q, c.st)
+            return x * 2
+
+        @staticmethod
+        def backward(ctx, dy):
+            return dy * ctx.saved_tensors[0].float().mean()
+
+    x = torch.randn((4, 128), device=DEV, requires_grad=True)
+    for graph in (lambda: (x @ w.t()).sum(), lambda: ByCodes.apply(x).sum()):
+        graph().backward()
+        loss = graph()
+        fp8q.adamw(plan, step=1, **H)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+        graph().backward()
+
+
+def test_inference_tensors(fp8q):
+    """They have no version counter; the step takes them."""
+    with torch.inference_mode():
+        p = torch.ones((2, 128), device=DEV)
+        st, c = fp8q.adamw_state(p), fp8q.weight_codes(p)
+        plan = fp8q.adamw_tensors([p], [torch.ones_like(p)], [st], [c])
+        fp8q.adamw(plan, step=1, lr=0.5, weight_decay=0.5)
+    assert (p < 0.5).all()
+    fp8q.adamw(plan, step=2, lr=0.5)
