@@ -463,7 +463,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grouped_wgrad_kernel(WgradPar
             stage ^= 1;
         }
         const int ln = lane_now();
-        __builtin_amdgcn_s_barrier();  // every wave is done with the stage just read
+        lds_barrier();  // every wave is done with the stage just read
         uint8_t* region = lds + (stage ^ 1) * Cfg::kStageBytes + wave * kRegion;
         if (inside) {
             if (job.partial) store_rows<Cfg, kDtypeF32, false>(acc, rc, row_bytes, wm, wn, ln, region);
