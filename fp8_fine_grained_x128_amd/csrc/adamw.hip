@@ -20,7 +20,7 @@
 //
 // Both kernels are bound by memory: every byte moves once (per element fp32 28,
 // with 8-bit moments and bf16 gradients 14; the codes add one byte each).  16
-// experts of 2048x7168 with 8-bit moments and both codes, 4.26 GB: 855 us, 5.0
+// experts of 2048x7168 with 8-bit moments and both codes, 4.26 GB: 854 us, 5.0
 // TB/s, where a large copy reaches 4.7; 29 million weights with fp32 moments
 // and both codes, 881 MB: 193 us, 4.6 TB/s.  With 8-bit moments the rounding's
 // instructions come close to the time of the bytes: the shorter forms that a
@@ -36,7 +36,9 @@ namespace fp8q {
 namespace {
 
 // Two rounds of xor-shift and multiplication: 32 bits that each depend on all
-// of x's.  The same function on the host (keys) and on the device.
+// of x's.  Shifts and factors are those of a published 32-bit integer hash,
+// searched for there so that every input bit flips every output bit half the
+// time.  The same function on the host (keys) and on the device.
 __host__ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
     x ^= x >> 16;
     x *= 0x7feb352du;
@@ -45,7 +47,10 @@ __host__ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
     return x ^ (x >> 16);
 }
 
-// b^t by squaring: t < 2^63, at most 2 x 63 roundings of 2^-53.
+// b^t by squaring.  Every squaring doubles the relative error of b's power, so
+// the result is within about t 2^-53.  What counts is 1 - b^t, whose relative
+// error is t b^t / (1 - b^t) 2^-53, at most 2^-53 / (1 - b): 2^-26 up to b =
+// 1 - 2^-27.
 __host__ __device__ inline double power(double b, int64_t t) {
     double r = 1.0;
     for (; t > 0; t >>= 1) {
@@ -107,8 +112,10 @@ __device__ __forceinline__ float round_normal_up_by(float y, uint32_t r20) {
 }
 
 // Square root rounded to nearest of v in [2^-90, 2^90]: the reciprocal root
-// (within an ulp), one step for the root and for half its reciprocal, and the
-// root's remainder.  11 issue slots; sqrtf, which takes any v, has 19.
+// (within an ulp), one step of Goldschmidt's iteration for the root and half its
+// reciprocal, and the root's remainder (all 2^24 significands of two binades,
+// at both ends of the range too, give sqrtf's root).  11 issue slots; sqrtf,
+// which takes any v, has 19.
 __device__ __forceinline__ float sqrt_in_range(float v) {
     const float y = __builtin_amdgcn_rsqf(v);
     float s = v * y, h = 0.5f * y;
@@ -146,7 +153,11 @@ struct CodedTensor : FlatTensor {
     uint32_t units;
 };
 
-// Scale of a tile of moments: fl32(amax * fl32(1 / 448)).
+// Scale of a tile of moments: fl32(amax * fl32(1 / 448)), a product where
+// make_scale divides: every lane forms two of them per eight elements.  That is
+// one rounding more; the scale is the header's definition of what is held, and
+// what it multiplies is rounded to four bits.  (The largest quotient may then
+// be an ulp above 448, and is held at 448.)
 __device__ __forceinline__ TileScale moment_scale(uint32_t amax_bits) {
     TileScale t;
     t.s = __uint_as_float(amax_bits) * (1.0f / kE4M3Max);
