@@ -1,6 +1,7 @@
 // adamw.hip -- one AdamW step over many tensors, with the FP8 codes of the new
-// weights.  For every element, in fp32, every product and sum of the moments
-// rounded (so that their codes can be reproduced bit for bit):
+// weights.  For every element, in fp32, every product and sum of 8-bit moments
+// rounded (so that their codes can be reproduced bit for bit), the sums of fp32
+// moments fused:
 //   m' = beta1 m + (1 - beta1) g,  v' = beta2 v + (1 - beta2) g^2,
 //   p' = p (1 - lr decay) - lr / (1 - beta1^t) * m' / (sqrt(v' / (1 - beta2^t)) + eps)
 // Moments of 32 bits are m and v.  Moments of 8 bits are E4M3 codes of m and of
@@ -81,7 +82,7 @@ struct StepArgs {
 __host__ __device__ inline void set_time(Step& s, double beta1, double beta2, double lr, double decay, int64_t t) {
     s.keep = (float)(1.0 - lr * decay);
     s.rate = (float)(lr / (1.0 - power(beta1, t)));
-    s.root = 1.0f / (float)sqrt(1.0 - power(beta2, t));
+    s.root = (float)(1.0 / sqrt(1.0 - power(beta2, t)));
     s.time = (uint32_t)t;
 }
 
@@ -260,8 +261,13 @@ struct Eight {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float x = gr[i] * s.grad;
-            m[i] = m[i] * s.beta1 + x * s.rest1;
-            v[i] = v[i] * s.beta2 + x * x * s.rest2;
+            if constexpr (BITS == 32) {  // one rounding less than 8-bit moments are defined with
+                m[i] = __builtin_fmaf(x, s.rest1, m[i] * s.beta1);
+                v[i] = __builtin_fmaf(x * x, s.rest2, v[i] * s.beta2);
+            } else {
+                m[i] = m[i] * s.beta1 + x * s.rest1;
+                v[i] = v[i] * s.beta2 + x * x * s.rest2;
+            }
         }
         // Where every second moment of the wave is far from the ends of the
         // range root and quotient take fewer instructions.  They are those of

@@ -47,3 +47,20 @@ def test_the_quotient_is_rounded_to_nearest(fp8q):
     assert np.array_equal(m, g * f(0.5)) and np.array_equal(v, g * g * f(0.25))
     d = np.sqrt(v) * f(2.0) + f(1e-8)  # sqrt(1 - 3/4) = 1/2
     assert np.array_equal(p.cpu().numpy(), -(m / d))
+
+
+def test_sums_of_fp32_moments_round_once(fp8q):
+    """m' = fl32(fl32(beta1 m) + (1 - beta1) x) and v' = fl32(fl32(beta2 v) + (1 - beta2) fl32(x^2)): with 5/8 and 3/8 the
+    factors are exact, and the sums are exact in 64 bits (numbers within 2^+-10)."""
+    n = 1 << 16
+    rng = np.random.default_rng(53)
+    g, m, v = (np.exp(rng.uniform(-3, 3, n)).astype(np.float32) for _ in range(3))
+    g[::2] *= -1
+    p = torch.zeros(n, device=DEV)
+    st = fp8q.adamw_state(p)
+    st.m.copy_(_f32(m))
+    st.v.copy_(_f32(v))
+    fp8q.adamw(fp8q.adamw_tensors([p], [_f32(g)], [st]), step=3, lr=0.5, beta1=0.625, beta2=0.625)
+    f, d = np.float32, np.float64
+    assert np.array_equal(st.m.cpu().numpy(), ((m * f(0.625)).astype(d) + 0.375 * g.astype(d)).astype(f))
+    assert np.array_equal(st.v.cpu().numpy(), ((v * f(0.625)).astype(d) + 0.375 * (g * g).astype(d)).astype(f))
