@@ -11,7 +11,7 @@
 // work-group walks many tiles as one stream of chunks: under the last chunk of
 // a tile the first one of the next is copied, and a tile's stores go on under
 // the next one's first chunk.  64 experts of 2048x7168 over 32768 rows, fp32:
-// 1255 to 1315 us, by box.  The products alone take 853 (equal groups) to 970
+// 1255 to 1330 us, by card.  The products alone take 853 (equal groups) to 970
 // (Zipf), the 3.8 GB of stores alone, in these pieces, 670 (5.6 TB/s).  What
 // does not overlap is the time for which a tile's 256 KB queue at the memory: copies that
 // are issued behind them arrive late, whichever wave issues them, and there is
@@ -20,7 +20,7 @@
 // 128x128 tiles, two work-groups a compute unit: 1021 without the stores, 1323
 // with, the same 300 more; stores between the last chunk's products:
 // 1347 : 1199.)  Few large experts are bound by the products (4 of 4096x7168,
-// 16384 rows, added: 920, of which the products alone are 740 to 796).
+// 16384 rows, added: 890 to 957, of which the products alone are 740 to 796).
 #include <cmath>
 #include <type_traits>
 
